@@ -1,0 +1,508 @@
+"""The 8-bit activation operators on the GPU against their definition in 64
+bits (tests/w8a8_reference.py): per-token quantization, the linear product,
+the gated block and their input gradients.
+
+Codes, scales and sums are bit-exact; products and gradients lie within the
+roundings that their definitions name (see the bounds of w8a8_reference).
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import w8a8_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lw():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import weight_only_bit_rtn_amd as lw
+    lw.load_library()
+    return lw
+
+
+def say(*a):
+    print("[w8a8]", *a, flush=True)
+
+
+def types():
+    import torch
+    return {"fp16": torch.float16, "bf16": torch.bfloat16}
+
+
+def gpu(a, kind=None):
+    """A numpy array on the GPU; with ``kind``, float values rounded to that type."""
+    import torch
+    t = torch.from_numpy(np.ascontiguousarray(a)).to("cuda:0")
+    return t if kind is None else t.to(types()[kind])
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def weights(rng, N, K, grid):
+    """codes uint8 [N][K], scales fp16 [N], zeros int32 [N]: what the quantizers produce."""
+    if grid == "sym":
+        codes = rng.integers(1, 256, (N, K))
+        zeros = np.full(N, 128)
+    else:
+        codes = rng.integers(0, 256, (N, K))
+        zeros = rng.integers(0, 256, N)
+        if grid == "far":      # one-signed rows: zero points far outside the codes, some at the fp16 extremes
+            zeros = np.where(np.arange(N) % 3 == 0, zeros, rng.integers(-522240, 522241, N))
+    # far zero points with small scales, as such rows have them: (code - zero) * scale stays below one
+    scales = (rng.uniform(0.5, 2, N) * (1e-6 if grid == "far" else 2e-4)).astype(np.float16)
+    return codes.astype(np.uint8), scales, zeros.astype(np.int32)
+
+
+def on_gpu(w):
+    codes, scales, zeros = w
+    N = codes.shape[0]
+    packed = codes.view(np.int32) if N else np.empty((0, codes.shape[1] // 4), np.int32)
+    return gpu(packed), gpu(scales.reshape(N, 1)), gpu(zeros.reshape(N, 1))
+
+
+def check(got, want, bound, what):
+    got = f64(got)
+    assert got.shape == want.shape, what
+    bad = ~(np.abs(got - want) <= bound)
+    if bad.any():
+        at = np.argwhere(bad)[:4]
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.size} outside; " + ", ".join(
+            f"{tuple(i)}: {got[tuple(i)]!r} want {want[tuple(i)]!r} +- {bound[tuple(i)]:.3g}" for i in at))
+
+
+def activations(rng, T, K, kind):
+    x = rng.standard_normal((T, K)) * np.exp(rng.uniform(-6, 3, (T, 1)))
+    x[:, rng.integers(0, K, max(1, K // 100))] *= 10
+    return gpu(x.astype(np.float32), kind)
+
+
+# ---------------------------------------------------------------------------
+# quantize_act
+# ---------------------------------------------------------------------------
+def check_codes(lw, x, what):
+    want = ref.quantize_act(x.float().cpu().numpy())
+    q = lw.quantize_act(x)
+    for name, w in zip(("codes", "scales", "sums"), want):
+        got = q[name].cpu().numpy()
+        assert got.shape == w.shape and got.dtype == w.dtype, (what, name)
+        if name == "scales":
+            assert np.array_equal(got.view(np.uint32)[np.isfinite(w)], w.view(np.uint32)[np.isfinite(w)]), what
+            assert np.array_equal(np.isnan(got), np.isnan(w)), what
+        else:
+            assert np.array_equal(got, w), f"{what}: {name} differ at {np.argwhere(got != w)[:5].tolist()}"
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("K", [32, 64, 96, 512, 544, 1024, 1056, 4096, 11008, 16384, 16416, 32768, 32800, 131072])
+def test_quantize_act(lw, K, kind):
+    say("quantize", K, kind)
+    rng = np.random.default_rng(K)
+    for T in (1, 3, 70):
+        if T * K <= 1 << 22:
+            check_codes(lw, activations(rng, T, K, kind), f"{T}x{K} {kind}")
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+def test_quantize_act_edges(lw, kind):
+    import torch
+    K = 256
+    rng = np.random.default_rng(1)
+    x = rng.standard_normal((16, K)).astype(np.float32)
+    x[0] = 0
+    x[1] = -3
+    x[2] = 0
+    x[2, 77] = 6e-8 if kind == "fp16" else 1e-40            # one subnormal
+    x[3] *= 1e-7 if kind == "fp16" else 1e-39
+    x[4] *= 1e4 if kind == "fp16" else 1e38
+    x[5, 9] = np.inf
+    x[6, 255] = -np.inf
+    x[7, 0] = np.nan
+    x[8] = np.arange(K) - 127                                # maximum 127 + 1: all kinds of halves
+    x[9] = (np.arange(K) - 128) / 2
+    x[10, :] = np.where(np.arange(K) % 2, 127, np.arange(K) / 2 - 60)  # scale 1: exact ties
+    x[11] = -x[10]
+    x[12, :] = 65504 if kind == "fp16" else 3.3e38
+    say("quantize edges", kind)
+    check_codes(lw, gpu(x, kind), kind)
+    # every finite positive value of the type as an element under several maxima
+    bits = torch.arange(0, 0x7c00 if kind == "fp16" else 0x7f80, dtype=torch.int32).to(torch.int16)
+    v = bits.view(types()[kind])
+    n = v.numel() // 32 * 32
+    for top in (1.0, 127.0, 381.0, 0.0999, 3.17e-3):
+        row = torch.where(v[:n].float() <= top, v[:n].float(), torch.tensor(top)).to(types()[kind])
+        check_codes(lw, row.reshape(1, n).cuda(), f"{kind} all values to {top}")
+
+
+# ---------------------------------------------------------------------------
+# linear
+# ---------------------------------------------------------------------------
+SHAPES = [(1, 1, 32), (1, 256, 256), (1, 515, 1056), (2, 3, 64), (3, 64, 96), (5, 33, 4128), (8, 130, 512),
+          (15, 100, 160), (16, 16, 128), (17, 127, 288), (31, 272, 2048), (33, 65, 1024), (63, 257, 192),
+          (64, 128, 256), (65, 129, 224), (100, 1000, 512), (127, 63, 128), (129, 300, 416), (200, 64, 4096),
+          (257, 130, 160), (300, 515, 352), (513, 257, 288), (600, 1030, 96), (1025, 511, 640)]
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_linear(lw, shape, kind):
+    T, N, K = shape
+    for grid in ("sym", "minmax", "far"):
+        say("linear", shape, kind, grid)
+        rng = np.random.default_rng([T, N, K])
+        w = weights(rng, N, K, grid)
+        x = activations(rng, T, K, kind)
+        a, s, _ = ref.quantize_act(x.float().cpu().numpy())
+        want = ref.product(a, s, *w)
+        y = lw.linear_w8a8(x, *on_gpu(w))
+        assert y.dtype == x.dtype
+        check(y, want, ref.linear_bound(want, kind), f"linear {shape} {kind} {grid}")
+        # codes handed over: the same bits
+        q = lw.quantize_act(x)
+        y2 = lw.linear_w8a8(q, *on_gpu(w), out_dtype=x.dtype)
+        assert bool((y2 == y).all()), f"codes and values differ at {shape}"
+
+
+@pytest.mark.parametrize("T", [1, 3, 20, 70, 600])
+def test_linear_longest_rows(lw, T):
+    """K at its limit with the largest codes: the integer sums come near 2^31."""
+    K, N = lw.W8A8_MAX_K, 5
+    say("longest rows", T)
+    codes = np.empty((N, K), np.uint8)
+    codes[0] = 0
+    codes[1] = 255
+    codes[2:] = np.random.default_rng(0).integers(0, 256, (N - 2, K))
+    w = codes, np.full(N, 1e-6, np.float16), np.array([128, 128, 0, 255, -522240], np.int32)
+    x = np.ones((T, K), np.float32)
+    x[T // 2:] *= -1
+    x = gpu(x, "bf16")
+    a, s, _ = ref.quantize_act(x.float().cpu().numpy())
+    want = ref.product(a, s, *w)
+    check(lw.linear_w8a8(x, *on_gpu(w)), want, ref.linear_bound(want, "bf16"), f"T={T}")
+
+
+@pytest.mark.parametrize("T", [1, 9, 40, 100, 520])
+def test_linear_rows_apart(lw, T):
+    """Zero tokens give zeros, tokens with an infinity or a NaN give NaN, and neither touches other tokens."""
+    N, K = 70, 320
+    rng = np.random.default_rng(T)
+    w = weights(rng, N, K, "minmax")
+    x = activations(rng, T, K, "fp16")
+    clean = lw.linear_w8a8(x, *on_gpu(w))
+    bad = x.clone()
+    bad[0, 3] = float("inf")
+    if T > 4:
+        bad[T // 2, K - 1] = float("nan")
+        bad[T - 1] = 0
+    say("rows apart", T)
+    y = lw.linear_w8a8(bad, *on_gpu(w))
+    assert bool(y[0].isnan().all())
+    if T > 4:
+        assert bool(y[T // 2].isnan().all()) and bool((y[T - 1] == 0).all())
+        keep = [t for t in range(1, T - 1) if t != T // 2]
+        assert bool((y[keep] == clean[keep]).all())
+
+
+def test_linear_of_the_quantizers_codes(lw):
+    """quantize_rtn's packed words, scales and zeros go in as they come."""
+    rng = np.random.default_rng(3)
+    N, K, T = 300, 544, 70
+    for sym in (False, True):
+        wf = (rng.standard_normal((N, K)) * 0.02).astype(np.float16)
+        wf[5] = 0.25          # constant rows
+        wf[6] = 0
+        q = lw.quantize_rtn(gpu(wf), 8, 0, symmetric=sym)
+        x = activations(rng, T, K, "fp16")
+        a, s, _ = ref.quantize_act(x.float().cpu().numpy())
+        want = ref.product(a, s, q["codes"].cpu().numpy(), q["scales"].cpu().numpy()[:, 0],
+                           q["zeros"].cpu().numpy()[:, 0])
+        y = lw.linear_w8a8(x, q["packed"], q["scales"], q["zeros"])
+        check(y, want, ref.linear_bound(want, "fp16"), f"sym={sym}")
+
+
+# ---------------------------------------------------------------------------
+# gated
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_gated(lw, shape, kind):
+    T, N, K = shape
+    for grid, act in (("sym", "silu"), ("minmax", "gelu_tanh"), ("far", "silu")):
+        say("gated", shape, kind, grid, act)
+        rng = np.random.default_rng([T, N, K, 1])
+        wg, wu = weights(rng, N, K, grid), weights(rng, N, K, grid)
+        x = activations(rng, T, K, kind)
+        a, s, _ = ref.quantize_act(x.float().cpu().numpy())
+        g, u = ref.product(a, s, *wg), ref.product(a, s, *wu)
+        want = ref.act_value(g, act) * u
+        top = 65504.0 if kind == "fp16" else 3.3e38
+        h, hg, hu = lw.gated_w8a8(x, *on_gpu(wg), *on_gpu(wu), act=act, save=True)
+        fits = np.abs(want) < top
+        got = np.where(fits, f64(h), 0)
+        bound = ref.gated_bound(want, g, kind, act)
+        assert (np.abs(got - np.where(fits, want, 0)) <= bound).all(), f"h {shape} {kind} {grid} {act}"
+        check(hg, g, ref.linear_bound(g, kind), "gate")
+        check(hu, u, ref.linear_bound(u, kind), "up")
+        alone = lw.gated_w8a8(x, *on_gpu(wg), *on_gpu(wu), act=act)
+        assert bool(((alone == h) | (alone.isnan() & h.isnan())).all())
+
+
+# ---------------------------------------------------------------------------
+# gradients
+# ---------------------------------------------------------------------------
+def norm_of(d):
+    return float(np.sqrt((d * d).sum()))
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_linear_grad(lw, shape, kind):
+    T, N, K = shape
+    for grid in ("sym", "minmax", "far"):
+        say("linear grad", shape, kind, grid)
+        rng = np.random.default_rng([T, N, K, 2])
+        w = weights(rng, N, K, grid)
+        size = np.exp(rng.uniform(-4, 2, (T, 1)))
+        dy = gpu((rng.standard_normal((T, N)) * size * 0.05).astype(np.float32), kind)
+        want = ref.linear_grad(f64(dy), *w)
+        dx = lw.linear_w8a8_grad(dy, *on_gpu(w))
+        assert dx.dtype == dy.dtype
+        check(dx, want, ref.grad_bound(want, [(f64(dy), *w)], kind), f"{shape} {kind} {grid}")
+        if grid == "sym" and N >= 64:
+            # independent roundings: half a step is their largest, not their common size
+            assert norm_of(f64(dx) - want) <= norm_of(want) * (2.0 ** -11 + ref.HALF_STEP[kind])
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_gated_grad(lw, shape, kind):
+    T, N, K = shape
+    for grid, act in (("sym", "gelu_tanh"), ("minmax", "silu")):
+        say("gated grad", shape, kind, grid, act)
+        rng = np.random.default_rng([T, N, K, 3])
+        wg, wu = weights(rng, N, K, grid), weights(rng, N, K, grid)
+        dh = gpu((rng.standard_normal((T, N)) * 0.05).astype(np.float32), kind)
+        gate = gpu((rng.standard_normal((T, N)) * 2).astype(np.float32), kind)
+        up = gpu(rng.standard_normal((T, N)).astype(np.float32), kind)
+        dg, du = ref.gated_parts(f64(dh), f64(gate), f64(up), act)
+        want = ref.linear_grad(dg, *wg) + ref.linear_grad(du, *wu)
+        dx, pg, pu = lw.gated_w8a8_grad(dh, gate, up, *on_gpu(wg), *on_gpu(wu), act=act, parts=True)
+        # sigma as in gated_bound; the slope is a difference of terms, each with such an error
+        g = f64(gate)
+        q = np.abs(ref.two_q(g, act))
+        r = (24 + 24 * q) * ref.U32
+        s = 1 / (1 + np.exp(-ref.two_q(g, act)))
+        rise = np.abs(ref.act_slope(g, act) - s)
+        slope_err = (s + rise) * r
+        ag, au = np.abs(f64(dh) * f64(up)) * slope_err, np.abs(du) * r
+        check(pg, dg, np.abs(dg) * ref.HALF_STEP[kind] * 1.01 + 2 * ag + ref.HALF_TINY[kind], "dgate")
+        check(pu, du, np.abs(du) * ref.HALF_STEP[kind] * 1.01 + 2 * au + ref.HALF_TINY[kind], "dup")
+        bound = ref.grad_bound(want, [(dg, *wg), (du, *wu)], kind)
+        for e, w in ((ag, wg), (au, wu)):
+            size = np.abs(w[0].astype(np.float64) - 128) + np.abs(128.0 - w[2].reshape(-1, 1))
+            bound += (2 * e * w[1].astype(np.float64)) @ size
+        check(dx, want, bound, f"{shape} {kind} {grid} {act}")
+        if grid == "sym" and N >= 64:
+            assert norm_of(f64(dx) - want) <= norm_of(want) * (2.0 ** -11 + ref.HALF_STEP[kind])
+        alone = lw.gated_w8a8_grad(dh, gate, up, *on_gpu(wg), *on_gpu(wu), act=act)
+        assert bool((alone == dx).all())
+
+
+@pytest.mark.parametrize("T", [1, 40, 100, 520])
+def test_grad_of_any_size(lw, T):
+    """Gradients far below and above the fp16 operands' range, zero tokens, and tokens with infinities or NaN."""
+    N, K = 130, 160
+    rng = np.random.default_rng(T)
+    w = weights(rng, N, K, "sym")
+    for scale in (1e-30, 1e-12, 1.0, 1e25):
+        say("grad size", T, scale)
+        dy = gpu((rng.standard_normal((T, N)) * scale).astype(np.float32), "bf16")
+        want = ref.linear_grad(f64(dy), *w)
+        dx = lw.linear_w8a8_grad(dy, *on_gpu(w))
+        check(dx, want, ref.grad_bound(want, [(f64(dy), *w)], "bf16"), f"{scale}")
+        bad = dy.clone()
+        bad[0, N - 1] = float("nan") if scale == 1.0 else float("inf")
+        if T > 2:
+            bad[T - 1] = 0
+        got = lw.linear_w8a8_grad(bad, *on_gpu(w))
+        assert bool(got[0].isnan().all())
+        if T > 2:
+            assert bool((got[T - 1] == 0).all()) and bool((got[1:T - 1] == dx[1:T - 1]).all())
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_gated_far_gates(lw, act):
+    """Gates where sigma is at its limits: no infinities or NaN from intermediate steps."""
+    N, K, T = 96, 64, 5
+    rng = np.random.default_rng(8)
+    wg, wu = weights(rng, N, K, "sym"), weights(rng, N, K, "sym")
+    g = np.concatenate([[0, 1e-30, -1e-30, 5, -5, 12, -12, 20, -20, 88, -88, 90, -90, 110, -110, 3e4, -3e4, 1e15, -1e15,
+                         1e30, -1e30], rng.standard_normal(N - 21)])
+    gate = gpu(np.tile(g, (T, 1)).astype(np.float32), "bf16")
+    up = gpu(rng.standard_normal((T, N)).astype(np.float32), "bf16")
+    dh = gpu(np.where(np.abs(g) > 1e3, 1e-28, 0.05).astype(np.float32) * rng.standard_normal((T, N)).astype(np.float32),
+             "bf16")
+    say("far gates", act)
+    dx, pg, pu = lw.gated_w8a8_grad(dh, gate, up, *on_gpu(wg), *on_gpu(wu), act=act, parts=True)
+    with np.errstate(over="ignore", invalid="ignore"):
+        dg, du = ref.gated_parts(f64(dh), np.clip(f64(gate), -600, 600), f64(up), act)
+        du = f64(dh) * ref.act_value(np.where(f64(gate) < -600, -600, f64(gate)), act)
+    # below e^-88 sigma is zero in 32 bits
+    tol = 2e-36
+    assert bool(dx.isfinite().all()) and bool(pg.isfinite().all()) and bool(pu.isfinite().all())
+    near = ref.HALF_STEP["bf16"] + 3e-5
+    assert (np.abs(f64(pg) - dg) <= near * np.abs(dg) + 3e-6 * np.abs(f64(dh) * f64(up)) + tol).all()
+    assert (np.abs(f64(pu) - du) <= near * np.abs(du) + tol).all()
+
+
+# ---------------------------------------------------------------------------
+# as they are used
+# ---------------------------------------------------------------------------
+def block(rng, N, K):
+    """The three matrices of a gated feed-forward block."""
+    return [weights(rng, *s, "minmax") for s in ((N, K), (N, K), (K, N))]
+
+
+def run_block(lw, x, w):
+    h, g, u = lw.gated_w8a8(x, *w[0], *w[1], save=True)
+    y = lw.linear_w8a8(h, *w[2])
+    dh = lw.linear_w8a8_grad(y, *w[2])
+    return h, y, dh, lw.gated_w8a8_grad(dh, g, u, *w[0], *w[1])
+
+
+@pytest.mark.parametrize("T", [1, 12, 50, 100, 600])
+def test_block_repeats_on_streams_and_in_graphs(lw, T):
+    """A feed-forward block forward and backward: the same bits again, on a side stream, with two calls at once,
+    and from a captured graph replayed between eager work of its own."""
+    import torch
+    say("block", T)
+    rng = np.random.default_rng(T)
+    w = [on_gpu(m) for m in block(rng, 352, 160)]
+    x = activations(rng, T, 160, "bf16")
+    x2 = activations(rng, T, 160, "bf16")
+    want, want2 = run_block(lw, x, w), run_block(lw, x2, w)
+    torch.cuda.synchronize()
+    assert all(bool(t.isfinite().all()) for t in want)
+
+    def same(a, b):
+        return all(bool((p == q).all()) for p, q in zip(a, b))
+
+    assert same(run_block(lw, x, w), want)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (s1, s2):
+        s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s1):
+        a = run_block(lw, x, w)
+    with torch.cuda.stream(s2):
+        b = run_block(lw, x2, w)
+    torch.cuda.synchronize()
+    assert same(a, want) and same(b, want2)
+
+    held = x.clone()
+    with torch.cuda.stream(s1):
+        run_block(lw, held, w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run_block(lw, held, w)
+    for i in range(4):
+        src, expect = (x, want) if i % 2 == 0 else (x2, want2)
+        held.copy_(src)
+        graph.replay()
+        other = run_block(lw, x2 if i % 2 == 0 else x, w)      # eager work between the replays
+        torch.cuda.synchronize()
+        assert same(out, expect), f"replay {i}"
+        assert same(other, want2 if i % 2 == 0 else want)
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 33, 64), (20, 65, 96), (70, 130, 160), (520, 259, 288)])
+def test_nothing_written_past_the_end(lw, T, N, K):
+    """Raw calls with every output and workspace of exactly its size inside guarded memory."""
+    import torch
+    say("guards", T, N, K)
+    rng = np.random.default_rng(N)
+    wg, wu = (on_gpu(weights(rng, N, K, "minmax")) for _ in range(2))
+    x = activations(rng, T, K, "fp16")
+    guards = []
+
+    def room(nbytes):
+        t = torch.full((nbytes + 1024,), 0xA5, dtype=torch.uint8, device="cuda")
+        guards.append((t, nbytes))
+        return t[512:].data_ptr()
+
+    def p(w):
+        return tuple(t.data_ptr() for t in w)
+
+    st = torch.cuda.current_stream().cuda_stream
+    assert lw.quantize_act_raw(x.data_ptr(), 0, T, K, room(T * K), room(T * 4), room(T * 4), st) == 0
+    need = lw.linear_w8a8_workspace_bytes(T, N, K, 0)
+    y = room(2 * T * N)
+    assert lw.linear_w8a8_raw(x.data_ptr(), 0, None, None, T, *p(wg), N, K, y, 0, room(need), need, st) == 0
+    need = lw.gated_w8a8_workspace_bytes(T, N, K, 0)
+    h, g, u = (room(2 * T * N) for _ in range(3))
+    assert lw.gated_w8a8_raw(x.data_ptr(), 0, None, None, T, *p(wg), *p(wu), N, K, 0, h, g, u, 0, room(need), need,
+                             st) == 0
+    need = lw.linear_w8a8_grad_workspace_bytes(T, N, K)
+    assert lw.linear_w8a8_grad_raw(y, 0, T, *p(wg), N, K, room(2 * T * K), room(need), need, st) == 0
+    need = lw.gated_w8a8_grad_workspace_bytes(T, N, K)
+    assert lw.gated_w8a8_grad_raw(h, g, u, 0, T, *p(wg), *p(wu), N, K, 1, room(2 * T * K), room(2 * T * N),
+                                  room(2 * T * N), room(need), need, st) == 0
+    torch.cuda.synchronize()
+    for t, n in guards:
+        assert bool((t[:512] == 0xA5).all()) and bool((t[512 + n:] == 0xA5).all())
+
+
+def test_empty_problems(lw):
+    import torch
+    rng = np.random.default_rng(0)
+    w = on_gpu(weights(rng, 8, 64, "sym"))
+    none = on_gpu(weights(rng, 0, 64, "sym"))
+    x = activations(rng, 3, 64, "fp16")
+    assert lw.linear_w8a8(x[:0], *w).shape == (0, 8)
+    assert lw.linear_w8a8(x, *none).shape == (3, 0)
+    assert lw.gated_w8a8(x[:0], *w, *w).shape == (0, 8)
+    assert lw.gated_w8a8(x, *none, *none).shape == (3, 0)
+    assert lw.quantize_act(x[:0])["codes"].shape == (0, 64)
+    dy = torch.zeros(0, 8, dtype=torch.float16, device="cuda")
+    assert lw.linear_w8a8_grad(dy, *w).shape == (0, 64)
+    dy = torch.zeros(3, 0, dtype=torch.float16, device="cuda")
+    out = torch.full((3, 64), 7, dtype=torch.float16, device="cuda")
+    assert bool((lw.linear_w8a8_grad(dy, *none, out=out) == 0).all())
+    assert bool((lw.gated_w8a8_grad(dy, dy, dy, *none, *none) == 0).all())
+
+
+def test_refusals(lw):
+    import torch
+    rng = np.random.default_rng(0)
+    w = on_gpu(weights(rng, 8, 64, "sym"))
+    x = activations(rng, 3, 64, "fp16")
+    dy = torch.zeros(3, 8, dtype=torch.float16, device="cuda")
+    other = on_gpu(weights(rng, 9, 64, "sym"))
+    for call, error in [
+            (lambda: lw.linear_w8a8(x.float(), *w), TypeError),
+            (lambda: lw.linear_w8a8(x.cpu(), *w), ValueError),
+            (lambda: lw.linear_w8a8(x.t(), *w), ValueError),
+            (lambda: lw.linear_w8a8(x[0], *w), ValueError),
+            (lambda: lw.linear_w8a8(x[:, :32].contiguous(), *w), ValueError),
+            (lambda: lw.linear_w8a8(x, w[0], w[1].float(), w[2]), TypeError),
+            (lambda: lw.linear_w8a8(x, w[0], w[1][:4], w[2]), ValueError),
+            (lambda: lw.linear_w8a8(x, w[0], w[1], w[2].cpu()), ValueError),
+            (lambda: lw.linear_w8a8(x, *w, out_dtype=torch.float32), TypeError),
+            (lambda: lw.linear_w8a8(x, *w, out=torch.empty(3, 9, dtype=torch.float16, device="cuda")), ValueError),
+            (lambda: lw.gated_w8a8(x, *w, *other), ValueError),
+            (lambda: lw.gated_w8a8(x, *w, *w, act="relu"), ValueError),
+            (lambda: lw.linear_w8a8_grad(dy[:, :7].contiguous(), *w), ValueError),
+            (lambda: lw.gated_w8a8_grad(dy, dy.bfloat16(), dy, *w, *w), TypeError),
+            (lambda: lw.gated_w8a8_grad(dy, dy, dy[:2], *w, *w), ValueError),
+            (lambda: lw.quantize_act(x.double()), TypeError),
+            (lambda: lw.quantize_act(torch.zeros(2, 40, dtype=torch.float16, device="cuda")), lw.LowbitError),
+            (lambda: lw.quantize_act(torch.zeros(1, lw.W8A8_MAX_K + 32, dtype=torch.float16, device="cuda")),
+             lw.LowbitError)]:
+        with pytest.raises(error):
+            call()

@@ -358,3 +358,11 @@ def quantize_gptq(w, x_calib, bits: int, group_size: int, damp: float = 0.01,
     _check(st, name)
     out["status"] = workspace[off:off + 4].view(torch.int32)
     return out
+
+
+# products in 8-bit integers (include/lowbit_w8a8.h)
+from .w8a8 import (  # noqa: E402,F401
+    EXPORTED_W8A8, W8A8_MAX_K, W8A8_MAX_TN, gated_w8a8, gated_w8a8_grad, gated_w8a8_grad_raw,
+    gated_w8a8_grad_workspace_bytes, gated_w8a8_raw, gated_w8a8_workspace_bytes, linear_w8a8,
+    linear_w8a8_grad, linear_w8a8_grad_raw, linear_w8a8_grad_workspace_bytes, linear_w8a8_raw,
+    linear_w8a8_workspace_bytes, quantize_act, quantize_act_raw)

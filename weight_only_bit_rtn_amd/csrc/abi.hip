@@ -304,9 +304,10 @@ const char* lowbit_status_string(int status) {
       return "invalid argument (null or misaligned pointer, negative size, batch out of range)";
     case LOWBIT_ERR_SHAPE:
       return "unsupported shape (K must be a positive multiple of 32 with K*bits a multiple of "
-             "128; group_size 0 or a multiple of 32 dividing K)";
+             "128; group_size 0 or a multiple of 32 dividing K; sizes within the entry point's "
+             "limits)";
     case LOWBIT_ERR_UNSUPPORTED:
-      return "unsupported bit width (2, 3, 4 or 8)";
+      return "unsupported bit width (2, 3, 4 or 8), element type or activation";
     case LOWBIT_ERR_HIP:
       return "HIP runtime error while launching";
     case LOWBIT_ERR_SCRATCH:

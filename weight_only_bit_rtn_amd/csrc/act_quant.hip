@@ -1,0 +1,111 @@
+// act_quant.hip -- per-token int8 quantization of activations.
+//
+// Per token t: amax = max_k |x|, S = fl32(amax / 127) (1 when that is zero),
+// a = clamp(rint(fl32(x / S)), -127, 127), and the sum of the codes.  One
+// workgroup per token holds its row in registers between the maximum and the
+// codes, so x is read once: 2 bytes read and 1 written for each value, bound
+// by HBM.
+//
+// The quotient is not divided out: with r = fl32(1 / S), x * r differs from
+// x / S by less than 2^-15 for |x / S| < 128, so rint of the two can differ
+// only when x * r lies within that of a half; there (and where r or the
+// product overflows) the division is done.
+#include "w8a8.h"
+
+namespace lowbit {
+namespace {
+
+// Code of one value.
+__device__ __forceinline__ int act_code(float x, float s, float r) {
+  const float q = x * r;
+  float n = rintf(q);
+  if (!(fabsf(q - n) <= 0.4999f)) n = rintf(x / s);
+  return (int)fminf(fmaxf(n, -127.0f), 127.0f);
+}
+
+// NC chunks of 8 values per thread, blockDim.x threads; chunk c of the row
+// belongs to thread c mod blockDim.x.
+template <int NC>
+__global__ __launch_bounds__(1024) void quantize_act_kernel(const uint16_t* __restrict__ x,
+                                                            int bf16, int K,
+                                                            int8_t* __restrict__ codes,
+                                                            float* __restrict__ scales,
+                                                            int32_t* __restrict__ sums) {
+  __shared__ int red[2][16];
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 63, wave = tid >> 6;
+  const int waves = nt >> 6, chunks = K / 8;
+  const int64_t row = blockIdx.x;
+  const us8_t* xr = reinterpret_cast<const us8_t*>(x + row * K);
+  us8_t v[NC];
+  int top = 0;  // largest |x| as bits: the order of the absolute values
+#pragma unroll
+  for (int i = 0; i < NC; i++) {
+    const int c = tid + i * nt;
+    v[i] = us8_t{};
+    if (c < chunks) v[i] = xr[c];
+  }
+#pragma unroll
+  for (int i = 0; i < NC; i++)
+#pragma unroll
+    for (int j = 0; j < 8; j++) top = max(top, (int)(v[i][j] & 0x7fff));
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) top = max(top, __shfl_xor(top, off, kWave));
+  if (lane == 0) red[0][wave] = top;
+  __syncthreads();
+  for (int w = 0; w < waves; w++) top = max(top, red[0][w]);
+  const bool finite = top < (bf16 ? 0x7f80 : 0x7c00);
+  const float amax = elem_to_f32((uint16_t)top, bf16);
+  float s = amax / 127.0f;
+  if (s == 0.0f) s = 1.0f;
+  const float r = 1.0f / s;
+  int sum = 0;
+  uint2* cr = reinterpret_cast<uint2*>(codes + row * K);
+#pragma unroll
+  for (int i = 0; i < NC; i++) {
+    const int c = tid + i * nt;
+    if (c >= chunks) continue;
+    uint32_t w[2] = {0, 0};
+    if (finite) {
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const int a = act_code(elem_to_f32(v[i][j], bf16), s, r);
+        sum += a;
+        w[j / 4] |= (uint32_t)(a & 255) << (8 * (j % 4));
+      }
+    }
+    cr[c] = make_uint2(w[0], w[1]);
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, kWave);
+  if (lane == 0) red[1][wave] = sum;
+  __syncthreads();
+  if (tid == 0) {
+    sum = 0;
+    for (int w = 0; w < waves; w++) sum += red[1][w];
+    scales[row] = finite ? s : __builtin_nanf("");
+    sums[row] = sum;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_quantize_act(const void* x, int dtype, int64_t T, int64_t K, int8_t* codes,
+                               float* scales, int32_t* sums, hipStream_t stream) {
+  const int chunks = (int)(K / 8);
+  // the fewest waves that leave a thread at most two chunks, up to 1024 threads
+  int nt = 64;
+  while (nt < 1024 && chunks > 2 * nt) nt *= 2;
+  const int nc = (chunks + nt - 1) / nt;
+  const auto* xp = static_cast<const uint16_t*>(x);
+  const dim3 grid((unsigned)T), block(nt);
+  const int bf = dtype == kBF16, k = (int)K;
+  if (nc <= 2)
+    quantize_act_kernel<2><<<grid, block, 0, stream>>>(xp, bf, k, codes, scales, sums);
+  else if (nc <= 4)
+    quantize_act_kernel<4><<<grid, block, 0, stream>>>(xp, bf, k, codes, scales, sums);
+  else
+    quantize_act_kernel<16><<<grid, block, 0, stream>>>(xp, bf, k, codes, scales, sums);
+  return hipGetLastError();
+}
+
+}  // namespace lowbit

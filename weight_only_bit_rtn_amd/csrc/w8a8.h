@@ -1,0 +1,113 @@
+// w8a8.h -- what the 8-bit activation kernels share: element types, the
+// activations of the gated block, LDS-direct tile loads, and the launchers
+// behind the C ABI (not exported).
+#pragma once
+
+#include "common.h"
+
+namespace lowbit {
+
+enum ElemType { kF16 = 0, kBF16 = 1, kI8 = 2 };
+enum ActKind { kSilu = 0, kGeluTanh = 1 };
+
+typedef int i4_t __attribute__((ext_vector_type(4)));
+typedef int i2_t __attribute__((ext_vector_type(2)));
+typedef uint16_t us4_t __attribute__((ext_vector_type(4)));
+typedef uint16_t us8_t __attribute__((ext_vector_type(8)));
+
+// One weight matrix as the quantizers leave it (8 bits, one group per row).
+struct W8 {
+  const uint8_t* codes;  // [N][K] code bytes
+  const uint16_t* scales;
+  const int32_t* zeros;
+};
+
+__device__ __forceinline__ float elem_to_f32(uint16_t bits, bool bf16) {
+  return bf16 ? __builtin_bit_cast(float, (uint32_t)bits << 16) : h_bits_to_f32(bits);
+}
+// Round to nearest even, once, to the output type.
+__device__ __forceinline__ uint16_t f32_to_elem(float v, bool bf16) {
+  return bf16 ? __builtin_bit_cast(uint16_t, (__bf16)v) : f32_to_h_bits(v);
+}
+
+// sigma = 1 / (1 + e^-2q) with 2q = v (SiLU) or 2p (GELU, tanh form): both
+// activations are v * sigma.  e^-2q overflows to infinity for very negative
+// arguments and sigma is then 0, the limit.  GELU's cube is taken of v within
+// [-16, 16]: beyond, sigma is 0 or 1 in fp32 already and its slope 0.
+__device__ __forceinline__ float act_sigma(float v, int act) {
+  float e;
+  if (act == kSilu) {
+    e = v;
+  } else {
+    const float c = fminf(fmaxf(v, -16.0f), 16.0f);
+    e = 1.5957691216057308f * (c + 0.044715f * c * c * c);
+  }
+  return __builtin_amdgcn_rcpf(1.0f + __expf(-e));
+}
+__device__ __forceinline__ float act_value(float v, int act) { return v * act_sigma(v, act); }
+// The activation's value and slope: sigma + v sigma (1 - sigma) (2q)'.
+__device__ __forceinline__ void act_value_slope(float v, int act, float& f, float& df) {
+  const float s = act_sigma(v, act);
+  f = v * s;
+  float w = v;  // v (2q)'
+  if (act != kSilu) {
+    const float c = fminf(fmaxf(v, -16.0f), 16.0f);
+    w = 1.5957691216057308f * c * (1.0f + 0.134145f * c * c);
+  }
+  df = s + s * (1.0f - s) * w;
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes,
+                                           0x00020000);
+}
+
+// 16 bytes per lane from a range-checked buffer straight into LDS: lane l's
+// land at lds + 16 l (lds is wave-uniform); an offset outside the buffer
+// brings zeros.
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, void* lds, uint32_t offset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      rs, (__attribute__((address_space(3))) void*)lds, 16, (int)offset, 0, 0, 0);
+}
+
+// Workgroup id -> tile: ids go round the 8 chiplets one by one, so give each
+// chiplet (its own L2) a contiguous run of tiles, and walk the runs in bands
+// of 8 token tiles by all weight tiles, so that the tiles in flight on one
+// chiplet share few rows of both operands.
+__device__ __forceinline__ void tile_of(int id, int total, int tiles_m, int tiles_n, int& tm,
+                                        int& tn) {
+  const int q = total / 8, r = total % 8, xcd = id % 8, at = id / 8;
+  const int t = xcd * q + min(xcd, r) + at;
+  constexpr int kBand = 8;
+  const int band = t / (kBand * tiles_n), in = t % (kBand * tiles_n);
+  const int rows = min(kBand, tiles_m - band * kBand);
+  tm = band * kBand + in % rows;
+  tn = in / rows;
+}
+
+hipError_t launch_quantize_act(const void* x, int dtype, int64_t T, int64_t K, int8_t* codes,
+                               float* scales, int32_t* sums, hipStream_t stream);
+
+// The activations of a product: codes with their scales and sums, or fp16 /
+// bf16 values that the launcher quantizes (into the workspace).
+struct Activations {
+  const void* x;
+  int dtype;
+  const float* scales;
+  const int32_t* sums;
+};
+
+size_t w8a8_workspace_bytes(int64_t T, int64_t N, int64_t K, int dtype, bool gated);
+hipError_t launch_linear_w8a8(const Activations& x, int64_t T, const W8& w, int64_t N, int64_t K,
+                              void* y, int out_dtype, void* workspace, hipStream_t stream);
+hipError_t launch_gated_w8a8(const Activations& x, int64_t T, const W8& gate, const W8& up,
+                             int64_t N, int64_t K, int act, void* h, void* g, void* u,
+                             int out_dtype, void* workspace, hipStream_t stream);
+
+size_t w8a8_grad_workspace_bytes(int64_t T, int64_t N, int64_t K, bool gated);
+hipError_t launch_w8a8_grad(const void* dh, const void* gate, const void* up, int dtype, int64_t T,
+                            const W8& wg, const W8& wu, bool gated, int64_t N, int64_t K, int act,
+                            void* dx, void* dgate, void* dup, void* workspace,
+                            hipStream_t stream);
+
+}  // namespace lowbit

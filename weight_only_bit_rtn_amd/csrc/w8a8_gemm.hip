@@ -1,0 +1,264 @@
+// w8a8_gemm.hip -- products in 8-bit integers on the matrix cores
+// (v_mfma_i32_16x16x64_i8 of gfx950): the linear layer and the gated block.
+//
+//   y[t][n] = S_t s_n (sum_k a[t][k] c'[n][k] + (128 - z_n) A_t)
+//
+// a are a token's codes, S its scale, A the sum of its codes; c' = code - 128
+// is the code byte with its top bit flipped, a signed byte; the zero point
+// enters once for each output.  Both grids of the weight quantizers are
+// covered and every integer sum is exact.
+#include "w8a8.h"
+
+namespace lowbit {
+namespace {
+
+constexpr int kStep = 128;  // bytes (values) of k per pipeline step
+
+struct GemmArgs {
+  const int8_t* a;
+  const float* xs;
+  const int32_t* xsum;
+  W8 w[2];
+  void* y;
+  void* g;
+  void* u;
+  int T, N, K, act, bf16, tiles_m, tiles_n;
+};
+
+// Integer sum of one output to fp32.  For K <= 65536 and a zero point in
+// [0, 255], |A| < 2^23 and the sum of a (code - z) fits 32 bits; otherwise it
+// is formed in fp64, where it is exact too (below 2^43).
+__device__ __forceinline__ float exact_sum(int acc, int zc, int total, bool small) {
+  if (small) return (float)(acc + __mul24(zc, total));
+  return (float)((double)acc + (double)zc * (double)total);
+}
+
+// One workgroup of WM x WN waves computes MT tokens by NT weight rows (gated:
+// NT / 2 rows of each matrix, the wave's first half gate, its second half up,
+// so a lane holds both projections of an output).  Steps of 128 k are staged
+// in LDS by direct loads, two buffers: step i + 1 is on its way while step i
+// is multiplied, one barrier per step.  A row of a step is 8 chunks of 16
+// bytes; chunk c of row r lies at c ^ (r & 7), so the 16 rows of one operand
+// read spread over all banks.  Values past the row's end, tokens past T and
+// rows past N come as zeros from the buffers' range check.
+template <int MT, int NT, int WM, int WN, bool GATED>
+__global__ __launch_bounds__(WM* WN * 64) void w8a8_kernel(const GemmArgs p) {
+  constexpr int kWaves = WM * WN;
+  constexpr int MW = MT / WM, NW = NT / WN;  // wave tile
+  constexpr int FM = MW / 16, FN = NW / 16;  // its fragments
+  constexpr int NO = GATED ? NT / 2 : NT;    // output columns of a tile
+  constexpr int LA = MT / 8 / kWaves, LB = NT / 8 / kWaves;  // 1 KiB loads per wave and step
+  static_assert(LA * 8 * kWaves == MT && LB * 8 * kWaves == NT, "whole loads");
+  static_assert(!GATED || (FN % 2 == 0 && LB % 2 == 0), "gate and up halves");
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  constexpr int kBuf = (MT + NT) * kStep;
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % WM, wn = wave / WM;
+  const int i16 = lane & 15, h = lane >> 4;
+  int tm, tn;
+  tile_of(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, tm, tn);
+  const int t0 = tm * MT, n0 = tn * NO;
+  const uint32_t K = (uint32_t)p.K;
+
+  const auto ra = buffer_of(p.a + (int64_t)t0 * K, (uint32_t)min(MT, p.T - t0) * K);
+  const uint32_t wbytes = (uint32_t)min(NO, p.N - n0) * K;
+  const auto rg = buffer_of(p.w[0].codes + (int64_t)n0 * K, wbytes);
+  const auto ru = GATED ? buffer_of(p.w[1].codes + (int64_t)n0 * K, wbytes) : rg;
+
+  // a load covers 8 rows of 128 bytes: lane l brings chunk (l & 7) ^ (l >> 3) of row l >> 3
+  const uint32_t r8 = lane >> 3, chunk = ((lane & 7) ^ r8) * 16;
+  uint32_t oa[LA], ob[LB];
+  int la[LA], lb[LB];
+#pragma unroll
+  for (int i = 0; i < LA; i++) {
+    const int row = (wave + i * kWaves) * 8;
+    oa[i] = (row + r8) * K + chunk;
+    la[i] = row * kStep;
+  }
+#pragma unroll
+  for (int i = 0; i < LB; i++) {
+    // gated: the first half of the loads is the gate matrix
+    const int b = wave + (GATED ? i % (LB / 2) : i) * kWaves;
+    const int row = b * 8;
+    ob[i] = (row + r8) * K + chunk;
+    const int slot = GATED ? row / (NW / 2) * NW + row % (NW / 2) + (i >= LB / 2 ? NW / 2 : 0) : row;
+    lb[i] = (MT + slot) * kStep;
+  }
+  auto stage = [&](uint8_t* buf, uint32_t k0) {
+    const uint32_t add = k0 + chunk < K ? k0 : 0x80000000u;
+#pragma unroll
+    for (int i = 0; i < LA; i++) load_to_lds(ra, buf + la[i], oa[i] + add);
+#pragma unroll
+    for (int i = 0; i < LB; i++)
+      load_to_lds(GATED && i >= LB / 2 ? ru : rg, buf + lb[i], ob[i] + add);
+  };
+
+  i4_t acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; i++)
+#pragma unroll
+    for (int j = 0; j < FM; j++) acc[i][j] = i4_t{0, 0, 0, 0};
+
+  const int steps = (p.K + kStep - 1) / kStep;
+  stage(lds, 0);
+  for (int s = 0; s < steps; s++) {
+    uint8_t* buf = lds + (s & 1) * kBuf;
+    __builtin_amdgcn_s_waitcnt(0xf70);  // vmcnt(0): this step's loads of this wave have landed
+    __syncthreads();                    // and everyone's; the other buffer is free
+    if (s + 1 < steps) stage(lds + ((s + 1) & 1) * kBuf, (uint32_t)(s + 1) * kStep);
+    const uint8_t* ba = buf + (wm * MW + i16) * kStep;
+    const uint8_t* bb = buf + (MT + wn * NW + i16) * kStep;
+#pragma unroll
+    for (int ks = 0; ks < 2; ks++) {
+      const int at = ((ks * 4 + h) ^ (i16 & 7)) * 16;
+      i4_t fa[FM], fb[FN];
+#pragma unroll
+      for (int i = 0; i < FN; i++) {
+        fb[i] = *reinterpret_cast<const i4_t*>(bb + i * 16 * kStep + at);
+        fb[i] ^= (int)0x80808080;
+      }
+#pragma unroll
+      for (int j = 0; j < FM; j++) fa[j] = *reinterpret_cast<const i4_t*>(ba + j * 16 * kStep + at);
+#pragma unroll
+      for (int i = 0; i < FN; i++)
+#pragma unroll
+        for (int j = 0; j < FM; j++)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[i], fa[j], acc[i][j], 0, 0, 0);
+    }
+  }
+
+  // lane l of a fragment holds outputs n = 4 (l / 16) + 0..3 of token l % 16
+  const bool bf = p.bf16;
+  const bool vec = p.N % 4 == 0;
+  constexpr int FO = GATED ? FN / 2 : FN;
+  const int nb = n0 + wn * (GATED ? NW / 2 : NW);
+#pragma unroll
+  for (int i = 0; i < FO; i++) {
+    const int n = nb + i * 16 + h * 4;
+    if (n >= p.N) continue;
+    float sc[2][4];
+    int zc[2][4];
+    bool small = p.K <= 65536;
+#pragma unroll
+    for (int m = 0; m < (GATED ? 2 : 1); m++)
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        const int nn = min(n + r, p.N - 1);
+        sc[m][r] = h_bits_to_f32(p.w[m].scales[nn]);
+        const int z = p.w[m].zeros[nn];
+        zc[m][r] = 128 - z;
+        small = small && (uint32_t)z < 256u;
+      }
+#pragma unroll
+    for (int j = 0; j < FM; j++) {
+      const int t = t0 + wm * MW + j * 16 + i16;
+      if (t >= p.T) continue;
+      const float xs = p.xs[t];
+      const int total = p.xsum[t];
+      us4_t out, og, ou;
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        const float v = exact_sum(acc[i][j][r], zc[0][r], total, small) * (xs * sc[0][r]);
+        if constexpr (GATED) {
+          const float u =
+              exact_sum(acc[i + FO][j][r], zc[1][r], total, small) * (xs * sc[1][r]);
+          out[r] = f32_to_elem(act_value(v, p.act) * u, bf);
+          og[r] = f32_to_elem(v, bf);
+          ou[r] = f32_to_elem(u, bf);
+        } else {
+          out[r] = f32_to_elem(v, bf);
+        }
+      }
+      const int64_t at = (int64_t)t * p.N + n;
+      auto put = [&](void* base, us4_t v) {
+        uint16_t* q = static_cast<uint16_t*>(base) + at;
+        if (vec) {
+          *reinterpret_cast<us4_t*>(q) = v;
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; r++)
+            if (n + r < p.N) q[r] = v[r];
+        }
+      };
+      put(p.y, out);
+      if (GATED && p.g) {
+        put(p.g, og);
+        put(p.u, ou);
+      }
+    }
+  }
+}
+
+template <int MT, int NT, int WM, int WN, bool GATED>
+hipError_t launch_tile(GemmArgs p, hipStream_t stream) {
+  constexpr int NO = GATED ? NT / 2 : NT;
+  constexpr int bytes = 2 * (MT + NT) * kStep;
+  auto kernel = w8a8_kernel<MT, NT, WM, WN, GATED>;
+  hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), bytes);
+  if (e != hipSuccess) return e;
+  p.tiles_m = (p.T + MT - 1) / MT;
+  p.tiles_n = (p.N + NO - 1) / NO;
+  const int64_t total = (int64_t)p.tiles_m * p.tiles_n;
+  if (total > INT32_MAX) return hipErrorInvalidValue;
+  kernel<<<dim3((unsigned)total), dim3(WM * WN * 64), bytes, stream>>>(p);
+  return hipGetLastError();
+}
+
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+template <bool GATED>
+hipError_t launch(const Activations& x, int64_t T, const W8& w0, const W8& w1, int64_t N,
+                  int64_t K, int act, void* y, void* g, void* u, int out_dtype, void* workspace,
+                  hipStream_t stream) {
+  GemmArgs p{};
+  if (x.dtype == kI8) {
+    p.a = static_cast<const int8_t*>(x.x);
+    p.xs = x.scales;
+    p.xsum = x.sums;
+  } else {
+    auto* ws = static_cast<uint8_t*>(workspace);
+    auto* codes = reinterpret_cast<int8_t*>(ws);
+    auto* xs = reinterpret_cast<float*>(ws + up256(T * K));
+    auto* sums = reinterpret_cast<int32_t*>(ws + up256(T * K) + up256(T * 4));
+    hipError_t e = launch_quantize_act(x.x, x.dtype, T, K, codes, xs, sums, stream);
+    if (e != hipSuccess) return e;
+    p.a = codes;
+    p.xs = xs;
+    p.xsum = sums;
+  }
+  p.w[0] = w0;
+  p.w[1] = w1;
+  p.y = y;
+  p.g = g;
+  p.u = u;
+  p.T = (int)T;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.act = act;
+  p.bf16 = out_dtype == kBF16;
+  if (T <= 64) return launch_tile<64, 64, 2, 2, GATED>(p, stream);
+  if (T <= 512) return launch_tile<128, 128, 2, 2, GATED>(p, stream);
+  return launch_tile<256, 256, 2, 4, GATED>(p, stream);
+}
+
+}  // namespace
+
+size_t w8a8_workspace_bytes(int64_t T, int64_t N, int64_t K, int dtype, bool gated) {
+  if (dtype == kI8 || T == 0) return 0;
+  return up256(T * K) + 2 * up256(T * 4);
+}
+
+hipError_t launch_linear_w8a8(const Activations& x, int64_t T, const W8& w, int64_t N, int64_t K,
+                              void* y, int out_dtype, void* workspace, hipStream_t stream) {
+  return launch<false>(x, T, w, w, N, K, 0, y, nullptr, nullptr, out_dtype, workspace, stream);
+}
+
+hipError_t launch_gated_w8a8(const Activations& x, int64_t T, const W8& gate, const W8& up,
+                             int64_t N, int64_t K, int act, void* h, void* g, void* u,
+                             int out_dtype, void* workspace, hipStream_t stream) {
+  return launch<true>(x, T, gate, up, N, K, act, h, g, u, out_dtype, workspace, stream);
+}
+
+}  // namespace lowbit

@@ -1,0 +1,327 @@
+"""Products in 8-bit integers: 8-bit weights, activations quantized per token.
+
+Binding of ``include/lowbit_w8a8.h``; argument marshalling only, as in the
+package's other functions.  Weights are the 8-bit per-row codes of
+``quantize_rtn(w, 8, 0)`` (either grid) or ``quantize_gptq(w, x, 8, 0)``:
+
+  quantize_act(x) -> dict                            codes, scales, sums of each token
+  linear_w8a8(x, packed, scales, zeros) -> y         x fp16 / bf16, or a quantize_act dict
+  gated_w8a8(x, gate's three, up's three, act) -> h  act(x G^T) * (x U^T), one kernel
+  linear_w8a8_grad(dy, packed, scales, zeros) -> dx
+  gated_w8a8_grad(dh, gate, up, gate's three, up's three, act) -> dx
+
+The gradients are with respect to x; the weights are constants, and the
+rounding of the activations is passed through unchanged.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+from . import (_check, _ptr, _require_gpu_tensor, _stream_handle, _torch,
+               load_library as _load_library)
+
+W8A8_MAX_K = 131072
+W8A8_MAX_TN = 1 << 20
+F16, BF16, I8 = 0, 1, 2
+ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
+
+EXPORTED_W8A8 = ("lowbit_quantize_act", "lowbit_linear_w8a8_workspace_bytes", "lowbit_linear_w8a8",
+                 "lowbit_gated_w8a8_workspace_bytes", "lowbit_gated_w8a8",
+                 "lowbit_linear_w8a8_grad_workspace_bytes", "lowbit_linear_w8a8_grad",
+                 "lowbit_gated_w8a8_grad_workspace_bytes", "lowbit_gated_w8a8_grad")
+
+_declared = None
+
+
+def _lib() -> ctypes.CDLL:
+    global _declared
+    lib = _load_library()
+    if _declared is lib:
+        return lib
+    vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    lib.lowbit_quantize_act.argtypes = [vp, i32, i64, i64, vp, vp, vp, vp]
+    lib.lowbit_linear_w8a8_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    lib.lowbit_linear_w8a8.argtypes = [vp, i32, vp, vp, i64, vp, vp, vp, i64, i64, vp, i32, vp,
+                                       i64, vp]
+    lib.lowbit_gated_w8a8_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    lib.lowbit_gated_w8a8.argtypes = [vp, i32, vp, vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i32,
+                                      vp, vp, vp, i32, vp, i64, vp]
+    lib.lowbit_linear_w8a8_grad_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.lowbit_linear_w8a8_grad.argtypes = [vp, i32, i64, vp, vp, vp, i64, i64, vp, vp, i64, vp]
+    lib.lowbit_gated_w8a8_grad_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.lowbit_gated_w8a8_grad.argtypes = [vp, vp, vp, i32, i64, vp, vp, vp, vp, vp, vp, i64, i64,
+                                           i32, vp, vp, vp, vp, i64, vp]
+    for name in EXPORTED_W8A8:
+        getattr(lib, name).restype = i64 if name.endswith("_bytes") else i32
+    _declared = lib
+    return lib
+
+
+# ---------------------------------------------------------------------------
+# raw entry points (device pointers as ints; the caller owns every buffer)
+# ---------------------------------------------------------------------------
+def quantize_act_raw(x, dtype, T, K, codes, scales, sums, stream) -> int:
+    return _lib().lowbit_quantize_act(x, dtype, T, K, codes, scales, sums, stream)
+
+
+def linear_w8a8_workspace_bytes(T: int, N: int, K: int, dtype: int) -> int:
+    return _lib().lowbit_linear_w8a8_workspace_bytes(T, N, K, dtype)
+
+
+def linear_w8a8_raw(x, dtype, x_scales, x_sums, T, packed, scales, zeros, N, K, y, out_dtype,
+                    workspace, workspace_bytes, stream) -> int:
+    return _lib().lowbit_linear_w8a8(x, dtype, x_scales, x_sums, T, packed, scales, zeros, N, K, y,
+                                     out_dtype, workspace, workspace_bytes, stream)
+
+
+def gated_w8a8_workspace_bytes(T: int, N: int, K: int, dtype: int) -> int:
+    return _lib().lowbit_gated_w8a8_workspace_bytes(T, N, K, dtype)
+
+
+def gated_w8a8_raw(x, dtype, x_scales, x_sums, T, packed_gate, scales_gate, zeros_gate, packed_up,
+                   scales_up, zeros_up, N, K, act, h, gate, up, out_dtype, workspace,
+                   workspace_bytes, stream) -> int:
+    return _lib().lowbit_gated_w8a8(x, dtype, x_scales, x_sums, T, packed_gate, scales_gate,
+                                    zeros_gate, packed_up, scales_up, zeros_up, N, K, act, h, gate,
+                                    up, out_dtype, workspace, workspace_bytes, stream)
+
+
+def linear_w8a8_grad_workspace_bytes(T: int, N: int, K: int) -> int:
+    return _lib().lowbit_linear_w8a8_grad_workspace_bytes(T, N, K)
+
+
+def linear_w8a8_grad_raw(dy, dtype, T, packed, scales, zeros, N, K, dx, workspace,
+                         workspace_bytes, stream) -> int:
+    return _lib().lowbit_linear_w8a8_grad(dy, dtype, T, packed, scales, zeros, N, K, dx, workspace,
+                                          workspace_bytes, stream)
+
+
+def gated_w8a8_grad_workspace_bytes(T: int, N: int, K: int) -> int:
+    return _lib().lowbit_gated_w8a8_grad_workspace_bytes(T, N, K)
+
+
+def gated_w8a8_grad_raw(dh, gate, up, dtype, T, packed_gate, scales_gate, zeros_gate, packed_up,
+                        scales_up, zeros_up, N, K, act, dx, dgate, dup, workspace,
+                        workspace_bytes, stream) -> int:
+    return _lib().lowbit_gated_w8a8_grad(dh, gate, up, dtype, T, packed_gate, scales_gate,
+                                         zeros_gate, packed_up, scales_up, zeros_up, N, K, act, dx,
+                                         dgate, dup, workspace, workspace_bytes, stream)
+
+
+# ---------------------------------------------------------------------------
+# tensor front end
+# ---------------------------------------------------------------------------
+def _float_type(t, name: str) -> int:
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+    return F16 if t.dtype == torch.float16 else BF16
+
+
+def _matrix(t, name: str, dtype, device=None, shape=None) -> None:
+    """``t`` is a dense GPU matrix of this type (and place and shape)."""
+    _require_gpu_tensor(t, name, dtype)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must live on {device}, got {t.device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _weights(packed, scales, zeros, device, N=None, K=None):
+    """N, K of one 8-bit per-row weight matrix, checked."""
+    torch = _torch()
+    _matrix(packed, "packed", torch.int32, device)
+    n, k = packed.shape[0], 4 * packed.shape[1]
+    if N is not None and (n, k) != (N, K):
+        raise ValueError(f"the two weight matrices must have one shape, got {[N, K]} and {[n, k]}")
+    _matrix(scales, "scales", torch.float16, device, (n, 1))
+    _matrix(zeros, "zeros", torch.int32, device, (n, 1))
+    return n, k
+
+
+def _activations(x, out_dtype):
+    """(pointer, type, scales, sums, T, K, device, output type) of a tensor or a quantize_act dict."""
+    torch = _torch()
+    if isinstance(x, dict):
+        codes, scales, sums = x["codes"], x["scales"], x["sums"]
+        _matrix(codes, "codes", torch.int8)
+        T, K = codes.shape
+        for t, name, dtype in ((scales, "scales of x", torch.float32),
+                               (sums, "sums of x", torch.int32)):
+            _require_gpu_tensor(t, name, dtype)
+            if tuple(t.shape) != (T,) or t.device != codes.device:
+                raise ValueError(f"{name} must be [{T}] on {codes.device}")
+        if out_dtype is None:
+            out_dtype = torch.float16
+        ptrs = (codes.data_ptr(), I8, scales.data_ptr(), sums.data_ptr())
+        dev = codes.device
+    else:
+        kind = _float_type(x, "x")
+        _matrix(x, "x", x.dtype)
+        T, K = x.shape
+        if out_dtype is None:
+            out_dtype = x.dtype
+        ptrs = (x.data_ptr(), kind, None, None)
+        dev = x.device
+    if out_dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"out_dtype must be torch.float16 or torch.bfloat16, got {out_dtype}")
+    return ptrs, T, K, dev, out_dtype
+
+
+def _on(device):
+    """Launches go to the current device: make it the tensors' one."""
+    torch = _torch()
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _workspace(need: int, what: str, device):
+    """(tensor or None, address): scratch of at least ``need`` bytes, 256-byte aligned."""
+    if need < 0:
+        _check(need, what)
+    if need == 0:
+        return None, None
+    # torch's caching allocator hands out blocks aligned to 512 bytes
+    t = _torch().empty(need, dtype=_torch().uint8, device=device)
+    return t, t.data_ptr()
+
+
+def _out(out, name, shape, dtype, device):
+    if out is None:
+        return _torch().empty(shape, dtype=dtype, device=device)
+    _matrix(out, name, dtype, device, shape)
+    return out
+
+
+def _act(act) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def quantize_act(x, out: dict | None = None) -> dict:
+    """Per-token int8 quantization of fp16 or bf16 ``x[T][K]``: a dict with
+    ``codes`` (int8 [T][K]), ``scales`` (fp32 [T]) and ``sums`` (int32 [T], the
+    sum of a token's codes), which the products take in place of x."""
+    torch = _torch()
+    kind = _float_type(x, "x")
+    _matrix(x, "x", x.dtype)
+    T, K = x.shape
+    dev = x.device
+    out = dict(out or {})
+    for name, shape, dtype in (("codes", (T, K), torch.int8), ("scales", (T,), torch.float32),
+                               ("sums", (T,), torch.int32)):
+        if name not in out:
+            out[name] = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            _require_gpu_tensor(out[name], name, dtype)
+            if tuple(out[name].shape) != shape or out[name].device != dev:
+                raise ValueError(f"{name} must be {list(shape)} on {dev}")
+    with _on(dev):
+        _check(quantize_act_raw(x.data_ptr(), kind, T, K, out["codes"].data_ptr(),
+                                out["scales"].data_ptr(), out["sums"].data_ptr(),
+                                _stream_handle(dev)), "lowbit_quantize_act")
+    return out
+
+
+def linear_w8a8(x, packed, scales, zeros, out_dtype=None, out=None):
+    """y[T][N] = x * deq(packed)^T in 8-bit integers.  ``x``: fp16 or bf16
+    [T][K], quantized on the way, or the dict of ``quantize_act``.  ``out_dtype``
+    is x's type, or fp16 for a dict, unless given."""
+    ptrs, T, K, dev, out_dtype = _activations(x, out_dtype)
+    N, k = _weights(packed, scales, zeros, dev)
+    if k != K:
+        raise ValueError("x and the weights must have the same K")
+    y = _out(out, "out", (T, N), out_dtype, dev)
+    with _on(dev):
+        need = linear_w8a8_workspace_bytes(T, N, K, ptrs[1])
+        ws, at = _workspace(need, "lowbit_linear_w8a8_workspace_bytes", dev)
+        _check(linear_w8a8_raw(*ptrs, T, packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
+                               N, K, y.data_ptr(), _float_type(y, "out"), at, need,
+                               _stream_handle(dev)), "lowbit_linear_w8a8")
+    return y
+
+
+def gated_w8a8(x, packed_gate, scales_gate, zeros_gate, packed_up, scales_up, zeros_up,
+               act: str = "silu", save: bool = False, out_dtype=None):
+    """h[T][N] = act(x * deq(gate)^T) * (x * deq(up)^T), both projections in
+    one kernel; ``act``: "silu" or "gelu_tanh"; ``x`` as for ``linear_w8a8``.
+    ``save``: (h, gate, up), the projections rounded to the output type, which
+    ``gated_w8a8_grad`` takes."""
+    torch = _torch()
+    kind = _act(act)
+    ptrs, T, K, dev, out_dtype = _activations(x, out_dtype)
+    N, k = _weights(packed_gate, scales_gate, zeros_gate, dev)
+    if k != K:
+        raise ValueError("x and the weights must have the same K")
+    _weights(packed_up, scales_up, zeros_up, dev, N, K)
+    outs = [torch.empty((T, N), dtype=out_dtype, device=dev) for _ in range(3 if save else 1)]
+    with _on(dev):
+        need = gated_w8a8_workspace_bytes(T, N, K, ptrs[1])
+        ws, at = _workspace(need, "lowbit_gated_w8a8_workspace_bytes", dev)
+        _check(gated_w8a8_raw(*ptrs, T, packed_gate.data_ptr(), scales_gate.data_ptr(),
+                              zeros_gate.data_ptr(), packed_up.data_ptr(), scales_up.data_ptr(),
+                              zeros_up.data_ptr(), N, K, kind, outs[0].data_ptr(),
+                              outs[1].data_ptr() if save else None,
+                              outs[2].data_ptr() if save else None, _float_type(outs[0], "h"), at,
+                              need, _stream_handle(dev)), "lowbit_gated_w8a8")
+    return tuple(outs) if save else outs[0]
+
+
+def linear_w8a8_grad(dy, packed, scales, zeros, out=None):
+    """dx[T][K] = dy[T][N] * deq(packed), of dy's type: the gradient of
+    ``linear_w8a8`` with respect to x."""
+    kind = _float_type(dy, "dy")
+    _matrix(dy, "dy", dy.dtype)
+    dev = dy.device
+    N, K = _weights(packed, scales, zeros, dev)
+    T = dy.shape[0]
+    if dy.shape[1] != N:
+        raise ValueError("dy.shape[1] must be the weights' N")
+    dx = _out(out, "out", (T, K), dy.dtype, dev)
+    with _on(dev):
+        need = linear_w8a8_grad_workspace_bytes(T, N, K)
+        ws, at = _workspace(need, "lowbit_linear_w8a8_grad_workspace_bytes", dev)
+        _check(linear_w8a8_grad_raw(dy.data_ptr(), kind, T, packed.data_ptr(), scales.data_ptr(),
+                                    zeros.data_ptr(), N, K, dx.data_ptr(), at, need,
+                                    _stream_handle(dev)), "lowbit_linear_w8a8_grad")
+    return dx
+
+
+def gated_w8a8_grad(dh, gate, up, packed_gate, scales_gate, zeros_gate, packed_up, scales_up,
+                    zeros_up, act: str = "silu", parts: bool = False):
+    """dx[T][K], the gradient of ``gated_w8a8`` with respect to x, from dh and
+    the projections that the forward call saved (one type).  ``parts``: (dx,
+    dgate, dup), with the gradients of both projections' outputs, from which
+    those of adapters beside them follow."""
+    torch = _torch()
+    code = _act(act)
+    kind = _float_type(dh, "dh")
+    _matrix(dh, "dh", dh.dtype)
+    dev = dh.device
+    N, K = _weights(packed_gate, scales_gate, zeros_gate, dev)
+    _weights(packed_up, scales_up, zeros_up, dev, N, K)
+    T = dh.shape[0]
+    if dh.shape[1] != N:
+        raise ValueError("dh.shape[1] must be the weights' N")
+    _matrix(gate, "gate", dh.dtype, dev, dh.shape)
+    _matrix(up, "up", dh.dtype, dev, dh.shape)
+    dx = torch.empty((T, K), dtype=dh.dtype, device=dev)
+    dgate = torch.empty_like(dh) if parts else None
+    dup = torch.empty_like(dh) if parts else None
+    with _on(dev):
+        need = gated_w8a8_grad_workspace_bytes(T, N, K)
+        ws, at = _workspace(need, "lowbit_gated_w8a8_grad_workspace_bytes", dev)
+        _check(gated_w8a8_grad_raw(dh.data_ptr(), gate.data_ptr(), up.data_ptr(), kind, T,
+                                   packed_gate.data_ptr(), scales_gate.data_ptr(),
+                                   zeros_gate.data_ptr(), packed_up.data_ptr(),
+                                   scales_up.data_ptr(), zeros_up.data_ptr(), N, K, code,
+                                   dx.data_ptr(), _ptr(dgate), _ptr(dup), at, need,
+                                   _stream_handle(dev)), "lowbit_gated_w8a8_grad")
+    return (dx, dgate, dup) if parts else dx
