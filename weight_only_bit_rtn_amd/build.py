@@ -15,7 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 SOURCES = ["abi.hip", "quantize.hip", "gemv.hip", "gemv2.hip", "gemv3.hip", "gemv4.hip", "gemv8.hip", "gemv_mma.hip", "gemm.hip", "gptq.hip",
-           "abi_w8a8.hip", "act_quant.hip", "w8a8_gemm.hip", "w8a8_grad.hip"]
+           "abi_w8a8.hip", "act_quant.hip", "w8a8_few.hip", "w8a8_gemm.hip",
+           "w8a8_grad.hip", "w8a8_skinny.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

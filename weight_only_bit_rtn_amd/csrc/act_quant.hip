@@ -5,23 +5,10 @@
 // workgroup per token holds its row in registers between the maximum and the
 // codes, so x is read once: 2 bytes read and 1 written for each value, bound
 // by HBM.
-//
-// The quotient is not divided out: with r = fl32(1 / S), x * r differs from
-// x / S by less than 2^-15 for |x / S| < 128, so rint of the two can differ
-// only when x * r lies within that of a half; there (and where r or the
-// product overflows) the division is done.
 #include "w8a8.h"
 
 namespace lowbit {
 namespace {
-
-// Code of one value.
-__device__ __forceinline__ int act_code(float x, float s, float r) {
-  const float q = x * r;
-  float n = rintf(q);
-  if (!(fabsf(q - n) <= 0.4999f)) n = rintf(x / s);
-  return (int)fminf(fmaxf(n, -127.0f), 127.0f);
-}
 
 // NC chunks of 8 values per thread, blockDim.x threads; chunk c of the row
 // belongs to thread c mod blockDim.x.

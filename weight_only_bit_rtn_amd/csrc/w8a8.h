@@ -11,6 +11,8 @@ enum ElemType { kF16 = 0, kBF16 = 1, kI8 = 2 };
 enum ActKind { kSilu = 0, kGeluTanh = 1 };
 
 typedef int i4_t __attribute__((ext_vector_type(4)));
+typedef int i16_t __attribute__((ext_vector_type(16)));
+typedef float f16_t __attribute__((ext_vector_type(16)));
 typedef int i2_t __attribute__((ext_vector_type(2)));
 typedef uint16_t us4_t __attribute__((ext_vector_type(4)));
 typedef uint16_t us8_t __attribute__((ext_vector_type(8)));
@@ -57,17 +59,36 @@ __device__ __forceinline__ void act_value_slope(float v, int act, float& f, floa
   df = s + s * (1.0f - s) * w;
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes,
-                                           0x00020000);
+// Buffer descriptor (raw, range-checked) of `bytes` bytes at a wave-uniform address.
+__device__ __forceinline__ i4_t buffer_of(const void* base, uint32_t bytes) {
+  const uint64_t at = reinterpret_cast<uint64_t>(base);
+  return i4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)at),
+              __builtin_amdgcn_readfirstlane((int)((uint32_t)(at >> 32) & 0xffffu)),
+              __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+
+// The LDS address of a pointer into shared memory.
+__device__ __forceinline__ uint32_t lds_address(void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)p;
 }
 
 // 16 bytes per lane from a range-checked buffer straight into LDS: lane l's
-// land at lds + 16 l (lds is wave-uniform); an offset outside the buffer
-// brings zeros.
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, void* lds, uint32_t offset) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(
-      rs, (__attribute__((address_space(3))) void*)lds, 16, (int)offset, 0, 0, 0);
+// land at address at + 16 l (wave-uniform); an offset outside the buffer
+// brings zeros.  Written in assembly, where it has no register result: behind
+// the builtin the compiler waits for every such load in flight before a
+// transposing LDS read (large gradient 4.1 -> 3.1 ms without those waits).
+// The caller waits with lds_loads_left() before the barrier that publishes
+// them, and for all of them before its wave ends.
+__device__ __forceinline__ void load_to_lds(i4_t rs, uint32_t at, uint32_t offset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(at), "v"(offset), "s"(rs)
+               : "memory", "m0");
+}
+// Waits until at most N of the wave's loads are on their way (they land in order).
+template <int N>
+__device__ __forceinline__ void lds_loads_left() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
 }
 
 // Workgroup id -> tile: ids go round the 8 chiplets one by one, so give each
@@ -84,6 +105,51 @@ __device__ __forceinline__ void tile_of(int id, int total, int tiles_m, int tile
   tm = band * kBand + in % rows;
   tn = in / rows;
 }
+
+// Code of one activation value: rint(fl32(x / s)) within [-127, 127], s the
+// token's scale and r = fl32(1 / s).  x * r differs from x / s by less than
+// 2^-15 for |x / s| < 128, so rint of the two can differ only when x * r lies
+// within that of a half; there (and where r or the product overflows) the
+// division is done.
+__device__ __forceinline__ int act_code(float x, float s, float r) {
+  const float q = x * r;
+  float n = rintf(q);
+  if (!(fabsf(q - n) <= 0.4999f)) n = rintf(x / s);
+  return (int)fminf(fmaxf(n, -127.0f), 127.0f);
+}
+
+// Integer sum of one output to fp32: acc = sum a (code - 128), zc = 128 -
+// zero point, total = sum a.  `small` (K <= 65536 and a zero point in
+// [0, 255]): |total| < 2^23 and the sum of a (code - z) fits 32 bits;
+// otherwise it is formed in fp64, where it is exact too (below 2^43).
+__device__ __forceinline__ float exact_sum(int acc, int zc, int total, bool small) {
+  if (small) return (float)(acc + __mul24(zc, total));
+  return (float)((double)acc + (double)zc * (double)total);
+}
+
+struct GemmArgs {
+  const int8_t* a;  // codes of the activations, or null: x is quantized in the kernel
+  const uint16_t* x;
+  const float* xs;
+  const int32_t* xsum;
+  W8 w[2];
+  void* y;
+  void* g;
+  void* u;
+  int T, N, K, act, bf16, x_bf16, tiles_m, tiles_n;
+};
+
+// Products of at most 8 tokens whose codes fit LDS (w8a8_few.hip).  Without
+// p.a the kernel quantizes p.x itself: T K <= kFusedMost.
+constexpr int kFewMostT = 8;
+constexpr int kFewMostCodes = 128 * 1024;
+constexpr int kFusedMost = 16384;
+bool few_takes(int64_t T, int64_t K);
+hipError_t launch_few(const GemmArgs& p, bool gated, hipStream_t stream);
+
+// Products of at most 64 tokens (w8a8_skinny.hip).
+constexpr int kSkinnyMostT = 64;
+hipError_t launch_skinny(const GemmArgs& p, bool gated, hipStream_t stream);
 
 hipError_t launch_quantize_act(const void* x, int dtype, int64_t T, int64_t K, int8_t* codes,
                                float* scales, int32_t* sums, hipStream_t stream);

@@ -1,0 +1,291 @@
+// w8a8_few.hip -- the 8-bit products for one to eight tokens: a decoding step.
+//
+// Reading the weights is all that takes time (one byte each, used once per
+// token), so each wave reads whole rows as they lie, 1 KiB per instruction,
+// and multiplies with v_dot4_i32_i8; the matrix cores would want 16 rows per
+// instruction, 64 bytes of each, and reading in such pieces ran at 5.0-5.6
+// TB/s where whole rows ran at DOC_RATE TB/s.
+//
+// One workgroup of 16 waves per CU keeps the tokens' codes in LDS: it
+// quantizes x itself when that is little (T K <= kFusedMost), while its
+// first weights are on their way, and copies codes otherwise.  Wave w of
+// workgroup b takes rows w G + b, then 16 G further (G workgroups), so few
+// rows still spread over all CUs.  Eight loads per lane are in flight,
+// running ahead into the wave's next rows.
+#include "w8a8.h"
+
+namespace lowbit {
+namespace {
+
+constexpr int kWaves = 16;
+constexpr int kChunk = 1024;   // bytes of a row per load
+constexpr int kInFlight = 8;   // loads per lane
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t checked(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes,
+                                           0x00020000);
+}
+__device__ __forceinline__ i4_t load16(__amdgpu_buffer_rsrc_t rs, uint32_t offset) {
+  return __builtin_bit_cast(i4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)offset, 0, 0));
+}
+
+// Bytes of one token's codes in LDS: whole chunks, zeros behind the last.
+__host__ __device__ constexpr int few_pitch(int K) {
+  return (K + kChunk - 1) / kChunk * kChunk;
+}
+
+// Sum over the 64 lanes, in lane 63.
+__device__ __forceinline__ int wave_sum_last(int v) {
+#define LOWBIT_ADD(ctrl, rows) v += __builtin_amdgcn_update_dpp(0, v, ctrl, rows, 0xf, false)
+  LOWBIT_ADD(0xb1, 0xf);   // quad_perm [1,0,3,2]
+  LOWBIT_ADD(0x4e, 0xf);   // quad_perm [2,3,0,1]
+  LOWBIT_ADD(0x141, 0xf);  // row_half_mirror
+  LOWBIT_ADD(0x140, 0xf);  // row_mirror
+  LOWBIT_ADD(0x142, 0xa);  // row_bcast:15 into rows 1 and 3
+  LOWBIT_ADD(0x143, 0xc);  // row_bcast:31 into rows 2 and 3
+#undef LOWBIT_ADD
+  return v;
+}
+
+// Codes of all tokens into LDS (rows of few_pitch), scales and sums into meta
+// (token t: meta[t] and meta[8 + t]).  Tokens share the waves out: 16 / TT
+// waves each, the token's values held in registers between its maximum and
+// its codes.  Ends with a barrier.
+template <int TT>
+__device__ __forceinline__ void quantize_here(const GemmArgs& p, int8_t* codes, int* meta,
+                                              int* red) {
+  constexpr int W = kWaves / TT;  // waves per token
+  // T K <= 16384 in chunks of 8 over 64 W lanes; TT is T or the next power of two
+  constexpr int NC = kFusedMost / 8 / (64 * kWaves) * 2;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int t = wave / W, part = wave % W;
+  const bool mine = t < p.T;
+  const int chunks = p.K / 8, all = few_pitch(p.K) / 8;
+  us8_t v[NC];
+  int top = 0;
+  const us8_t* xr = reinterpret_cast<const us8_t*>(p.x + (int64_t)(mine ? t : 0) * p.K);
+#pragma unroll
+  for (int i = 0; i < NC; i++) {
+    const int c = part * 64 + lane + i * (64 * W);
+    v[i] = us8_t{};
+    if (c < chunks) v[i] = xr[c];
+  }
+#pragma unroll
+  for (int i = 0; i < NC; i++)
+#pragma unroll
+    for (int j = 0; j < 8; j++) top = max(top, (int)(v[i][j] & 0x7fff));
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) top = max(top, __shfl_xor(top, off, kWave));
+  if (lane == 0) red[wave] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < W; w++) top = max(top, red[t * W + w]);
+  const bool finite = top < (p.x_bf16 ? 0x7f80 : 0x7c00);
+  float s = elem_to_f32((uint16_t)top, p.x_bf16) / 127.0f;
+  if (s == 0.0f) s = 1.0f;
+  const float r = 1.0f / s;
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < NC; i++) {
+    const int c = part * 64 + lane + i * (64 * W);
+    uint32_t w[2] = {0, 0};
+    if (c < chunks && finite) {
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const int a = act_code(elem_to_f32(v[i][j], p.x_bf16), s, r);
+        sum += a;
+        w[j / 4] |= (uint32_t)(a & 255) << (8 * (j % 4));
+      }
+    }
+    if (mine && c < all)
+      *reinterpret_cast<uint2*>(codes + t * few_pitch(p.K) + c * 8) = make_uint2(w[0], w[1]);
+  }
+  // zeros up to whole chunks of the products, where the loop above ends before
+  if (mine)
+    for (int c = part * 64 + lane + NC * (64 * W); c < all; c += 64 * W)
+      *reinterpret_cast<uint2*>(codes + t * few_pitch(p.K) + c * 8) = make_uint2(0, 0);
+  sum = wave_sum_last(sum);
+  if (lane == 63) red[kWaves + wave] = sum;
+  __syncthreads();
+  if (tid < p.T) {
+    sum = 0;
+#pragma unroll
+    for (int w = 0; w < W; w++) sum += red[kWaves + tid * W + w];
+    meta[8 + tid] = sum;
+  }
+  if (lane == 0 && part == 0 && mine)
+    meta[t] = __builtin_bit_cast(int, finite ? s : __builtin_nanf(""));
+  __syncthreads();
+}
+
+// TT tokens (those past T repeat the last), RR rows per item; gated: RR / 2
+// rows of each matrix.
+template <int TT, int RR, bool GATED, bool FUSED>
+__global__ __launch_bounds__(kWaves * 64) void few_kernel(const GemmArgs p) {
+  constexpr int D = kInFlight / RR;
+  constexpr int RO = GATED ? RR / 2 : RR;  // output columns per item
+  static_assert(!FUSED || TT <= 8, "tokens per wave");
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  int* meta = reinterpret_cast<int*>(lds);  // scales, sums, scratch: 64 words
+  int8_t* codes = reinterpret_cast<int8_t*>(lds + 256);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t K = (uint32_t)p.K;
+  const int steps = (p.K + kChunk - 1) / kChunk, pitch = few_pitch(p.K);
+  const int items = (p.N + RO - 1) / RO, stride = gridDim.x * kWaves;
+  const int first = wave * gridDim.x + blockIdx.x;
+
+  i4_t w[D][RR];
+  int li = first, ls = 0;  // item and step of the next load
+  // positions past a row's end and rows past the last come as zeros
+  auto load = [&](i4_t(&wd)[RR]) {
+    const uint32_t k = (uint32_t)ls * kChunk + lane * 16;
+    const uint32_t at = k < K ? k : 0x80000000u;
+#pragma unroll
+    for (int m = 0; m < (GATED ? 2 : 1); m++) {
+      const int n = li * RO;
+      const auto rs = checked(p.w[m].codes + (int64_t)n * K,
+                              (uint32_t)max(0, min(RO, p.N - n)) * K);
+#pragma unroll
+      for (int r = 0; r < RO; r++) wd[m * RO + r] = load16(rs, at + r * K);
+    }
+    if (++ls == steps) {
+      ls = 0;
+      li += stride;
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D; d++) load(w[d]);
+  if constexpr (FUSED) {
+    quantize_here<TT>(p, codes, meta, meta + 16);
+  } else {
+    for (int c = threadIdx.x; c < p.T * (pitch / 16); c += kWaves * 64) {
+      const int t = c / (pitch / 16), k = c % (pitch / 16) * 16;
+      i4_t v = {0, 0, 0, 0};
+      if (k < p.K) v = *reinterpret_cast<const i4_t*>(p.a + (int64_t)t * K + k);
+      *reinterpret_cast<i4_t*>(codes + c * 16) = v;
+    }
+    if (threadIdx.x < (unsigned)p.T) {
+      meta[threadIdx.x] = __builtin_bit_cast(int, p.xs[threadIdx.x]);
+      meta[8 + threadIdx.x] = p.xsum[threadIdx.x];
+    }
+    __syncthreads();
+  }
+
+  // the lane that finishes output (r, t) of an item is lane r TT + t
+  const int fr = lane / TT % RO, ft = lane % TT;
+  const bool finishes = lane < RO * TT && ft < p.T;
+  const float xs = __builtin_bit_cast(float, meta[min(ft, p.T - 1)]);
+  const int total = meta[8 + min(ft, p.T - 1)];
+  int acc[RR][TT];
+  for (int item = first, step = 0; item < items;) {
+#pragma unroll
+    for (int d = 0; d < D; d++) {
+      if (step == 0) {
+#pragma unroll
+        for (int r = 0; r < RR; r++)
+#pragma unroll
+          for (int t = 0; t < TT; t++) acc[r][t] = 0;
+      }
+      i4_t wx[RR];
+#pragma unroll
+      for (int r = 0; r < RR; r++) wx[r] = w[d][r] ^ (int)0x80808080;
+#pragma unroll
+      for (int t = 0; t < TT; t++) {
+        const i4_t a = *reinterpret_cast<const i4_t*>(codes + min(t, p.T - 1) * pitch +
+                                                      step * kChunk + lane * 16);
+#pragma unroll
+        for (int r = 0; r < RR; r++)
+#pragma unroll
+          for (int q = 0; q < 4; q++)
+            acc[r][t] = __builtin_amdgcn_sdot4(wx[r][q], a[q], acc[r][t], false);
+      }
+      load(w[d]);
+      __builtin_amdgcn_sched_barrier(0);  // keeps the other loads in flight
+      if (++step == steps) {
+        if (item < items) {
+          const int n = item * RO + fr;
+          const bool last = finishes && n < p.N;
+          float sc[2];
+          int z[2];
+#pragma unroll
+          for (int m = 0; m < (GATED ? 2 : 1); m++) {
+            sc[m] = last ? h_bits_to_f32(p.w[m].scales[n]) : 0.0f;
+            z[m] = last ? p.w[m].zeros[n] : 0;
+          }
+          int mine[2] = {0, 0};
+#pragma unroll
+          for (int r = 0; r < RR; r++)
+#pragma unroll
+            for (int t = 0; t < TT; t++) {
+              const int v = __builtin_amdgcn_readlane(wave_sum_last(acc[r][t]), 63);
+              if (lane == r % RO * TT + t) mine[r / RO] = v;
+            }
+          if (last) {
+            float v[2];
+#pragma unroll
+            for (int m = 0; m < (GATED ? 2 : 1); m++)
+              v[m] = exact_sum(mine[m], 128 - z[m], total,
+                               p.K <= 65536 && (uint32_t)z[m] < 256u) * (xs * sc[m]);
+            const int64_t at = (int64_t)ft * p.N + n;
+            auto put = [&](void* base, float f) {
+              static_cast<uint16_t*>(base)[at] = f32_to_elem(f, p.bf16);
+            };
+            if constexpr (GATED) {
+              put(p.y, act_value(v[0], p.act) * v[1]);
+              if (p.g) {
+                put(p.g, v[0]);
+                put(p.u, v[1]);
+              }
+            } else {
+              put(p.y, v[0]);
+            }
+          }
+        }
+        step = 0;
+        item += stride;
+      }
+    }
+  }
+}
+
+template <int TT, int RR, bool GATED, bool FUSED>
+hipError_t launch_one(const GemmArgs& p, hipStream_t stream) {
+  constexpr int RO = GATED ? RR / 2 : RR;
+  constexpr int most = 256 + kFewMostCodes;
+  const int bytes = 256 + p.T * few_pitch(p.K);
+  auto kernel = few_kernel<TT, RR, GATED, FUSED>;
+  hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), most);
+  if (e != hipSuccess) return e;
+  const int items = (p.N + RO - 1) / RO;
+  const int groups = items < device_cu_count() ? items : device_cu_count();
+  kernel<<<dim3((unsigned)groups), dim3(kWaves * 64), bytes, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <int TT, int RR, bool GATED>
+hipError_t launch_x(const GemmArgs& p, hipStream_t stream) {
+  return p.a ? launch_one<TT, RR, GATED, false>(p, stream)
+             : launch_one<TT, RR, GATED, true>(p, stream);
+}
+
+}  // namespace
+
+bool few_takes(int64_t T, int64_t K) {
+  return T <= kFewMostT && T * few_pitch((int)K) <= kFewMostCodes;
+}
+
+hipError_t launch_few(const GemmArgs& p, bool gated, hipStream_t stream) {
+  if (gated) {
+    if (p.T <= 1) return launch_x<1, 2, true>(p, stream);
+    if (p.T <= 2) return launch_x<2, 2, true>(p, stream);
+    if (p.T <= 4) return launch_x<4, 2, true>(p, stream);
+    return launch_x<8, 2, true>(p, stream);
+  }
+  if (p.T <= 1) return launch_x<1, 1, false>(p, stream);
+  if (p.T <= 2) return launch_x<2, 1, false>(p, stream);
+  if (p.T <= 4) return launch_x<4, 2, false>(p, stream);
+  return launch_x<8, 2, false>(p, stream);
+}
+
+}  // namespace lowbit

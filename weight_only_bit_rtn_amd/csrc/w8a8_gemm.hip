@@ -12,26 +12,8 @@
 namespace lowbit {
 namespace {
 
-constexpr int kStep = 128;  // bytes (values) of k per pipeline step
-
-struct GemmArgs {
-  const int8_t* a;
-  const float* xs;
-  const int32_t* xsum;
-  W8 w[2];
-  void* y;
-  void* g;
-  void* u;
-  int T, N, K, act, bf16, tiles_m, tiles_n;
-};
-
-// Integer sum of one output to fp32.  For K <= 65536 and a zero point in
-// [0, 255], |A| < 2^23 and the sum of a (code - z) fits 32 bits; otherwise it
-// is formed in fp64, where it is exact too (below 2^43).
-__device__ __forceinline__ float exact_sum(int acc, int zc, int total, bool small) {
-  if (small) return (float)(acc + __mul24(zc, total));
-  return (float)((double)acc + (double)zc * (double)total);
-}
+constexpr int kStep = 64;    // bytes (values) of k per pipeline step
+constexpr int kBuffers = 4;  // LDS buffers of one step each
 
 // One workgroup of WM x WN waves computes MT tokens by NT weight rows (gated:
 // NT / 2 rows of each matrix, the wave's first half gate, its second half up,
@@ -47,8 +29,9 @@ __global__ __launch_bounds__(WM* WN * 64) void w8a8_kernel(const GemmArgs p) {
   constexpr int MW = MT / WM, NW = NT / WN;  // wave tile
   constexpr int FM = MW / 16, FN = NW / 16;  // its fragments
   constexpr int NO = GATED ? NT / 2 : NT;    // output columns of a tile
-  constexpr int LA = MT / 8 / kWaves, LB = NT / 8 / kWaves;  // 1 KiB loads per wave and step
-  static_assert(LA * 8 * kWaves == MT && LB * 8 * kWaves == NT, "whole loads");
+  constexpr int LA = MT / 16 / kWaves, LB = NT / 16 / kWaves;  // 1 KiB loads per wave and step
+  constexpr int kLoads = LA + LB;
+  static_assert(LA * 16 * kWaves == MT && LB * 16 * kWaves == NT, "whole loads");
   static_assert(!GATED || (FN % 2 == 0 && LB % 2 == 0), "gate and up halves");
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   constexpr int kBuf = (MT + NT) * kStep;
@@ -67,32 +50,33 @@ __global__ __launch_bounds__(WM* WN * 64) void w8a8_kernel(const GemmArgs p) {
   const auto rg = buffer_of(p.w[0].codes + (int64_t)n0 * K, wbytes);
   const auto ru = GATED ? buffer_of(p.w[1].codes + (int64_t)n0 * K, wbytes) : rg;
 
-  // a load covers 8 rows of 128 bytes: lane l brings chunk (l & 7) ^ (l >> 3) of row l >> 3
-  const uint32_t r8 = lane >> 3, chunk = ((lane & 7) ^ r8) * 16;
+  // a load covers 16 rows of 64 bytes: lane l brings chunk (l & 3) ^ swizzle of row l >> 2
+  const uint32_t r16 = lane >> 2, chunk = ((lane & 3) ^ (-(lane >> 4) & 3)) * 16;
   uint32_t oa[LA], ob[LB];
-  int la[LA], lb[LB];
+  uint32_t la[LA], lb[LB];
+  const uint32_t base = lds_address(lds);
 #pragma unroll
   for (int i = 0; i < LA; i++) {
-    const int row = (wave + i * kWaves) * 8;
-    oa[i] = (row + r8) * K + chunk;
-    la[i] = row * kStep;
+    const int row = (wave + i * kWaves) * 16;
+    oa[i] = (row + r16) * K + chunk;
+    la[i] = base + row * kStep;
   }
 #pragma unroll
   for (int i = 0; i < LB; i++) {
     // gated: the first half of the loads is the gate matrix
-    const int b = wave + (GATED ? i % (LB / 2) : i) * kWaves;
-    const int row = b * 8;
-    ob[i] = (row + r8) * K + chunk;
+    const int row = (wave + (GATED ? i % (LB / 2) : i) * kWaves) * 16;
+    ob[i] = (row + r16) * K + chunk;
     const int slot = GATED ? row / (NW / 2) * NW + row % (NW / 2) + (i >= LB / 2 ? NW / 2 : 0) : row;
-    lb[i] = (MT + slot) * kStep;
+    lb[i] = base + (MT + slot) * kStep;
   }
-  auto stage = [&](uint8_t* buf, uint32_t k0) {
+  // load i of the LA + LB of step s; past the last step it brings zeros
+  auto load = [&](int s, int i) {
+    const uint32_t k0 = (uint32_t)s * kStep, buf = (uint32_t)(s % kBuffers) * kBuf;
     const uint32_t add = k0 + chunk < K ? k0 : 0x80000000u;
-#pragma unroll
-    for (int i = 0; i < LA; i++) load_to_lds(ra, buf + la[i], oa[i] + add);
-#pragma unroll
-    for (int i = 0; i < LB; i++)
-      load_to_lds(GATED && i >= LB / 2 ? ru : rg, buf + lb[i], ob[i] + add);
+    if (i < LA)
+      load_to_lds(ra, la[i] + buf, oa[i] + add);
+    else
+      load_to_lds(GATED && i - LA >= LB / 2 ? ru : rg, lb[i - LA] + buf, ob[i - LA] + add);
   };
 
   i4_t acc[FN][FM];
@@ -101,33 +85,54 @@ __global__ __launch_bounds__(WM* WN * 64) void w8a8_kernel(const GemmArgs p) {
 #pragma unroll
     for (int j = 0; j < FM; j++) acc[i][j] = i4_t{0, 0, 0, 0};
 
-  const int steps = (p.K + kStep - 1) / kStep;
-  stage(lds, 0);
-  for (int s = 0; s < steps; s++) {
-    uint8_t* buf = lds + (s & 1) * kBuf;
-    __builtin_amdgcn_s_waitcnt(0xf70);  // vmcnt(0): this step's loads of this wave have landed
-    __syncthreads();                    // and everyone's; the other buffer is free
-    if (s + 1 < steps) stage(lds + ((s + 1) & 1) * kBuf, (uint32_t)(s + 1) * kStep);
-    const uint8_t* ba = buf + (wm * MW + i16) * kStep;
-    const uint8_t* bb = buf + (MT + wn * NW + i16) * kStep;
+  // operands from LDS: row lane % 16, chunk lane / 16
+  const uint32_t swizzled = (h ^ (-(i16 >> 2) & 3)) * 16;
+  const uint32_t ra0 = (wm * MW + i16) * kStep + swizzled, rb0 = (MT + wn * NW + i16) * kStep + swizzled;
+  auto tokens = [&](int s, int j) {
+    return *reinterpret_cast<const i4_t*>(lds + s % kBuffers * kBuf + ra0 + j * 16 * kStep);
+  };
+  auto rows = [&](int s, int i) {
+    return *reinterpret_cast<const i4_t*>(lds + s % kBuffers * kBuf + rb0 + i * 16 * kStep);
+  };
+  // one step: its tokens are in fa and its first kAhead row operands in fb;
+  // reads the next step's tokens into fn and the row operands kAhead ahead
+  constexpr int kAhead = 2;
+  i4_t fb[kAhead];
+  auto step = [&](int s, const i4_t(&fa)[FM], i4_t(&fn)[FM]) {
+    lds_loads_left<(kBuffers - 3) * kLoads>();  // this wave's part of step s + 1 has landed
+    __syncthreads();                            // and everyone's; step s - 1 has been read
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int ks = 0; ks < 2; ks++) {
-      const int at = ((ks * 4 + h) ^ (i16 & 7)) * 16;
-      i4_t fa[FM], fb[FN];
+    for (int i = 0; i < FN; i++) {
 #pragma unroll
-      for (int i = 0; i < FN; i++) {
-        fb[i] = *reinterpret_cast<const i4_t*>(bb + i * 16 * kStep + at);
-        fb[i] ^= (int)0x80808080;
-      }
+      for (int l = i * kLoads / FN; l < (i + 1) * kLoads / FN; l++) load(s + kBuffers - 1, l);
+      const i4_t w = fb[i % kAhead] ^ (int)0x80808080;
+      fb[i % kAhead] = i + kAhead < FN ? rows(s, i + kAhead) : rows(s + 1, i + kAhead - FN);
 #pragma unroll
-      for (int j = 0; j < FM; j++) fa[j] = *reinterpret_cast<const i4_t*>(ba + j * 16 * kStep + at);
+      for (int j = i * FM / FN; j < (i + 1) * FM / FN; j++) fn[j] = tokens(s + 1, j);
 #pragma unroll
-      for (int i = 0; i < FN; i++)
-#pragma unroll
-        for (int j = 0; j < FM; j++)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[i], fa[j], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < FM; j++)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, fa[j], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
+  };
+  const int steps = (p.K + kStep - 1) / kStep;
+  i4_t f0[FM], f1[FM];
+#pragma unroll
+  for (int s = 0; s < kBuffers - 1; s++)
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) load(s, i);
+  lds_loads_left<(kBuffers - 2) * kLoads>();
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < FM; j++) f0[j] = tokens(0, j);
+#pragma unroll
+  for (int i = 0; i < kAhead; i++) fb[i] = rows(0, i);
+  for (int s = 0; s < steps; s += 2) {
+    step(s, f0, f1);
+    step(s + 1, f1, f0);  // past the end: zeros
   }
+  lds_loads_left<0>();
 
   // lane l of a fragment holds outputs n = 4 (l / 16) + 0..3 of token l % 16
   const bool bf = p.bf16;
@@ -173,13 +178,13 @@ __global__ __launch_bounds__(WM* WN * 64) void w8a8_kernel(const GemmArgs p) {
       }
       const int64_t at = (int64_t)t * p.N + n;
       auto put = [&](void* base, us4_t v) {
-        uint16_t* q = static_cast<uint16_t*>(base) + at;
+        uint16_t* d = static_cast<uint16_t*>(base) + at;
         if (vec) {
-          *reinterpret_cast<us4_t*>(q) = v;
+          *reinterpret_cast<us4_t*>(d) = v;
         } else {
 #pragma unroll
           for (int r = 0; r < 4; r++)
-            if (n + r < p.N) q[r] = v[r];
+            if (n + r < p.N) d[r] = v[r];
         }
       };
       put(p.y, out);
@@ -194,7 +199,7 @@ __global__ __launch_bounds__(WM* WN * 64) void w8a8_kernel(const GemmArgs p) {
 template <int MT, int NT, int WM, int WN, bool GATED>
 hipError_t launch_tile(GemmArgs p, hipStream_t stream) {
   constexpr int NO = GATED ? NT / 2 : NT;
-  constexpr int bytes = 2 * (MT + NT) * kStep;
+  constexpr int bytes = kBuffers * (MT + NT) * kStep;
   auto kernel = w8a8_kernel<MT, NT, WM, WN, GATED>;
   hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), bytes);
   if (e != hipSuccess) return e;
@@ -208,6 +213,11 @@ hipError_t launch_tile(GemmArgs p, hipStream_t stream) {
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
+// Few activations are quantized inside the product's kernel.
+bool fused(int64_t T, int64_t K, int dtype) {
+  return dtype != kI8 && few_takes(T, K) && T * K <= kFusedMost;
+}
+
 template <bool GATED>
 hipError_t launch(const Activations& x, int64_t T, const W8& w0, const W8& w1, int64_t N,
                   int64_t K, int act, void* y, void* g, void* u, int out_dtype, void* workspace,
@@ -217,6 +227,9 @@ hipError_t launch(const Activations& x, int64_t T, const W8& w0, const W8& w1, i
     p.a = static_cast<const int8_t*>(x.x);
     p.xs = x.scales;
     p.xsum = x.sums;
+  } else if (fused(T, K, x.dtype)) {
+    p.x = static_cast<const uint16_t*>(x.x);
+    p.x_bf16 = x.dtype == kBF16;
   } else {
     auto* ws = static_cast<uint8_t*>(workspace);
     auto* codes = reinterpret_cast<int8_t*>(ws);
@@ -238,7 +251,8 @@ hipError_t launch(const Activations& x, int64_t T, const W8& w0, const W8& w1, i
   p.K = (int)K;
   p.act = act;
   p.bf16 = out_dtype == kBF16;
-  if (T <= 64) return launch_tile<64, 64, 2, 2, GATED>(p, stream);
+  if (few_takes(T, K)) return launch_few(p, GATED, stream);
+  if (T <= kSkinnyMostT) return launch_skinny(p, GATED, stream);
   if (T <= 512) return launch_tile<128, 128, 2, 2, GATED>(p, stream);
   return launch_tile<256, 256, 2, 4, GATED>(p, stream);
 }
@@ -246,7 +260,7 @@ hipError_t launch(const Activations& x, int64_t T, const W8& w0, const W8& w1, i
 }  // namespace
 
 size_t w8a8_workspace_bytes(int64_t T, int64_t N, int64_t K, int dtype, bool gated) {
-  if (dtype == kI8 || T == 0) return 0;
+  if (dtype == kI8 || T == 0 || fused(T, K, dtype)) return 0;
   return up256(T * K) + 2 * up256(T * 4);
 }
 

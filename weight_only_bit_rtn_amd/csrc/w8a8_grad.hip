@@ -178,7 +178,7 @@ __global__ __launch_bounds__(WM* WN * 64) void grad_kernel(const GradArgs p) {
     ow[i] = k0 + c * 16 < p.K ? (uint32_t)rw[i] * K + k0 + c * 16 : 0x80000000u;
     lw[i] = kA + (wave + i * kWaves) * 1024;
   }
-  auto stage = [&](uint8_t* buf, int s) {
+  auto stage = [&](uint32_t buf, int s) {
 #pragma unroll
     for (int i = 0; i < LA; i++) load_to_lds(ra, buf + la[i], oa[i] + (uint32_t)s * (kStepN * 2));
     const int m = s >= p.half_steps;
@@ -195,12 +195,13 @@ __global__ __launch_bounds__(WM* WN * 64) void grad_kernel(const GradArgs p) {
 #pragma unroll
     for (int j = 0; j < FM; j++) acc[i][j] = f4_t{0, 0, 0, 0};
 
-  if (p.steps > 0) stage(lds, 0);
+  const uint32_t base = lds_address(lds);
+  if (p.steps > 0) stage(base, 0);
   for (int s = 0; s < p.steps; s++) {
     uint8_t* buf = lds + (s & 1) * kBuf;
-    __builtin_amdgcn_s_waitcnt(0xf70);  // vmcnt(0): this step's loads of this wave have landed
-    __syncthreads();                    // and everyone's; the other buffer is free
-    if (s + 1 < p.steps) stage(lds + ((s + 1) & 1) * kBuf, s + 1);
+    lds_loads_left<0>();  // this step's loads of this wave have landed
+    __syncthreads();   // and everyone's; the other buffer is free
+    if (s + 1 < p.steps) stage(base + ((s + 1) & 1) * kBuf, s + 1);
     const uint8_t* ba = buf + (wm * MW + i16) * (kStepN * 2);
     const uint8_t* bw = buf + kA;
 #pragma unroll

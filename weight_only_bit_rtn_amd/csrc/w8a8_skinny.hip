@@ -1,0 +1,219 @@
+// w8a8_skinny.hip -- the 8-bit products for at most 64 tokens, where reading
+// the weights is what takes time.
+//
+// Weights go from HBM straight into the matrix cores' operand registers: a
+// workgroup of 8 waves owns 16 NR rows (gated: of each matrix) and its waves
+// share out K in steps of 64, wave w taking steps w, w + 8, ..., so the eight
+// waves together read 512 consecutive bytes of each row at a time.  Four
+// steps are in flight per wave.  Tokens are the other operand, in tiles of
+// 16: their codes come from the caches, or (one or a few tokens) from LDS,
+// where the workgroup has put them itself, quantized from x while its first
+// weights were on their way.  The waves' integer sums meet in LDS.
+#include "w8a8.h"
+
+namespace lowbit {
+namespace {
+
+// Shape of the ring: waves, bytes of a row per step, steps.
+template <int NT, bool GATED>
+struct Ring {
+  static constexpr int FR = GATED ? 2 : 1;
+  static constexpr int OPS = FR + NT;  // 16-row operands per step
+  static constexpr int W = 4;
+  static constexpr int CH = OPS <= 4 ? 256 : 128;
+  static constexpr int D = OPS == 2 ? 4 : 2;
+  static constexpr int kOp = 16 * CH;                // bytes of an operand
+  static constexpr int kRing = W * D * OPS * kOp;
+  static constexpr int kSums = W * FR * NT * 1024;
+};
+
+// 16 weight rows (of each matrix) per tile, NT token tiles.  The
+// workgroup walks tiles blockIdx.x, blockIdx.x + gridDim.x, ...; a wave's
+// loads run ahead into its next tile.
+template <int NT, bool GATED>
+__global__ __launch_bounds__((Ring<NT, GATED>::W * 64)) void skinny_kernel(const GemmArgs p) {
+  using R = Ring<NT, GATED>;
+  constexpr int FR = R::FR, OPS = R::OPS, CH = R::CH, D = R::D, kWaves = R::W;
+  constexpr int NR = 1, kSlots = CH / 16, kLoads = CH / 64;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  // the waves' rings, and their sums
+  i4_t* sums = reinterpret_cast<i4_t*>(lds + R::kRing);
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i16 = lane & 15, h = lane >> 4;
+  const uint32_t K = (uint32_t)p.K;
+  const int steps = (p.K + kWaves * CH - 1) / (kWaves * CH);  // of each wave and tile
+  const int tiles = (p.N + 15) / 16;
+  const i4_t ra = buffer_of(p.a, (uint32_t)p.T * K);
+
+  // load q of an operand: rows q * (1024 / CH) + ..., chunk c of a row at slot c ^ row
+  uint32_t off[kLoads], kc[kLoads];
+#pragma unroll
+  for (int q = 0; q < kLoads; q++) {
+    const int row = q * (1024 / CH) + lane / kSlots;
+    kc[q] = ((lane % kSlots) ^ (row & (kSlots < 16 ? 7 : 15))) * 16;
+    off[q] = row * K + kc[q];
+  }
+  const uint32_t ring = lds_address(lds) + wave * D * OPS * R::kOp;
+  int lt = blockIdx.x, ls = 0;  // tile and step of the next load
+  // values past the row's end come as zeros, and so do rows and tiles past the last
+  auto load = [&](int slot) {
+    const int n0 = lt * 16;
+    const uint32_t bytes = (uint32_t)max(0, min(16, p.N - n0)) * K;
+    const uint32_t k0 = (uint32_t)(ls * kWaves + wave) * CH;
+    const uint32_t to = ring + slot * OPS * R::kOp;
+#pragma unroll
+    for (int o = 0; o < OPS; o++) {
+      const i4_t rs = o < FR ? buffer_of(p.w[o].codes + (int64_t)n0 * K, bytes) : ra;
+#pragma unroll
+      for (int q = 0; q < kLoads; q++) {
+        uint32_t at = off[q] + k0 + (o < FR ? 0 : (o - FR) * 16 * K);
+        if (k0 + kc[q] >= K) at = 0x80000000u;
+        load_to_lds(rs, to + o * R::kOp + q * 1024, at);
+      }
+    }
+    if (++ls == steps) {
+      ls = 0;
+      lt += gridDim.x;
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D; d++) load(d);
+  i4_t acc[FR][NT];
+  auto clear = [&]() {
+#pragma unroll
+    for (int i = 0; i < FR; i++)
+#pragma unroll
+      for (int j = 0; j < NT; j++) acc[i][j] = i4_t{0, 0, 0, 0};
+  };
+  clear();
+  const bool bf = p.bf16, vec = p.N % 4 == 0;
+  // joins the waves' sums of a tile; the waves take turns to finish its
+  // NR x NT fragments: lane l holds outputs n = 4 (l / 16) + 0..3 of token l % 16
+  auto finish = [&](int tile, int round) {
+    __syncthreads();  // the last tile's sums have been read
+#pragma unroll
+    for (int i = 0; i < FR; i++)
+#pragma unroll
+      for (int j = 0; j < NT; j++) sums[(wave * FR * NT + i * NT + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    for (int o = (wave + round) % kWaves; o < NR * NT; o += kWaves) {
+      const int i = o / NT, j = o % NT;
+      const int n = tile * (16 * NR) + i * 16 + h * 4, t = j * 16 + i16;
+      if (n >= p.N || t >= p.T) continue;
+      i4_t sum[2] = {i4_t{0, 0, 0, 0}, i4_t{0, 0, 0, 0}};
+#pragma unroll
+      for (int v = 0; v < kWaves; v++) {
+        sum[0] += sums[(v * FR * NT + o) * 64 + lane];
+        if constexpr (GATED) sum[1] += sums[(v * FR * NT + NR * NT + o) * 64 + lane];
+      }
+      const float xs = p.xs[t];
+      const int total = p.xsum[t];
+      us4_t out, og, ou;
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        const int nn = min(n + r, p.N - 1);
+        float v[2];
+#pragma unroll
+        for (int m = 0; m < (GATED ? 2 : 1); m++) {
+          const int z = p.w[m].zeros[nn];
+          v[m] = exact_sum(sum[m][r], 128 - z, total, p.K <= 65536 && (uint32_t)z < 256u) *
+                 (xs * h_bits_to_f32(p.w[m].scales[nn]));
+        }
+        if constexpr (GATED) {
+          out[r] = f32_to_elem(act_value(v[0], p.act) * v[1], bf);
+          og[r] = f32_to_elem(v[0], bf);
+          ou[r] = f32_to_elem(v[1], bf);
+        } else {
+          out[r] = f32_to_elem(v[0], bf);
+        }
+      }
+      const int64_t at = (int64_t)t * p.N + n;
+      auto put = [&](void* base, us4_t v) {
+        uint16_t* d = static_cast<uint16_t*>(base) + at;
+        if (vec) {
+          *reinterpret_cast<us4_t*>(d) = v;
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; r++)
+            if (n + r < p.N) d[r] = v[r];
+        }
+      };
+      put(p.y, out);
+      if (GATED && p.g) {
+        put(p.g, og);
+        put(p.u, ou);
+      }
+    }
+    clear();
+  };
+
+  int tile = blockIdx.x, step = 0, round = 0;
+  const uint8_t* mine = lds + wave * D * OPS * R::kOp + i16 * CH;
+  const int turn = i16 & (kSlots < 16 ? 7 : 15);
+  while (tile < tiles) {
+#pragma unroll
+    for (int d = 0; d < D; d++) {
+      lds_loads_left<(D - 1) * OPS * kLoads>();
+      const uint8_t* buf = mine + d * OPS * R::kOp;
+#pragma unroll
+      for (int s = 0; s < CH / 64; s++) {
+        const int at = ((s * 4 + h) ^ turn) * 16;
+        i4_t a[NT];
+#pragma unroll
+        for (int j = 0; j < NT; j++) {
+          a[j] = *reinterpret_cast<const i4_t*>(buf + (FR + j) * R::kOp + at);
+        }
+#pragma unroll
+        for (int i = 0; i < FR; i++) {
+          const i4_t w = *reinterpret_cast<const i4_t*>(buf + i * R::kOp + at) ^ (int)0x80808080;
+#pragma unroll
+          for (int j = 0; j < NT; j++)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, a[j], acc[i][j], 0, 0, 0);
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read: free for the next load
+      load(d);
+      if (++step == steps) {
+        if (tile < tiles) finish(tile, round);  // the same for all waves
+        step = 0;
+        tile += gridDim.x;
+        round++;
+      }
+    }
+  }
+  lds_loads_left<0>();
+}
+
+template <int NT, bool GATED>
+hipError_t launch_one(const GemmArgs& p, hipStream_t stream) {
+  using R = Ring<NT, GATED>;
+  constexpr int bytes = R::kRing + R::kSums;
+  static_assert(bytes <= 160 * 1024, "LDS of a CU");
+  auto kernel = skinny_kernel<NT, GATED>;
+  hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), bytes);
+  if (e != hipSuccess) return e;
+  const int tiles = (p.N + 15) / 16;
+  // whole rounds of tiles, as even as they can be
+  const int most_groups = device_cu_count();
+  const int rounds = (tiles + most_groups - 1) / most_groups;
+  kernel<<<dim3((unsigned)((tiles + rounds - 1) / rounds)), dim3(R::W * 64), bytes, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <bool GATED>
+hipError_t launch_tokens(const GemmArgs& p, hipStream_t stream) {
+  if (p.T <= 16) return launch_one<1, GATED>(p, stream);
+  if (p.T <= 32) return launch_one<2, GATED>(p, stream);
+  if (p.T <= 48) return launch_one<3, GATED>(p, stream);
+  return launch_one<4, GATED>(p, stream);
+}
+
+}  // namespace
+
+hipError_t launch_skinny(const GemmArgs& p, bool gated, hipStream_t stream) {
+  return gated ? launch_tokens<true>(p, stream) : launch_tokens<false>(p, stream);
+}
+
+}  // namespace lowbit
