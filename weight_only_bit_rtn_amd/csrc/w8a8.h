@@ -139,12 +139,11 @@ struct GemmArgs {
   int T, N, K, act, bf16, x_bf16, tiles_m, tiles_n;
 };
 
-// Products of at most 8 tokens whose codes fit LDS (w8a8_few.hip).  Without
-// p.a the kernel quantizes p.x itself: T K <= kFusedMost.
-constexpr int kFewMostT = 8;
+// Products of one or two tokens (gated: up to four) whose codes fit LDS
+// (w8a8_few.hip).  Without p.a the kernel quantizes p.x itself: T K <= kFusedMost.
 constexpr int kFewMostCodes = 128 * 1024;
 constexpr int kFusedMost = 16384;
-bool few_takes(int64_t T, int64_t K);
+bool few_takes(int64_t T, int64_t K, bool gated);
 hipError_t launch_few(const GemmArgs& p, bool gated, hipStream_t stream);
 
 // Products of at most 64 tokens (w8a8_skinny.hip).

@@ -1,10 +1,10 @@
-// w8a8_few.hip -- the 8-bit products for one to eight tokens: a decoding step.
+// w8a8_few.hip -- the 8-bit products for one to four tokens: a decoding step.
 //
 // Reading the weights is all that takes time (one byte each, used once per
 // token), so each wave reads whole rows as they lie, 1 KiB per instruction,
 // and multiplies with v_dot4_i32_i8; the matrix cores would want 16 rows per
 // instruction, 64 bytes of each, and reading in such pieces ran at 5.0-5.6
-// TB/s where whole rows ran at DOC_RATE TB/s.
+// TB/s where whole rows ran at 6.0 TB/s (1x28672x8192 gated, 79 us; 1x49152x12288, 100 us).
 //
 // One workgroup of 16 waves per CU keeps the tokens' codes in LDS: it
 // quantizes x itself when that is little (T K <= kFusedMost), while its
@@ -124,7 +124,6 @@ template <int TT, int RR, bool GATED, bool FUSED>
 __global__ __launch_bounds__(kWaves * 64) void few_kernel(const GemmArgs p) {
   constexpr int D = kInFlight / RR;
   constexpr int RO = GATED ? RR / 2 : RR;  // output columns per item
-  static_assert(!FUSED || TT <= 8, "tokens per wave");
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   int* meta = reinterpret_cast<int*>(lds);  // scales, sums, scratch: 64 words
   int8_t* codes = reinterpret_cast<int8_t*>(lds + 256);
@@ -154,6 +153,21 @@ __global__ __launch_bounds__(kWaves * 64) void few_kernel(const GemmArgs p) {
       li += stride;
     }
   };
+  // the lane that finishes output (r, t) of an item is lane r TT + t; it has
+  // the row's scale and zero point loaded by then
+  const int fr = lane / TT % RO, ft = lane % TT;
+  const bool finishes = lane < RO * TT && ft < p.T;
+  float sc[2];
+  int z[2];
+  auto load_params = [&](int item) {
+    const int n = min(item * RO + fr, p.N - 1);
+#pragma unroll
+    for (int m = 0; m < (GATED ? 2 : 1); m++) {
+      sc[m] = h_bits_to_f32(p.w[m].scales[n]);
+      z[m] = p.w[m].zeros[n];
+    }
+  };
+  load_params(min(first, items - 1));
 #pragma unroll
   for (int d = 0; d < D; d++) load(w[d]);
   if constexpr (FUSED) {
@@ -172,9 +186,6 @@ __global__ __launch_bounds__(kWaves * 64) void few_kernel(const GemmArgs p) {
     __syncthreads();
   }
 
-  // the lane that finishes output (r, t) of an item is lane r TT + t
-  const int fr = lane / TT % RO, ft = lane % TT;
-  const bool finishes = lane < RO * TT && ft < p.T;
   const float xs = __builtin_bit_cast(float, meta[min(ft, p.T - 1)]);
   const int total = meta[8 + min(ft, p.T - 1)];
   int acc[RR][TT];
@@ -206,13 +217,6 @@ __global__ __launch_bounds__(kWaves * 64) void few_kernel(const GemmArgs p) {
         if (item < items) {
           const int n = item * RO + fr;
           const bool last = finishes && n < p.N;
-          float sc[2];
-          int z[2];
-#pragma unroll
-          for (int m = 0; m < (GATED ? 2 : 1); m++) {
-            sc[m] = last ? h_bits_to_f32(p.w[m].scales[n]) : 0.0f;
-            z[m] = last ? p.w[m].zeros[n] : 0;
-          }
           int mine[2] = {0, 0};
 #pragma unroll
           for (int r = 0; r < RR; r++)
@@ -244,6 +248,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_kernel(const GemmArgs p) {
         }
         step = 0;
         item += stride;
+        load_params(min(item, items - 1));
       }
     }
   }
@@ -271,21 +276,21 @@ hipError_t launch_x(const GemmArgs& p, hipStream_t stream) {
 
 }  // namespace
 
-bool few_takes(int64_t T, int64_t K) {
-  return T <= kFewMostT && T * few_pitch((int)K) <= kFewMostCodes;
+// Up to here whole rows read this way beat the rings of w8a8_skinny.hip, in us:
+// linear 2x11008x4096 14.0 / 14.5, but 4x28672x8192 43.2 / 41.2 and 8x12288x12288
+// 33.6 / 28.3; gated 4x4096x4096 10.1 / 12.0, but 8x28672x8192 95.9 / 89.3.
+bool few_takes(int64_t T, int64_t K, bool gated) {
+  return T <= (gated ? 4 : 2) && T * few_pitch((int)K) <= kFewMostCodes;
 }
 
 hipError_t launch_few(const GemmArgs& p, bool gated, hipStream_t stream) {
   if (gated) {
     if (p.T <= 1) return launch_x<1, 2, true>(p, stream);
     if (p.T <= 2) return launch_x<2, 2, true>(p, stream);
-    if (p.T <= 4) return launch_x<4, 2, true>(p, stream);
-    return launch_x<8, 2, true>(p, stream);
+    return launch_x<4, 2, true>(p, stream);
   }
   if (p.T <= 1) return launch_x<1, 1, false>(p, stream);
-  if (p.T <= 2) return launch_x<2, 1, false>(p, stream);
-  if (p.T <= 4) return launch_x<4, 2, false>(p, stream);
-  return launch_x<8, 2, false>(p, stream);
+  return launch_x<2, 1, false>(p, stream);
 }
 
 }  // namespace lowbit

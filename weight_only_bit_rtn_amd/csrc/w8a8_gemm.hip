@@ -214,8 +214,8 @@ hipError_t launch_tile(GemmArgs p, hipStream_t stream) {
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // Few activations are quantized inside the product's kernel.
-bool fused(int64_t T, int64_t K, int dtype) {
-  return dtype != kI8 && few_takes(T, K) && T * K <= kFusedMost;
+bool fused(int64_t T, int64_t K, int dtype, bool gated) {
+  return dtype != kI8 && few_takes(T, K, gated) && T * K <= kFusedMost;
 }
 
 template <bool GATED>
@@ -227,7 +227,7 @@ hipError_t launch(const Activations& x, int64_t T, const W8& w0, const W8& w1, i
     p.a = static_cast<const int8_t*>(x.x);
     p.xs = x.scales;
     p.xsum = x.sums;
-  } else if (fused(T, K, x.dtype)) {
+  } else if (fused(T, K, x.dtype, GATED)) {
     p.x = static_cast<const uint16_t*>(x.x);
     p.x_bf16 = x.dtype == kBF16;
   } else {
@@ -251,7 +251,7 @@ hipError_t launch(const Activations& x, int64_t T, const W8& w0, const W8& w1, i
   p.K = (int)K;
   p.act = act;
   p.bf16 = out_dtype == kBF16;
-  if (few_takes(T, K)) return launch_few(p, GATED, stream);
+  if (few_takes(T, K, GATED)) return launch_few(p, GATED, stream);
   if (T <= kSkinnyMostT) return launch_skinny(p, GATED, stream);
   if (T <= 512) return launch_tile<128, 128, 2, 2, GATED>(p, stream);
   return launch_tile<256, 256, 2, 4, GATED>(p, stream);
@@ -260,7 +260,7 @@ hipError_t launch(const Activations& x, int64_t T, const W8& w0, const W8& w1, i
 }  // namespace
 
 size_t w8a8_workspace_bytes(int64_t T, int64_t N, int64_t K, int dtype, bool gated) {
-  if (dtype == kI8 || T == 0 || fused(T, K, dtype)) return 0;
+  if (dtype == kI8 || T == 0 || fused(T, K, dtype, gated)) return 0;
   return up256(T * K) + 2 * up256(T * 4);
 }
 

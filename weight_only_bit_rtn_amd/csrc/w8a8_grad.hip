@@ -121,7 +121,8 @@ struct GradArgs {
   const int32_t* e;
   W8 w[2];
   void* dx;
-  int T, N, K, pitch, half_steps, steps, bf16, tiles_m, tiles_n;
+  float* parts;  // [splits][T][K] sums of each share of the steps, when splits > 1
+  int T, N, K, pitch, half_steps, steps, bf16, splits, tiles_m, tiles_n;
 };
 
 // Four code bytes to the exact fp16 integers code - 128: one byte permute
@@ -132,21 +133,35 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, h2_t& lo, h2_t& hi) {
   hi = as_h2(__builtin_amdgcn_perm(0x64646464u, w, 0x04030402u)) - off;
 }
 
-// One workgroup of WM x WN waves: MT tokens by KT columns of dx, steps of 64
-// weight rows through LDS in two buffers, one barrier per step.  The weight
-// tile lies as it does in memory, rows of KT code bytes; the matrix cores
-// need eight rows of one column per lane, which the transposing LDS read
-// delivers (16 lanes read 8 rows of 16 bytes and get a column each).  Chunk c
-// (16 bytes) of a row lies at c ^ (row & 7) in both tiles, so that neither
-// kind of read meets one bank twice.
-template <int MT, int KT, int WM, int WN>
-__global__ __launch_bounds__(WM* WN * 64) void grad_kernel(const GradArgs p) {
+// Where chunk c (16 bytes) of weight row n lies in its row of KT bytes: the 16
+// rows that two quarters of a transposing read touch meet 16 different 16-byte
+// slots of the 256 bytes that the banks span.
+template <int KT>
+__device__ __forceinline__ int slot_of(int n, int c) {
+  if constexpr (KT % 256 == 0) return c ^ (n & 15);
+  if constexpr (KT == 128) return c ^ ((n >> 1) & 7);
+  return (c & ~3) | ((c + (n >> 2)) & 3);  // 64 and 192
+}
+template <int KT>
+__device__ __forceinline__ int chunk_at(int n, int slot) {
+  if constexpr (KT % 256 == 0 || KT == 128) return slot_of<KT>(n, slot);
+  return (slot & ~3) | ((slot - (n >> 2)) & 3);
+}
+
+// One workgroup of WM x WN waves: MT tokens by KT columns of dx over its share
+// of the steps, 64 weight rows each, staged in LDS by direct loads on a ring
+// of NB buffers, one barrier per step.  The weight tile lies as it does in
+// memory, rows of KT code bytes; the matrix cores need eight rows of one
+// column per lane, which the transposing LDS read delivers (16 lanes read 8
+// rows of 16 bytes and get a column each).  A step is two halves of 32 rows:
+// while one half is multiplied, the operands of the next are read.
+template <int MT, int KT, int WM, int WN, int NB>
+__global__ __launch_bounds__(WM* WN * 64, 2) void grad_kernel(const GradArgs p) {
   constexpr int kWaves = WM * WN;
   constexpr int MW = MT / WM, KW = KT / WN;
   constexpr int FM = MW / 16, FK = KW / 16;
   constexpr int kA = MT * kStepN * 2, kW = kStepN * KT, kBuf = kA + kW;
-  constexpr int LA = kA / 1024 / kWaves, LW = kW / 1024 / kWaves;
-  constexpr int kRows = 1024 / KT;  // weight rows per load
+  constexpr int LA = kA / 1024 / kWaves, LW = kW / 1024 / kWaves, kLoads = LA + LW;
   static_assert(LA * 1024 * kWaves == kA && LW * 1024 * kWaves == kW, "whole loads");
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
 
@@ -154,39 +169,43 @@ __global__ __launch_bounds__(WM* WN * 64) void grad_kernel(const GradArgs p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WM, wn = wave / WM;
   const int i16 = lane & 15, h = lane >> 4;
+  const int tiles = p.tiles_m * p.tiles_n;
+  const int split = blockIdx.x / tiles;
   int tm, tn;
-  tile_of(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, tm, tn);
+  tile_of(blockIdx.x % tiles, tiles, p.tiles_m, p.tiles_n, tm, tn);
   const int t0 = tm * MT, k0 = tn * KT;
   const uint32_t K = (uint32_t)p.K;
+  const int s0 = (int)((int64_t)p.steps * split / p.splits);
+  const int s1 = (int)((int64_t)p.steps * (split + 1) / p.splits);
 
   const uint32_t pitch = (uint32_t)p.pitch * 2;
-  const auto ra = buffer_of(p.a + (int64_t)t0 * p.pitch, (uint32_t)min(MT, p.T - t0) * pitch);
+  const i4_t ra = buffer_of(p.a + (int64_t)t0 * p.pitch, (uint32_t)min(MT, p.T - t0) * pitch);
   uint32_t oa[LA], ow[LW];
-  int la[LA], lw[LW], rw[LW];
+  const uint32_t base = lds_address(lds);
 #pragma unroll
-  for (int i = 0; i < LA; i++) {
-    const int row = (wave + i * kWaves) * 8;
-    oa[i] = (uint32_t)(row + (lane >> 3)) * pitch + ((lane & 7) ^ (lane >> 3)) * 16;
-    la[i] = row * kStepN * 2;
-  }
-  constexpr int kLanes = KT / 16;  // lanes per weight row
+  for (int i = 0; i < LA; i++)
+    oa[i] = (uint32_t)((wave + i * kWaves) * 8 + (lane >> 3)) * pitch +
+            ((lane & 7) ^ (lane >> 3)) * 16;
 #pragma unroll
   for (int i = 0; i < LW; i++) {
-    rw[i] = (wave + i * kWaves) * kRows + lane / kLanes;
-    const int c = (lane % kLanes) ^ (rw[i] & 7);
+    const int at = (wave + i * kWaves) * 64 + lane, n = at / (KT / 16);
+    const int k = k0 + chunk_at<KT>(n, at % (KT / 16)) * 16;
     // columns past the end: not stored, so not loaded either
-    ow[i] = k0 + c * 16 < p.K ? (uint32_t)rw[i] * K + k0 + c * 16 : 0x80000000u;
-    lw[i] = kA + (wave + i * kWaves) * 1024;
+    ow[i] = k < p.K ? (uint32_t)n * K + k : 0x80000000u;
   }
-  auto stage = [&](uint32_t buf, int s) {
-#pragma unroll
-    for (int i = 0; i < LA; i++) load_to_lds(ra, buf + la[i], oa[i] + (uint32_t)s * (kStepN * 2));
-    const int m = s >= p.half_steps;
-    const int n = (s - m * p.half_steps) * kStepN;
-    const auto rs = buffer_of(p.w[m].codes + (int64_t)n * K,
-                              (uint32_t)max(0, min(kStepN, p.N - n)) * K);
-#pragma unroll
-    for (int i = 0; i < LW; i++) load_to_lds(rs, buf + lw[i], ow[i]);
+  // load i of step s; past the share's end it brings zeros
+  auto load = [&](int s, int i) {
+    const uint32_t buf = base + (uint32_t)((s - s0) % NB) * kBuf;
+    if (i < LA) {
+      const uint32_t at = s < s1 ? (uint32_t)s * (kStepN * 2) : 0x80000000u;
+      load_to_lds(ra, buf + (wave + i * kWaves) * 1024, oa[i] + at);
+    } else {
+      const int m = s >= p.half_steps;
+      const int n = (s - m * p.half_steps) * kStepN;
+      const int rows = s < s1 ? max(0, min(kStepN, p.N - n)) : 0;
+      const i4_t rs = buffer_of(p.w[m].codes + (int64_t)n * K, (uint32_t)rows * K);
+      load_to_lds(rs, buf + kA + (wave + (i - LA) * kWaves) * 1024, ow[i - LA]);
+    }
   };
 
   f4_t acc[FK][FM];
@@ -195,42 +214,70 @@ __global__ __launch_bounds__(WM* WN * 64) void grad_kernel(const GradArgs p) {
 #pragma unroll
     for (int j = 0; j < FM; j++) acc[i][j] = f4_t{0, 0, 0, 0};
 
-  const uint32_t base = lds_address(lds);
-  if (p.steps > 0) stage(base, 0);
-  for (int s = 0; s < p.steps; s++) {
-    uint8_t* buf = lds + (s & 1) * kBuf;
-    lds_loads_left<0>();  // this step's loads of this wave have landed
-    __syncthreads();   // and everyone's; the other buffer is free
-    if (s + 1 < p.steps) stage(base + ((s + 1) & 1) * kBuf, s + 1);
-    const uint8_t* ba = buf + (wm * MW + i16) * (kStepN * 2);
-    const uint8_t* bw = buf + kA;
+  // operands of a half step: tokens as they lie, codes transposed
+  const int ra0 = (wm * MW + i16) * (kStepN * 2);
+  auto tokens = [&](int s, int ks, int j) {
+    const int at = ((ks * 4 + h) ^ (i16 & 7)) * 16;
+    return *reinterpret_cast<const h8_t*>(lds + (s - s0) % NB * kBuf + ra0 +
+                                          j * 16 * (kStepN * 2) + at);
+  };
+  auto rows = [&](int s, int ks, int i) {
+    // lanes 2r and 2r + 1 of 16 read the two halves of row r's 16 bytes
+    const int n = ks * 32 + h * 8 + (i16 >> 1);
+    const uint8_t* at = lds + (s - s0) % NB * kBuf + kA + n * KT +
+                        slot_of<KT>(n, wn * (KW / 16) + i) * 16 + (i16 & 1) * 8;
+    return __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+        (__attribute__((address_space(3))) i2_t*)at);
+  };
+  auto multiply = [&](const i2_t w, const h8_t(&fa)[FM], int i) {
+    h2_t q[4];
+    codes_to_f16((uint32_t)w[0], q[0], q[1]);
+    codes_to_f16((uint32_t)w[1], q[2], q[3]);
+    const h8_t fw = {q[0][0], q[0][1], q[1][0], q[1][1], q[2][0], q[2][1], q[3][0], q[3][1]};
 #pragma unroll
-    for (int ks = 0; ks < 2; ks++) {
-      h8_t fa[FM], fw[FK];
-      // lanes 2r and 2r + 1 of 16 read the two halves of row r's 16 bytes
-      const int n = ks * 32 + h * 8 + (i16 >> 1);
+    for (int j = 0; j < FM; j++)
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw, fa[j], acc[i][j], 0, 0, 0);
+  };
+  if (s0 < s1) {
+    h8_t f0[FM], f1[FM];
+    i2_t w0[FK], w1[FK];
+#pragma unroll
+    for (int s = 0; s < NB - 1; s++)
+#pragma unroll
+      for (int i = 0; i < kLoads; i++) load(s0 + s, i);
+    lds_loads_left<(NB - 2) * kLoads>();
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < FK; i++) w0[i] = rows(s0, 0, i);
+#pragma unroll
+    for (int j = 0; j < FM; j++) f0[j] = tokens(s0, 0, j);
+    for (int s = s0; s < s1; s++) {
 #pragma unroll
       for (int i = 0; i < FK; i++) {
-        const int c = (wn * KW / 16 + i) ^ (n & 7);
-        const i2_t w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-            (__attribute__((address_space(3))) i2_t*)(bw + n * KT + c * 16 + (i16 & 1) * 8));
-        h2_t q[4];
-        codes_to_f16((uint32_t)w[0], q[0], q[1]);
-        codes_to_f16((uint32_t)w[1], q[2], q[3]);
-        fw[i] = h8_t{q[0][0], q[0][1], q[1][0], q[1][1], q[2][0], q[2][1], q[3][0], q[3][1]};
+#pragma unroll
+        for (int l = i * kLoads / FK; l < (i + 1) * kLoads / FK; l++) load(s + NB - 1, l);
+        w1[i] = rows(s, 1, i);
+#pragma unroll
+        for (int j = i * FM / FK; j < (i + 1) * FM / FK; j++) f1[j] = tokens(s, 1, j);
+        multiply(w0[i], f0, i);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      const int at = ((ks * 4 + h) ^ (i16 & 7)) * 16;
+      lds_loads_left<(NB - 2) * kLoads>();  // this wave's part of the next step has landed
+      __syncthreads();                      // and everyone's; step s has been read
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < FM; j++)
-        fa[j] = *reinterpret_cast<const h8_t*>(ba + j * 16 * (kStepN * 2) + at);
+      for (int i = 0; i < FK; i++) {
+        w0[i] = rows(s + 1, 0, i);
 #pragma unroll
-      for (int i = 0; i < FK; i++)
-#pragma unroll
-        for (int j = 0; j < FM; j++)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[i], fa[j], acc[i][j], 0, 0, 0);
+        for (int j = i * FM / FK; j < (i + 1) * FM / FK; j++) f0[j] = tokens(s + 1, 0, j);
+        multiply(w1[i], f1, i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
+    lds_loads_left<0>();
   }
 
+  // lane l of a fragment holds columns k = 4 (l / 16) + 0..3 of token l % 16
   const bool bf = p.bf16;
 #pragma unroll
   for (int j = 0; j < FM; j++) {
@@ -242,37 +289,86 @@ __global__ __launch_bounds__(WM* WN * 64) void grad_kernel(const GradArgs p) {
     for (int i = 0; i < FK; i++) {
       const int k = k0 + wn * KW + i * 16 + h * 4;
       if (k >= p.K) continue;
-      us4_t out;
+      const int64_t at = (int64_t)t * p.K + k;
+      if (p.splits > 1) {
+        *reinterpret_cast<f4_t*>(p.parts + (int64_t)split * p.T * p.K + at) = acc[i][j];
+      } else {
+        us4_t out;
 #pragma unroll
-      for (int q = 0; q < 4; q++)
-        out[q] = f32_to_elem(__builtin_amdgcn_ldexpf(acc[i][j][q] + r, e), bf);
-      *reinterpret_cast<us4_t*>(static_cast<uint16_t*>(p.dx) + (int64_t)t * p.K + k) = out;
+        for (int q = 0; q < 4; q++)
+          out[q] = f32_to_elem(__builtin_amdgcn_ldexpf(acc[i][j][q] + r, e), bf);
+        *reinterpret_cast<us4_t*>(static_cast<uint16_t*>(p.dx) + at) = out;
+      }
     }
   }
 }
 
-template <int MT, int KT, int WM, int WN>
+// Joins the shares' sums, in their order.
+__global__ __launch_bounds__(256) void grad_join_kernel(const GradArgs p) {
+  const int64_t all = (int64_t)p.T * p.K;
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (at >= all) return;
+  f4_t sum = *reinterpret_cast<const f4_t*>(p.parts + at);
+  for (int z = 1; z < p.splits; z++) sum += *reinterpret_cast<const f4_t*>(p.parts + z * all + at);
+  const int t = (int)(at / p.K);
+  const float r = p.r[t];
+  const int e = -p.e[t];
+  us4_t out;
+#pragma unroll
+  for (int q = 0; q < 4; q++)
+    out[q] = f32_to_elem(__builtin_amdgcn_ldexpf(sum[q] + r, e), p.bf16);
+  *reinterpret_cast<us4_t*>(static_cast<uint16_t*>(p.dx) + at) = out;
+}
+
+template <int MT, int KT, int WM, int WN, int NB>
 hipError_t launch_tile(GradArgs p, hipStream_t stream) {
-  constexpr int bytes = 2 * (MT * kStepN * 2 + kStepN * KT);
-  auto kernel = grad_kernel<MT, KT, WM, WN>;
+  constexpr int bytes = NB * (MT * kStepN * 2 + kStepN * KT);
+  auto kernel = grad_kernel<MT, KT, WM, WN, NB>;
   hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), bytes);
   if (e != hipSuccess) return e;
   p.tiles_m = (p.T + MT - 1) / MT;
   p.tiles_n = (p.K + KT - 1) / KT;
-  const int64_t total = (int64_t)p.tiles_m * p.tiles_n;
+  const int64_t total = (int64_t)p.tiles_m * p.tiles_n * p.splits;
   if (total > INT32_MAX) return hipErrorInvalidValue;
   kernel<<<dim3((unsigned)total), dim3(WM * WN * 64), bytes, stream>>>(p);
+  e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  const int64_t quads = (int64_t)p.T * p.K / 4;
+  grad_join_kernel<<<dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream>>>(p);
   return hipGetLastError();
 }
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 int64_t padded(int64_t N) { return (N + kStepN - 1) / kStepN * kStepN; }
 
+// Token rows and columns of a tile for T tokens.
+void tile_shape(int64_t T, int& mt, int& kt) {
+  mt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 512 ? 128 : 256;
+  kt = mt == 256 ? 256 : 128;
+}
+
+// How many shares the steps of each tile are cut into: with few tiles, as
+// many as give each CU two workgroups, at least 8 steps each.  The shares'
+// sums are written and read again, so large problems, which have tiles
+// enough, are not split.
+int split_count(int64_t T, int64_t K, int64_t steps) {
+  int mt, kt;
+  tile_shape(T, mt, kt);
+  if (mt == 256) return 1;
+  const int64_t tiles = ((T + mt - 1) / mt) * ((K + kt - 1) / kt);
+  const int64_t want = 512 / tiles, most = steps / 8;
+  const int64_t z = want < most ? want : most;
+  return (int)(z < 1 ? 1 : z > 16 ? 16 : z);
+}
+
 }  // namespace
 
 size_t w8a8_grad_workspace_bytes(int64_t T, int64_t N, int64_t K, bool gated) {
   if (T == 0) return 0;
-  return up256((size_t)T * padded(N) * (gated ? 4 : 2)) + 2 * up256((size_t)T * 4);
+  const int64_t pitch = padded(N) * (gated ? 2 : 1);
+  const int splits = split_count(T, K, pitch / kStepN);
+  return up256((size_t)T * pitch * 2) + 2 * up256((size_t)T * 4) +
+         (splits > 1 ? (size_t)splits * T * K * 4 : 0);
 }
 
 hipError_t launch_w8a8_grad(const void* dh, const void* gate, const void* up, int dtype, int64_t T,
@@ -319,9 +415,15 @@ hipError_t launch_w8a8_grad(const void* dh, const void* gate, const void* up, in
   p.half_steps = (int)(half / kStepN);
   p.steps = (int)(pitch / kStepN);
   p.bf16 = q.bf16;
-  if (T <= 64) return launch_tile<64, 128, 2, 2>(p, stream);
-  if (T <= 512) return launch_tile<128, 128, 2, 2>(p, stream);
-  return launch_tile<256, 256, 2, 4>(p, stream);
+  p.splits = split_count(T, K, p.steps);
+  p.parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(q.e) + up256((size_t)T * 4));
+  int mt, kt;
+  tile_shape(T, mt, kt);
+  if (mt == 16) return launch_tile<16, 128, 1, 2, 4>(p, stream);
+  if (mt == 32) return launch_tile<32, 128, 1, 4, 4>(p, stream);
+  if (mt == 64) return launch_tile<64, 128, 1, 4, 4>(p, stream);
+  if (mt == 128) return launch_tile<128, 128, 2, 2, 3>(p, stream);
+  return launch_tile<256, 256, 2, 4, 3>(p, stream);
 }
 
 }  // namespace lowbit

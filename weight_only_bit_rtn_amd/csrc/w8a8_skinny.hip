@@ -21,7 +21,7 @@ struct Ring {
   static constexpr int OPS = FR + NT;  // 16-row operands per step
   static constexpr int W = 4;
   static constexpr int CH = OPS <= 4 ? 256 : 128;
-  static constexpr int D = OPS == 2 ? 4 : 2;
+  static constexpr int D = OPS == 2 ? 4 : OPS == 3 || OPS == 5 ? 3 : 2;
   static constexpr int kOp = 16 * CH;                // bytes of an operand
   static constexpr int kRing = W * D * OPS * kOp;
   static constexpr int kSums = W * FR * NT * 1024;
