@@ -54,7 +54,93 @@ __device__ __forceinline__ float block_max(float v, float* red, int tid) {
   return v;
 }
 
-// One workgroup per token.
+// One workgroup per token, N in whole chunks of 8 (16 bytes): the token's
+// factors stay in registers (NC chunks per thread) between their largest and
+// their rounding, so the inputs are read once.  Bound by HBM; each row's scales
+// and zero points come from L2.
+template <bool GATED, int NC>
+__global__ __launch_bounds__(1024) void grad_prep_chunks_kernel(const PrepArgs p) {
+  __shared__ float red[16];
+  const int tid = threadIdx.x, nt = blockDim.x, chunks = p.N / 8;
+  const int64_t row = blockIdx.x;
+  const bool bf = p.bf16;
+  constexpr int M = GATED ? 2 : 1;
+  auto in = [&](const uint16_t* base, int c) {
+    return reinterpret_cast<const us8_t*>(base + row * p.N)[c];
+  };
+  float a[NC][M][8];
+  float top = 0;
+  bool finite = true;
+#pragma unroll
+  for (int i = 0; i < NC; i++) {
+    const int c = tid + i * nt;
+#pragma unroll
+    for (int m = 0; m < M; m++)
+#pragma unroll
+      for (int j = 0; j < 8; j++) a[i][m][j] = 0;
+    if (c >= chunks) continue;
+    const us8_t d = in(p.d, c);
+    us8_t g, u, og, ou;
+    if constexpr (GATED) {
+      g = in(p.gate, c);
+      u = in(p.up, c);
+    }
+    us8_t sc[M];
+#pragma unroll
+    for (int m = 0; m < M; m++) sc[m] = reinterpret_cast<const us8_t*>(p.w[m].scales)[c];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      float d0 = elem_to_f32(d[j], bf), d1 = 0;
+      if constexpr (GATED) {
+        float f, df;
+        act_value_slope(elem_to_f32(g[j], bf), p.act, f, df);
+        d1 = d0 * f;
+        d0 = d0 * elem_to_f32(u[j], bf) * df;
+        og[j] = f32_to_elem(d0, bf);
+        ou[j] = f32_to_elem(d1, bf);
+        a[i][M - 1][j] = d1 * h_bits_to_f32(sc[M - 1][j]);
+      }
+      a[i][0][j] = d0 * h_bits_to_f32(sc[0][j]);
+      finite = finite && fabsf(d0) < INFINITY && fabsf(d1) < INFINITY;
+#pragma unroll
+      for (int m = 0; m < M; m++) top = fmaxf(top, fabsf(a[i][m][j]));
+    }
+    if (GATED && p.dgate) {
+      reinterpret_cast<us8_t*>(p.dgate + row * p.N)[c] = og;
+      reinterpret_cast<us8_t*>(p.dup + row * p.N)[c] = ou;
+    }
+  }
+  top = block_max(finite ? top : INFINITY, red, tid);
+  const bool ok = top < INFINITY;
+  const int e = ok && top > 0 ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
+  float r = 0;
+#pragma unroll
+  for (int i = 0; i < NC; i++) {
+    const int c = tid + i * nt;
+    if (c >= p.half / 8) continue;
+#pragma unroll
+    for (int m = 0; m < M; m++) {
+      us8_t out = {};
+      if (ok && c < chunks) {
+        const i4_t* zp = reinterpret_cast<const i4_t*>(p.w[m].zeros) + c * 2;
+        const i4_t z[2] = {zp[0], zp[1]};
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          out[j] = f32_to_h_bits(__builtin_amdgcn_ldexpf(a[i][m][j], e));
+          r += h_bits_to_f32(out[j]) * (float)(128 - z[j / 4][j % 4]);
+        }
+      }
+      reinterpret_cast<us8_t*>(p.a + row * p.pitch + m * p.half)[c] = out;
+    }
+  }
+  r = block_sum(r, red, tid);
+  if (tid == 0) {
+    p.r[row] = ok ? r : __builtin_nanf("");
+    p.e[row] = e;
+  }
+}
+
+// The same for any N, value by value, the inputs read twice.
 template <bool GATED>
 __global__ __launch_bounds__(1024) void grad_prep_kernel(const PrepArgs p) {
   __shared__ float red[16];
@@ -338,6 +424,23 @@ hipError_t launch_tile(GradArgs p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <bool GATED>
+void launch_prep(const PrepArgs& q, int64_t T, hipStream_t stream) {
+  const dim3 grid((unsigned)T);
+  const int chunks = q.half / 8;
+  int nt = 64;
+  while (nt < 1024 && nt < chunks) nt *= 2;
+  const bool whole = q.N % 8 == 0;
+  if (whole && chunks <= nt)
+    grad_prep_chunks_kernel<GATED, 1><<<grid, dim3(nt), 0, stream>>>(q);
+  else if (whole && chunks <= 2 * nt)
+    grad_prep_chunks_kernel<GATED, 2><<<grid, dim3(nt), 0, stream>>>(q);
+  else if (whole && chunks <= 4 * nt)
+    grad_prep_chunks_kernel<GATED, 4><<<grid, dim3(nt), 0, stream>>>(q);
+  else
+    grad_prep_kernel<GATED><<<grid, dim3(nt), 0, stream>>>(q);
+}
+
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 int64_t padded(int64_t N) { return (N + kStepN - 1) / kStepN * kStepN; }
 
@@ -393,12 +496,10 @@ hipError_t launch_w8a8_grad(const void* dh, const void* gate, const void* up, in
   q.half = (int)half;
   q.act = act;
   q.bf16 = dtype == kBF16;
-  int nt = 64;
-  while (nt < 1024 && nt * 8 < N) nt *= 2;
   if (gated)
-    grad_prep_kernel<true><<<dim3((unsigned)T), dim3(nt), 0, stream>>>(q);
+    launch_prep<true>(q, T, stream);
   else
-    grad_prep_kernel<false><<<dim3((unsigned)T), dim3(nt), 0, stream>>>(q);
+    launch_prep<false>(q, T, stream);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   GradArgs p{};
