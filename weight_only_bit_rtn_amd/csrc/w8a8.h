@@ -94,11 +94,11 @@ __device__ __forceinline__ void lds_loads_left() {
 // Workgroup id -> tile: ids go round the 8 chiplets one by one, so give each
 // chiplet (its own L2) a contiguous run of tiles, and walk the runs in bands
 // of 8 token tiles by all weight tiles, so that the tiles in flight on one
-// chiplet share few rows of both operands.
+// chiplet share few rows of both operands.  Ids from `total` on are tiles as they come.
 __device__ __forceinline__ void tile_of(int id, int total, int tiles_m, int tiles_n, int& tm,
                                         int& tn) {
   const int q = total / 8, r = total % 8, xcd = id % 8, at = id / 8;
-  const int t = xcd * q + min(xcd, r) + at;
+  const int t = id < total ? xcd * q + min(xcd, r) + at : id;
   constexpr int kBand = 8;
   const int band = t / (kBand * tiles_n), in = t % (kBand * tiles_n);
   const int rows = min(kBand, tiles_m - band * kBand);
@@ -136,8 +136,99 @@ struct GemmArgs {
   void* y;
   void* g;
   void* u;
-  int T, N, K, act, bf16, x_bf16, tiles_m, tiles_n;
+  int T, N, K, act, bf16, x_bf16;
 };
+
+// Scales and 128 - zero points of four output columns n..n + 3.
+template <bool GATED>
+struct Columns {
+  float sc[GATED ? 2 : 1][4];
+  int zc[GATED ? 2 : 1][4];
+  bool small;
+  __device__ __forceinline__ Columns(const GemmArgs& p, int n) : small(p.K <= 65536) {
+#pragma unroll
+    for (int m = 0; m < (GATED ? 2 : 1); m++)
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        const int nn = min(n + r, p.N - 1);
+        sc[m][r] = h_bits_to_f32(p.w[m].scales[nn]);
+        const int z = p.w[m].zeros[nn];
+        zc[m][r] = 128 - z;
+        small = small && (uint32_t)z < 256u;
+      }
+  }
+};
+
+// The outputs of token t at columns n..n + 3 (n % 4 == 0) from their integer
+// sums a0 (gated: the gate's, and a1 the up's); xs and total are the token's
+// scale and the sum of its codes.
+template <bool GATED>
+__device__ __forceinline__ void store4(const GemmArgs& p, const Columns<GATED>& c, i4_t a0, i4_t a1,
+                                       int n, int t, float xs, int total) {
+  us4_t out, og, ou;
+#pragma unroll
+  for (int r = 0; r < 4; r++) {
+    const float v = exact_sum(a0[r], c.zc[0][r], total, c.small) * (xs * c.sc[0][r]);
+    if constexpr (GATED) {
+      const float u = exact_sum(a1[r], c.zc[1][r], total, c.small) * (xs * c.sc[1][r]);
+      out[r] = f32_to_elem(act_value(v, p.act) * u, p.bf16);
+      og[r] = f32_to_elem(v, p.bf16);
+      ou[r] = f32_to_elem(u, p.bf16);
+    } else {
+      out[r] = f32_to_elem(v, p.bf16);
+    }
+  }
+  const int64_t at = (int64_t)t * p.N + n;
+  auto put = [&](void* base, us4_t v) {
+    uint16_t* d = static_cast<uint16_t*>(base) + at;
+    if (p.N % 4 == 0) {
+      *reinterpret_cast<us4_t*>(d) = v;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; r++)
+        if (n + r < p.N) d[r] = v[r];
+    }
+  };
+  put(p.y, out);
+  if (GATED && p.g) {
+    put(p.g, og);
+    put(p.u, ou);
+  }
+}
+
+// Tiles of a product over `slots` workgroups at a time: `whole` of them are
+// computed by one workgroup each, and each of the `rest`, which would leave
+// most slots idle, by `splits` workgroups that share its steps and leave
+// their sums in the workspace for a second kernel to join.
+struct TilePlan {
+  int tiles_m, tiles_n, whole, rest, splits;
+  int blocks() const { return whole + rest * splits; }
+};
+// A tile's steps take about `step_us` each; a join costs about 5 us and the
+// partial sums (`tile_bytes` for each share) are written and read again.
+inline TilePlan plan_tiles(int64_t tm, int64_t tn, int slots, int steps, double step_us,
+                           double tile_bytes, double* us) {
+  TilePlan best{(int)tm, (int)tn, (int)(tm * tn), 0, 1};
+  const int64_t tiles = tm * tn, rounds = (tiles + slots - 1) / slots;
+  double least = rounds * steps * step_us;
+  const int64_t whole = tiles / slots * slots, rest = tiles - whole;
+  if (rest > 0) {
+    int64_t z = slots / rest < steps / 8 ? slots / rest : steps / 8;
+    z = z < 16 ? z : 16;
+    if (z > 1) {
+      const double t = ((rounds - 1) * steps + (steps + z - 1) / z) * step_us + 5.0 +
+                       (double)rest * z * tile_bytes * 2 / 4e6;
+      if (t < least) {
+        best.whole = (int)whole;
+        best.rest = (int)rest;
+        best.splits = (int)z;
+        least = t;
+      }
+    }
+  }
+  *us = least;
+  return best;
+}
 
 // Products of one or two tokens (gated: up to four) whose codes fit LDS
 // (w8a8_few.hip).  Without p.a the kernel quantizes p.x itself: T K <= kFusedMost.

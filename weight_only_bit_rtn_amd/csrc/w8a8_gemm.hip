@@ -9,6 +9,10 @@
 // covered and every integer sum is exact.
 #include "w8a8.h"
 
+#ifndef SMALL_US
+#define SMALL_US 0.65
+#define LARGE_US 0.95
+#endif
 namespace lowbit {
 namespace {
 
@@ -24,7 +28,8 @@ constexpr int kBuffers = 4;  // LDS buffers of one step each
 // read spread over all banks.  Values past the row's end, tokens past T and
 // rows past N come as zeros from the buffers' range check.
 template <int MT, int NT, int WM, int WN, bool GATED>
-__global__ __launch_bounds__(WM* WN * 64) void w8a8_kernel(const GemmArgs p) {
+__global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, const TilePlan plan,
+                                                                 i4_t* __restrict__ parts) {
   constexpr int kWaves = WM * WN;
   constexpr int MW = MT / WM, NW = NT / WN;  // wave tile
   constexpr int FM = MW / 16, FN = NW / 16;  // its fragments
@@ -40,8 +45,15 @@ __global__ __launch_bounds__(WM* WN * 64) void w8a8_kernel(const GemmArgs p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WM, wn = wave / WM;
   const int i16 = lane & 15, h = lane >> 4;
+  const int steps = (p.K + kStep - 1) / kStep;
+  // a whole tile, or a share of the steps of one of the rest
+  const int over = (int)blockIdx.x - plan.whole;
+  const int split = over < 0 ? 0 : over % plan.splits;
+  const int s0 = over < 0 ? 0 : (int)((int64_t)steps * split / plan.splits);
+  const int s1 = over < 0 ? steps : (int)((int64_t)steps * (split + 1) / plan.splits);
   int tm, tn;
-  tile_of(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, tm, tn);
+  tile_of(over < 0 ? (int)blockIdx.x : plan.whole + over / plan.splits, plan.whole,
+          plan.tiles_m, plan.tiles_n, tm, tn);
   const int t0 = tm * MT, n0 = tn * NO;
   const uint32_t K = (uint32_t)p.K;
 
@@ -55,6 +67,7 @@ __global__ __launch_bounds__(WM* WN * 64) void w8a8_kernel(const GemmArgs p) {
   uint32_t oa[LA], ob[LB];
   uint32_t la[LA], lb[LB];
   const uint32_t base = lds_address(lds);
+  const uint32_t kend = min((uint32_t)s1 * kStep, K);
 #pragma unroll
   for (int i = 0; i < LA; i++) {
     const int row = (wave + i * kWaves) * 16;
@@ -69,10 +82,10 @@ __global__ __launch_bounds__(WM* WN * 64) void w8a8_kernel(const GemmArgs p) {
     const int slot = GATED ? row / (NW / 2) * NW + row % (NW / 2) + (i >= LB / 2 ? NW / 2 : 0) : row;
     lb[i] = base + (MT + slot) * kStep;
   }
-  // load i of the LA + LB of step s; past the last step it brings zeros
+  // load i of the LA + LB of step s; past the share's last step it brings zeros
   auto load = [&](int s, int i) {
     const uint32_t k0 = (uint32_t)s * kStep, buf = (uint32_t)(s % kBuffers) * kBuf;
-    const uint32_t add = k0 + chunk < K ? k0 : 0x80000000u;
+    const uint32_t add = k0 + chunk < kend ? k0 : 0x80000000u;
     if (i < LA)
       load_to_lds(ra, la[i] + buf, oa[i] + add);
     else
@@ -116,102 +129,116 @@ __global__ __launch_bounds__(WM* WN * 64) void w8a8_kernel(const GemmArgs p) {
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  const int steps = (p.K + kStep - 1) / kStep;
   i4_t f0[FM], f1[FM];
 #pragma unroll
   for (int s = 0; s < kBuffers - 1; s++)
 #pragma unroll
-    for (int i = 0; i < kLoads; i++) load(s, i);
+    for (int i = 0; i < kLoads; i++) load(s0 + s, i);
   lds_loads_left<(kBuffers - 2) * kLoads>();
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < FM; j++) f0[j] = tokens(0, j);
+  for (int j = 0; j < FM; j++) f0[j] = tokens(s0, j);
 #pragma unroll
-  for (int i = 0; i < kAhead; i++) fb[i] = rows(0, i);
-  for (int s = 0; s < steps; s += 2) {
+  for (int i = 0; i < kAhead; i++) fb[i] = rows(s0, i);
+  for (int s = s0; s < s1; s += 2) {
     step(s, f0, f1);
     step(s + 1, f1, f0);  // past the end: zeros
   }
   lds_loads_left<0>();
 
+  if (over >= 0) {
+    i4_t* to = parts + ((int64_t)over * kWaves + wave) * (FN * FM * 64) + lane;
+#pragma unroll
+    for (int i = 0; i < FN; i++)
+#pragma unroll
+      for (int j = 0; j < FM; j++) to[(i * FM + j) * 64] = acc[i][j];
+    return;
+  }
   // lane l of a fragment holds outputs n = 4 (l / 16) + 0..3 of token l % 16
-  const bool bf = p.bf16;
-  const bool vec = p.N % 4 == 0;
   constexpr int FO = GATED ? FN / 2 : FN;
   const int nb = n0 + wn * (GATED ? NW / 2 : NW);
 #pragma unroll
   for (int i = 0; i < FO; i++) {
     const int n = nb + i * 16 + h * 4;
     if (n >= p.N) continue;
-    float sc[2][4];
-    int zc[2][4];
-    bool small = p.K <= 65536;
-#pragma unroll
-    for (int m = 0; m < (GATED ? 2 : 1); m++)
-#pragma unroll
-      for (int r = 0; r < 4; r++) {
-        const int nn = min(n + r, p.N - 1);
-        sc[m][r] = h_bits_to_f32(p.w[m].scales[nn]);
-        const int z = p.w[m].zeros[nn];
-        zc[m][r] = 128 - z;
-        small = small && (uint32_t)z < 256u;
-      }
+    const Columns<GATED> c(p, n);
 #pragma unroll
     for (int j = 0; j < FM; j++) {
       const int t = t0 + wm * MW + j * 16 + i16;
       if (t >= p.T) continue;
-      const float xs = p.xs[t];
-      const int total = p.xsum[t];
-      us4_t out, og, ou;
-#pragma unroll
-      for (int r = 0; r < 4; r++) {
-        const float v = exact_sum(acc[i][j][r], zc[0][r], total, small) * (xs * sc[0][r]);
-        if constexpr (GATED) {
-          const float u =
-              exact_sum(acc[i + FO][j][r], zc[1][r], total, small) * (xs * sc[1][r]);
-          out[r] = f32_to_elem(act_value(v, p.act) * u, bf);
-          og[r] = f32_to_elem(v, bf);
-          ou[r] = f32_to_elem(u, bf);
-        } else {
-          out[r] = f32_to_elem(v, bf);
-        }
-      }
-      const int64_t at = (int64_t)t * p.N + n;
-      auto put = [&](void* base, us4_t v) {
-        uint16_t* d = static_cast<uint16_t*>(base) + at;
-        if (vec) {
-          *reinterpret_cast<us4_t*>(d) = v;
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; r++)
-            if (n + r < p.N) d[r] = v[r];
-        }
-      };
-      put(p.y, out);
-      if (GATED && p.g) {
-        put(p.g, og);
-        put(p.u, ou);
-      }
+      store4<GATED>(p, c, acc[i][j], acc[FN - FO + i][j], n, t, p.xs[t], p.xsum[t]);
     }
   }
 }
 
+// Joins the shares of the plan's rest: one wave for each fragment of a tile.
 template <int MT, int NT, int WM, int WN, bool GATED>
-hipError_t launch_tile(GemmArgs p, hipStream_t stream) {
-  constexpr int NO = GATED ? NT / 2 : NT;
+__global__ __launch_bounds__(256) void w8a8_join_kernel(const GemmArgs p, const TilePlan plan,
+                                                        const i4_t* __restrict__ parts) {
+  constexpr int kWaves = WM * WN;
+  constexpr int MW = MT / WM, NW = NT / WN, FM = MW / 16, FN = NW / 16;
+  constexpr int NO = GATED ? NT / 2 : NT, FO = GATED ? FN / 2 : FN;
+  constexpr int kFragments = kWaves * FO * FM;
+  const int lane = threadIdx.x & 63;
+  const int at = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int tile = at / kFragments, f = at % kFragments;
+  if (tile >= plan.rest) return;
+  const int wave = f / (FO * FM), i = f / FM % FO, j = f % FM;
+  int tm, tn;
+  tile_of(plan.whole + tile, plan.whole, plan.tiles_m, plan.tiles_n, tm, tn);
+  const int n = tn * NO + wave / WM * (GATED ? NW / 2 : NW) + i * 16 + (lane >> 4) * 4;
+  const int t = tm * MT + wave % WM * MW + j * 16 + (lane & 15);
+  if (n >= p.N || t >= p.T) return;
+  i4_t sum[2] = {i4_t{0, 0, 0, 0}, i4_t{0, 0, 0, 0}};
+  for (int z = 0; z < plan.splits; z++) {
+    const i4_t* from =
+        parts + ((int64_t)(tile * plan.splits + z) * kWaves + wave) * (FN * FM * 64) + lane;
+    sum[0] += from[(i * FM + j) * 64];
+    if constexpr (GATED) sum[1] += from[((FO + i) * FM + j) * 64];
+  }
+  store4<GATED>(p, Columns<GATED>(p, n), sum[0], sum[1], n, t, p.xs[t], p.xsum[t]);
+}
+
+template <int MT, int NT, int WM, int WN, bool GATED>
+hipError_t launch_tile(const GemmArgs& p, const TilePlan& plan, i4_t* parts, hipStream_t stream) {
   constexpr int bytes = kBuffers * (MT + NT) * kStep;
   auto kernel = w8a8_kernel<MT, NT, WM, WN, GATED>;
   hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), bytes);
   if (e != hipSuccess) return e;
-  p.tiles_m = (p.T + MT - 1) / MT;
-  p.tiles_n = (p.N + NO - 1) / NO;
-  const int64_t total = (int64_t)p.tiles_m * p.tiles_n;
-  if (total > INT32_MAX) return hipErrorInvalidValue;
-  kernel<<<dim3((unsigned)total), dim3(WM * WN * 64), bytes, stream>>>(p);
+  kernel<<<dim3((unsigned)plan.blocks()), dim3(WM * WN * 64), bytes, stream>>>(p, plan, parts);
+  e = hipGetLastError();
+  if (e != hipSuccess || plan.rest == 0) return e;
+  constexpr int fragments = (MT / 16) * (NT / 16) / (GATED ? 2 : 1);
+  w8a8_join_kernel<MT, NT, WM, WN, GATED>
+      <<<dim3((unsigned)(plan.rest * fragments / 4)), dim3(256), 0, stream>>>(p, plan, parts);
   return hipGetLastError();
 }
 
+// Tiles of 256 x 256 (one workgroup per CU) or 128 x 128 (two), whichever
+// should finish first.
+struct GemmPlan {
+  TilePlan tiles;
+  bool large;
+  size_t part_bytes() const {
+    return (size_t)tiles.rest * tiles.splits * (large ? 256 * 256 : 128 * 128) * 4;
+  }
+};
+GemmPlan gemm_plan(int64_t T, int64_t N, int64_t K, bool gated) {
+  const int cus = device_cu_count(), steps = (int)((K + kStep - 1) / kStep);
+  const int64_t rows = gated ? 2 * N : N;
+  double small_us, large_us;
+  const TilePlan small = plan_tiles((T + 127) / 128, (rows + 127) / 128, 2 * cus, steps, SMALL_US,
+                                    128 * 128 * 4, &small_us);
+  const TilePlan large = plan_tiles((T + 255) / 256, (rows + 255) / 256, cus, steps, LARGE_US,
+                                    256 * 256 * 4, &large_us);
+  if (large_us < small_us) return {large, true};
+  return {small, false};
+}
+
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// Codes, scales and sums of the activations in the workspace.
+size_t code_bytes(int64_t T, int64_t K) { return up256(T * K) + 2 * up256(T * 4); }
 
 // Few activations are quantized inside the product's kernel.
 bool fused(int64_t T, int64_t K, int dtype, bool gated) {
@@ -253,15 +280,19 @@ hipError_t launch(const Activations& x, int64_t T, const W8& w0, const W8& w1, i
   p.bf16 = out_dtype == kBF16;
   if (few_takes(T, K, GATED)) return launch_few(p, GATED, stream);
   if (T <= kSkinnyMostT) return launch_skinny(p, GATED, stream);
-  if (T <= 512) return launch_tile<128, 128, 2, 2, GATED>(p, stream);
-  return launch_tile<256, 256, 2, 4, GATED>(p, stream);
+  const GemmPlan plan = gemm_plan(T, N, K, GATED);
+  auto* parts = reinterpret_cast<i4_t*>(static_cast<uint8_t*>(workspace) +
+                                        (x.dtype == kI8 ? 0 : code_bytes(T, K)));
+  return plan.large ? launch_tile<256, 256, 2, 4, GATED>(p, plan.tiles, parts, stream)
+                    : launch_tile<128, 128, 2, 2, GATED>(p, plan.tiles, parts, stream);
 }
 
 }  // namespace
 
 size_t w8a8_workspace_bytes(int64_t T, int64_t N, int64_t K, int dtype, bool gated) {
-  if (dtype == kI8 || T == 0 || fused(T, K, dtype, gated)) return 0;
-  return up256(T * K) + 2 * up256(T * 4);
+  if (T == 0 || N == 0) return 0;
+  const size_t codes = dtype == kI8 || fused(T, K, dtype, gated) ? 0 : code_bytes(T, K);
+  return codes + (T > kSkinnyMostT ? gemm_plan(T, N, K, gated).part_bytes() : 0);
 }
 
 hipError_t launch_linear_w8a8(const Activations& x, int64_t T, const W8& w, int64_t N, int64_t K,

@@ -88,7 +88,6 @@ __global__ __launch_bounds__((Ring<NT, GATED>::W * 64)) void skinny_kernel(const
       for (int j = 0; j < NT; j++) acc[i][j] = i4_t{0, 0, 0, 0};
   };
   clear();
-  const bool bf = p.bf16, vec = p.N % 4 == 0;
   // joins the waves' sums of a tile; the waves take turns to finish its
   // NR x NT fragments: lane l holds outputs n = 4 (l / 16) + 0..3 of token l % 16
   auto finish = [&](int tile, int round) {
@@ -108,43 +107,7 @@ __global__ __launch_bounds__((Ring<NT, GATED>::W * 64)) void skinny_kernel(const
         sum[0] += sums[(v * FR * NT + o) * 64 + lane];
         if constexpr (GATED) sum[1] += sums[(v * FR * NT + NR * NT + o) * 64 + lane];
       }
-      const float xs = p.xs[t];
-      const int total = p.xsum[t];
-      us4_t out, og, ou;
-#pragma unroll
-      for (int r = 0; r < 4; r++) {
-        const int nn = min(n + r, p.N - 1);
-        float v[2];
-#pragma unroll
-        for (int m = 0; m < (GATED ? 2 : 1); m++) {
-          const int z = p.w[m].zeros[nn];
-          v[m] = exact_sum(sum[m][r], 128 - z, total, p.K <= 65536 && (uint32_t)z < 256u) *
-                 (xs * h_bits_to_f32(p.w[m].scales[nn]));
-        }
-        if constexpr (GATED) {
-          out[r] = f32_to_elem(act_value(v[0], p.act) * v[1], bf);
-          og[r] = f32_to_elem(v[0], bf);
-          ou[r] = f32_to_elem(v[1], bf);
-        } else {
-          out[r] = f32_to_elem(v[0], bf);
-        }
-      }
-      const int64_t at = (int64_t)t * p.N + n;
-      auto put = [&](void* base, us4_t v) {
-        uint16_t* d = static_cast<uint16_t*>(base) + at;
-        if (vec) {
-          *reinterpret_cast<us4_t*>(d) = v;
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; r++)
-            if (n + r < p.N) d[r] = v[r];
-        }
-      };
-      put(p.y, out);
-      if (GATED && p.g) {
-        put(p.g, og);
-        put(p.u, ou);
-      }
+      store4<GATED>(p, Columns<GATED>(p, n), sum[0], sum[1], n, t, p.xs[t], p.xsum[t]);
     }
     clear();
   };
