@@ -91,6 +91,28 @@ __device__ __forceinline__ void lds_loads_left() {
   asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
 }
 
+// Workgroup barrier that waits for nothing but the other waves: not for LDS
+// reads on their way, as __syncthreads() does.
+__device__ __forceinline__ void bare_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// 16 bytes per lane from a range-checked buffer into registers; zeros from
+// outside it.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t checked_buffer(const void* base, uint32_t bytes) {
+  const uint64_t at = reinterpret_cast<uint64_t>(base);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)at);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((uint64_t)hi << 32 | lo),
+                                           (short)0, __builtin_amdgcn_readfirstlane((int)bytes),
+                                           0x00020000);
+}
+__device__ __forceinline__ i4_t load16(__amdgpu_buffer_rsrc_t rs, uint32_t offset) {
+  return __builtin_bit_cast(i4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)offset, 0, 0));
+}
+
 // Workgroup id -> tile: ids go round the 8 chiplets one by one, so give each
 // chiplet (its own L2) a contiguous run of tiles, and walk the runs in bands
 // of 8 token tiles by all weight tiles, so that the tiles in flight on one
@@ -196,37 +218,34 @@ __device__ __forceinline__ void store4(const GemmArgs& p, const Columns<GATED>& 
   }
 }
 
-// Tiles of a product over `slots` workgroups at a time: `whole` of them are
-// computed by one workgroup each, and each of the `rest`, which would leave
-// most slots idle, by `splits` workgroups that share its steps and leave
-// their sums in the workspace for a second kernel to join.
+// Tiles of a product: `whole` of them, as many as fill the CUs some times over,
+// are computed by one workgroup each, and each of the `rest` by `splits`
+// workgroups that share its steps and leave their sums in the workspace for a
+// second kernel to join.
 struct TilePlan {
   int tiles_m, tiles_n, whole, rest, splits;
   int blocks() const { return whole + rest * splits; }
 };
-// A tile's steps take about `step_us` each; a join costs about 5 us and the
-// partial sums (`tile_bytes` for each share) are written and read again.
-inline TilePlan plan_tiles(int64_t tm, int64_t tn, int slots, int steps, double step_us,
+// The plan that should finish first, and when: a CU takes step_us for a step
+// of one of its tiles; a join costs about 7 us, and the partial sums
+// (tile_bytes for each share) are written and read again at about 8 TB/s (they stay in the caches).
+inline TilePlan plan_tiles(int64_t tm, int64_t tn, int cus, int steps, double step_us,
                            double tile_bytes, double* us) {
-  TilePlan best{(int)tm, (int)tn, (int)(tm * tn), 0, 1};
-  const int64_t tiles = tm * tn, rounds = (tiles + slots - 1) / slots;
-  double least = rounds * steps * step_us;
-  const int64_t whole = tiles / slots * slots, rest = tiles - whole;
-  if (rest > 0) {
-    int64_t z = slots / rest < steps / 8 ? slots / rest : steps / 8;
-    z = z < 16 ? z : 16;
-    if (z > 1) {
-      const double t = ((rounds - 1) * steps + (steps + z - 1) / z) * step_us + 5.0 +
-                       (double)rest * z * tile_bytes * 2 / 4e6;
-      if (t < least) {
-        best.whole = (int)whole;
-        best.rest = (int)rest;
-        best.splits = (int)z;
-        least = t;
-      }
+  const int64_t tiles = tm * tn, rest = tiles % cus, whole = tiles - rest;
+  const double before = (double)(whole / cus) * steps * step_us;
+  TilePlan best{(int)tm, (int)tn, (int)tiles, 0, 1};
+  *us = before + (rest > 0 ? steps * step_us : 0.0);
+  for (int z = 2; rest > 0 && z <= 16 && z <= steps / 8; z++) {
+    const int64_t rounds = (rest * z + cus - 1) / cus;
+    const double t = before + (double)(rounds * ((steps + z - 1) / z)) * step_us + 7.0 +
+                     (double)rest * z * tile_bytes * 2 / 8e6;
+    if (t < *us) {
+      best.whole = (int)whole;
+      best.rest = (int)rest;
+      best.splits = z;
+      *us = t;
     }
   }
-  *us = least;
   return best;
 }
 

@@ -21,14 +21,6 @@ constexpr int kWaves = 16;
 constexpr int kChunk = 1024;   // bytes of a row per load
 constexpr int kInFlight = 8;   // loads per lane
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t checked(const void* base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes,
-                                           0x00020000);
-}
-__device__ __forceinline__ i4_t load16(__amdgpu_buffer_rsrc_t rs, uint32_t offset) {
-  return __builtin_bit_cast(i4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)offset, 0, 0));
-}
-
 // Bytes of one token's codes in LDS: whole chunks, zeros behind the last.
 __host__ __device__ constexpr int few_pitch(int K) {
   return (K + kChunk - 1) / kChunk * kChunk;
@@ -143,7 +135,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_kernel(const GemmArgs p) {
 #pragma unroll
     for (int m = 0; m < (GATED ? 2 : 1); m++) {
       const int n = li * RO;
-      const auto rs = checked(p.w[m].codes + (int64_t)n * K,
+      const auto rs = checked_buffer(p.w[m].codes + (int64_t)n * K,
                               (uint32_t)max(0, min(RO, p.N - n)) * K);
 #pragma unroll
       for (int r = 0; r < RO; r++) wd[m * RO + r] = load16(rs, at + r * K);

@@ -9,10 +9,6 @@
 // covered and every integer sum is exact.
 #include "w8a8.h"
 
-#ifndef SMALL_US
-#define SMALL_US 0.65
-#define LARGE_US 0.95
-#endif
 namespace lowbit {
 namespace {
 
@@ -34,10 +30,12 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, 
   constexpr int MW = MT / WM, NW = NT / WN;  // wave tile
   constexpr int FM = MW / 16, FN = NW / 16;  // its fragments
   constexpr int NO = GATED ? NT / 2 : NT;    // output columns of a tile
-  constexpr int LA = MT / 16 / kWaves, LB = NT / 16 / kWaves;  // 1 KiB loads per wave and step
-  constexpr int kLoads = LA + LB;
-  static_assert(LA * 16 * kWaves == MT && LB * 16 * kWaves == NT, "whole loads");
-  static_assert(!GATED || (FN % 2 == 0 && LB % 2 == 0), "gate and up halves");
+  // 1 KiB loads per wave and step; where the rows do not come out even, the
+  // last go to a place of their own, so that every wave counts as many
+  constexpr int kA = MT / 16, kB = NT / 16;
+  constexpr int LA = kA / kWaves, LB = (kB + kWaves - 1) / kWaves, kLoads = LA + LB;
+  static_assert(LA * kWaves == kA && MT % (16 * WM) == 0 && NT % (16 * WN) == 0, "whole loads");
+  static_assert(!GATED || FN % 2 == 0, "gate and up halves");
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   constexpr int kBuf = (MT + NT) * kStep;
 
@@ -74,13 +72,17 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, 
     oa[i] = (row + r16) * K + chunk;
     la[i] = base + row * kStep;
   }
+  bool up[LB], spare[LB];
 #pragma unroll
   for (int i = 0; i < LB; i++) {
-    // gated: the first half of the loads is the gate matrix
-    const int row = (wave + (GATED ? i % (LB / 2) : i) * kWaves) * 16;
-    ob[i] = (row + r16) * K + chunk;
-    const int slot = GATED ? row / (NW / 2) * NW + row % (NW / 2) + (i >= LB / 2 ? NW / 2 : 0) : row;
-    lb[i] = base + (MT + slot) * kStep;
+    // LDS rows of the weight tile, in order; of each wave's NW rows the first
+    // half is gate rows, the second up rows
+    const int slot = (wave + i * kWaves) * 16, in = slot % NW;
+    up[i] = GATED && in >= NW / 2;
+    spare[i] = kB % kWaves != 0 && slot >= NT;
+    const int row = GATED ? slot / NW * (NW / 2) + in % (NW / 2) : slot;
+    ob[i] = spare[i] ? 0x80000000u : (row + r16) * K + chunk;
+    lb[i] = base + (spare[i] ? kBuffers * kBuf : (MT + slot) * kStep);
   }
   // load i of the LA + LB of step s; past the share's last step it brings zeros
   auto load = [&](int s, int i) {
@@ -89,7 +91,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, 
     if (i < LA)
       load_to_lds(ra, la[i] + buf, oa[i] + add);
     else
-      load_to_lds(GATED && i - LA >= LB / 2 ? ru : rg, lb[i - LA] + buf, ob[i - LA] + add);
+      load_to_lds(up[i - LA] ? ru : rg, lb[i - LA] + (spare[i - LA] ? 0 : buf),
+                  spare[i - LA] ? ob[i - LA] : ob[i - LA] + add);
   };
 
   i4_t acc[FN][FM];
@@ -201,7 +204,7 @@ __global__ __launch_bounds__(256) void w8a8_join_kernel(const GemmArgs p, const 
 
 template <int MT, int NT, int WM, int WN, bool GATED>
 hipError_t launch_tile(const GemmArgs& p, const TilePlan& plan, i4_t* parts, hipStream_t stream) {
-  constexpr int bytes = kBuffers * (MT + NT) * kStep;
+  constexpr int bytes = kBuffers * (MT + NT) * kStep + (NT / 16 % (WM * WN) ? 1024 : 0);
   auto kernel = w8a8_kernel<MT, NT, WM, WN, GATED>;
   hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), bytes);
   if (e != hipSuccess) return e;
@@ -214,25 +217,40 @@ hipError_t launch_tile(const GemmArgs& p, const TilePlan& plan, i4_t* parts, hip
   return hipGetLastError();
 }
 
-// Tiles of 256 x 256 (one workgroup per CU) or 128 x 128 (two), whichever
-// should finish first.
+// Tile shapes: tokens, weight rows, and what a step of 64 k of one tile takes
+// of a CU's time (us, measured; two workgroups of the first share a CU at twice
+// that).
+struct TileShape {
+  int mt, nt;
+  double step_us;
+};
+constexpr TileShape kShapes[] = {{128, 128, 0.40}, {256, 256, 1.03}, {256, 192, 0.90}};
+
+// The shape that should finish first.
 struct GemmPlan {
   TilePlan tiles;
-  bool large;
+  int shape;
   size_t part_bytes() const {
-    return (size_t)tiles.rest * tiles.splits * (large ? 256 * 256 : 128 * 128) * 4;
+    return (size_t)tiles.rest * tiles.splits * kShapes[shape].mt * kShapes[shape].nt * 4;
   }
 };
 GemmPlan gemm_plan(int64_t T, int64_t N, int64_t K, bool gated) {
   const int cus = device_cu_count(), steps = (int)((K + kStep - 1) / kStep);
   const int64_t rows = gated ? 2 * N : N;
-  double small_us, large_us;
-  const TilePlan small = plan_tiles((T + 127) / 128, (rows + 127) / 128, 2 * cus, steps, SMALL_US,
-                                    128 * 128 * 4, &small_us);
-  const TilePlan large = plan_tiles((T + 255) / 256, (rows + 255) / 256, cus, steps, LARGE_US,
-                                    256 * 256 * 4, &large_us);
-  if (large_us < small_us) return {large, true};
-  return {small, false};
+  GemmPlan best{};
+  double least = 0;
+  for (int i = 0; i < 3; i++) {
+    const TileShape& t = kShapes[i];
+    double us;
+    const TilePlan plan =
+        plan_tiles((T + t.mt - 1) / t.mt, (rows + t.nt - 1) / t.nt, cus, steps, t.step_us,
+                   (double)t.mt * t.nt * 4, &us);
+    if (i == 0 || us < least) {
+      best = {plan, i};
+      least = us;
+    }
+  }
+  return best;
 }
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -283,8 +301,9 @@ hipError_t launch(const Activations& x, int64_t T, const W8& w0, const W8& w1, i
   const GemmPlan plan = gemm_plan(T, N, K, GATED);
   auto* parts = reinterpret_cast<i4_t*>(static_cast<uint8_t*>(workspace) +
                                         (x.dtype == kI8 ? 0 : code_bytes(T, K)));
-  return plan.large ? launch_tile<256, 256, 2, 4, GATED>(p, plan.tiles, parts, stream)
-                    : launch_tile<128, 128, 2, 2, GATED>(p, plan.tiles, parts, stream);
+  if (plan.shape == 0) return launch_tile<128, 128, 2, 2, GATED>(p, plan.tiles, parts, stream);
+  if (plan.shape == 1) return launch_tile<256, 256, 2, 4, GATED>(p, plan.tiles, parts, stream);
+  return launch_tile<256, 192, 4, 2, GATED>(p, plan.tiles, parts, stream);
 }
 
 }  // namespace
