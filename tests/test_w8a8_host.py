@@ -45,7 +45,8 @@ def test_header_library_and_binding_agree(lw):
             "gelu_tanh": int(consts["LOWBIT_ACT_GELU_TANH"])} == w8a8.ACTIVATIONS
 
 
-# Addresses that are never dereferenced: each call is refused, or empty.
+# Addresses that are never dereferenced: each call is refused, or empty.  (100 tokens: the products then need a
+# workspace.)
 P = 0x7F0000000000
 MIS = P + 2
 BIG = 1 << 40
@@ -55,12 +56,12 @@ def quant(lw, x=P, dtype=0, T=4, K=64, codes=P, scales=P, sums=P):
     return lw.quantize_act_raw(x, dtype, T, K, codes, scales, sums, None)
 
 
-def linear(lw, x=P, dtype=0, xs=None, sums=None, T=4, packed=P, scales=P, zeros=P, N=8, K=64, y=P, out=0, ws=P,
+def linear(lw, x=P, dtype=0, xs=None, sums=None, T=100, packed=P, scales=P, zeros=P, N=8, K=64, y=P, out=0, ws=P,
            size=BIG):
     return lw.linear_w8a8_raw(x, dtype, xs, sums, T, packed, scales, zeros, N, K, y, out, ws, size, None)
 
 
-def gated(lw, x=P, dtype=0, xs=None, sums=None, T=4, pg=P, sg=P, zg=P, pu=P, su=P, zu=P, N=8, K=64, act=0, h=P, g=None,
+def gated(lw, x=P, dtype=0, xs=None, sums=None, T=100, pg=P, sg=P, zg=P, pu=P, su=P, zu=P, N=8, K=64, act=0, h=P, g=None,
           u=None, out=0, ws=P, size=BIG):
     return lw.gated_w8a8_raw(x, dtype, xs, sums, T, pg, sg, zg, pu, su, zu, N, K, act, h, g, u, out, ws, size, None)
 

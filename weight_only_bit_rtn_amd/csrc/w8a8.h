@@ -226,18 +226,21 @@ struct TilePlan {
   int tiles_m, tiles_n, whole, rest, splits;
   int blocks() const { return whole + rest * splits; }
 };
-// The plan that should finish first, and when: a CU takes step_us for a step
-// of one of its tiles; a join costs about 7 us, and the partial sums
-// (tile_bytes for each share) are written and read again at about 8 TB/s (they stay in the caches).
-inline TilePlan plan_tiles(int64_t tm, int64_t tn, int cus, int steps, double step_us,
-                           double tile_bytes, double* us) {
+// The plan that should finish first, and when.  A CU takes alone_us for a step
+// of a tile that it has to itself, and shared_us for each tile's where it has
+// several workgroups; a join costs about 7 us, and the partial sums (tile_bytes
+// for each share) are written and read again at about 8 TB/s (they stay in the
+// caches).
+inline TilePlan plan_tiles(int64_t tm, int64_t tn, int cus, int steps, double alone_us,
+                           double shared_us, double tile_bytes, double* us) {
   const int64_t tiles = tm * tn, rest = tiles % cus, whole = tiles - rest;
-  const double before = (double)(whole / cus) * steps * step_us;
+  const int64_t rounds = (tiles + cus - 1) / cus;
   TilePlan best{(int)tm, (int)tn, (int)tiles, 0, 1};
-  *us = before + (rest > 0 ? steps * step_us : 0.0);
-  for (int z = 2; rest > 0 && z <= 16 && z <= steps / 8; z++) {
-    const int64_t rounds = (rest * z + cus - 1) / cus;
-    const double t = before + (double)(rounds * ((steps + z - 1) / z)) * step_us + 7.0 +
+  *us = rounds * steps * (rounds > 1 ? shared_us : alone_us);
+  for (int z = 2; rest > 0 && z <= 16 && z <= steps / 4; z++) {
+    const int64_t more = (rest * z + cus - 1) / cus;
+    const double work = (double)(whole / cus) * steps + (double)(more * ((steps + z - 1) / z));
+    const double t = work * (whole / cus + more > 1 ? shared_us : alone_us) + 7.0 +
                      (double)rest * z * tile_bytes * 2 / 8e6;
     if (t < *us) {
       best.whole = (int)whole;

@@ -243,7 +243,7 @@ GemmPlan gemm_plan(int64_t T, int64_t N, int64_t K, bool gated) {
     const TileShape& t = kShapes[i];
     double us;
     const TilePlan plan =
-        plan_tiles((T + t.mt - 1) / t.mt, (rows + t.nt - 1) / t.nt, cus, steps, t.step_us,
+        plan_tiles((T + t.mt - 1) / t.mt, (rows + t.nt - 1) / t.nt, cus, steps, t.step_us, t.step_us,
                    (double)t.mt * t.nt * 4, &us);
     if (i == 0 || us < least) {
       best = {plan, i};

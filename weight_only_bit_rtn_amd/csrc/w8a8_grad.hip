@@ -207,8 +207,7 @@ struct GradArgs {
   const int32_t* e;
   W8 w[2];
   void* dx;
-  float* parts;  // [splits][T][K] sums of each share of the steps, when splits > 1
-  int T, N, K, pitch, half_steps, steps, bf16, splits, tiles_m, tiles_n;
+  int T, N, K, pitch, half_steps, steps, bf16;
 };
 
 // Four code bytes to the exact fp16 integers code - 128: one byte permute
@@ -234,6 +233,14 @@ __device__ __forceinline__ int chunk_at(int n, int slot) {
   return (slot & ~3) | ((slot - (n >> 2)) & 3);
 }
 
+__device__ __forceinline__ void store_dx(const GradArgs& p, f4_t sum, float r, int e, int t, int k) {
+  us4_t out;
+#pragma unroll
+  for (int q = 0; q < 4; q++)
+    out[q] = f32_to_elem(__builtin_amdgcn_ldexpf(sum[q] + r, e), p.bf16);
+  *reinterpret_cast<us4_t*>(static_cast<uint16_t*>(p.dx) + (int64_t)t * p.K + k) = out;
+}
+
 // One workgroup of WM x WN waves: MT tokens by KT columns of dx over its share
 // of the steps, 64 weight rows each, staged in LDS by direct loads on a ring
 // of NB buffers, one barrier per step.  The weight tile lies as it does in
@@ -242,27 +249,33 @@ __device__ __forceinline__ int chunk_at(int n, int slot) {
 // rows of 16 bytes and get a column each).  A step is two halves of 32 rows:
 // while one half is multiplied, the operands of the next are read.
 template <int MT, int KT, int WM, int WN, int NB>
-__global__ __launch_bounds__(WM* WN * 64, 2) void grad_kernel(const GradArgs p) {
+__global__ __launch_bounds__(WM* WN * 64, 2) void grad_kernel(const GradArgs p, const TilePlan plan,
+                                                                 f4_t* __restrict__ parts) {
   constexpr int kWaves = WM * WN;
   constexpr int MW = MT / WM, KW = KT / WN;
   constexpr int FM = MW / 16, FK = KW / 16;
   constexpr int kA = MT * kStepN * 2, kW = kStepN * KT, kBuf = kA + kW;
-  constexpr int LA = kA / 1024 / kWaves, LW = kW / 1024 / kWaves, kLoads = LA + LW;
-  static_assert(LA * 1024 * kWaves == kA && LW * 1024 * kWaves == kW, "whole loads");
+  // 1 KiB loads per wave and step; where the weight rows do not come out even,
+  // the last go to a place of their own, so that every wave counts as many
+  constexpr int LA = kA / 1024 / kWaves, kLW = kW / 1024, LW = (kLW + kWaves - 1) / kWaves;
+  constexpr int kLoads = LA + LW;
+  static_assert(LA * 1024 * kWaves == kA && kLW * 1024 == kW, "whole loads");
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WM, wn = wave / WM;
   const int i16 = lane & 15, h = lane >> 4;
-  const int tiles = p.tiles_m * p.tiles_n;
-  const int split = blockIdx.x / tiles;
+  // a whole tile, or a share of the steps of one of the rest
+  const int over = (int)blockIdx.x - plan.whole;
+  const int split = over < 0 ? 0 : over % plan.splits;
+  const int s0 = over < 0 ? 0 : (int)((int64_t)p.steps * split / plan.splits);
+  const int s1 = over < 0 ? p.steps : (int)((int64_t)p.steps * (split + 1) / plan.splits);
   int tm, tn;
-  tile_of(blockIdx.x % tiles, tiles, p.tiles_m, p.tiles_n, tm, tn);
+  tile_of(over < 0 ? (int)blockIdx.x : plan.whole + over / plan.splits, plan.whole, plan.tiles_m,
+          plan.tiles_n, tm, tn);
   const int t0 = tm * MT, k0 = tn * KT;
   const uint32_t K = (uint32_t)p.K;
-  const int s0 = (int)((int64_t)p.steps * split / p.splits);
-  const int s1 = (int)((int64_t)p.steps * (split + 1) / p.splits);
 
   const uint32_t pitch = (uint32_t)p.pitch * 2;
   const i4_t ra = buffer_of(p.a + (int64_t)t0 * p.pitch, (uint32_t)min(MT, p.T - t0) * pitch);
@@ -277,7 +290,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grad_kernel(const GradArgs p) 
     const int at = (wave + i * kWaves) * 64 + lane, n = at / (KT / 16);
     const int k = k0 + chunk_at<KT>(n, at % (KT / 16)) * 16;
     // columns past the end: not stored, so not loaded either
-    ow[i] = k < p.K ? (uint32_t)n * K + k : 0x80000000u;
+    ow[i] = k < p.K && n < kStepN ? (uint32_t)n * K + k : 0x80000000u;
   }
   // load i of step s; past the share's end it brings zeros
   auto load = [&](int s, int i) {
@@ -290,7 +303,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grad_kernel(const GradArgs p) 
       const int n = (s - m * p.half_steps) * kStepN;
       const int rows = s < s1 ? max(0, min(kStepN, p.N - n)) : 0;
       const i4_t rs = buffer_of(p.w[m].codes + (int64_t)n * K, (uint32_t)rows * K);
-      load_to_lds(rs, buf + kA + (wave + (i - LA) * kWaves) * 1024, ow[i - LA]);
+      const int at = wave + (i - LA) * kWaves;
+      const bool spare = kLW % kWaves != 0 && at >= kLW;
+      load_to_lds(rs, spare ? base + NB * kBuf : buf + kA + at * 1024, ow[i - LA]);
     }
   };
 
@@ -363,8 +378,15 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grad_kernel(const GradArgs p) 
     lds_loads_left<0>();
   }
 
+  if (over >= 0) {
+    f4_t* to = parts + ((int64_t)over * kWaves + wave) * (FK * FM * 64) + lane;
+#pragma unroll
+    for (int i = 0; i < FK; i++)
+#pragma unroll
+      for (int j = 0; j < FM; j++) to[(i * FM + j) * 64] = acc[i][j];
+    return;
+  }
   // lane l of a fragment holds columns k = 4 (l / 16) + 0..3 of token l % 16
-  const bool bf = p.bf16;
 #pragma unroll
   for (int j = 0; j < FM; j++) {
     const int t = t0 + wm * MW + j * 16 + i16;
@@ -374,53 +396,49 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grad_kernel(const GradArgs p) 
 #pragma unroll
     for (int i = 0; i < FK; i++) {
       const int k = k0 + wn * KW + i * 16 + h * 4;
-      if (k >= p.K) continue;
-      const int64_t at = (int64_t)t * p.K + k;
-      if (p.splits > 1) {
-        *reinterpret_cast<f4_t*>(p.parts + (int64_t)split * p.T * p.K + at) = acc[i][j];
-      } else {
-        us4_t out;
-#pragma unroll
-        for (int q = 0; q < 4; q++)
-          out[q] = f32_to_elem(__builtin_amdgcn_ldexpf(acc[i][j][q] + r, e), bf);
-        *reinterpret_cast<us4_t*>(static_cast<uint16_t*>(p.dx) + at) = out;
-      }
+      if (k < p.K) store_dx(p, acc[i][j], r, e, t, k);
     }
   }
 }
 
-// Joins the shares' sums, in their order.
-__global__ __launch_bounds__(256) void grad_join_kernel(const GradArgs p) {
-  const int64_t all = (int64_t)p.T * p.K;
-  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (at >= all) return;
-  f4_t sum = *reinterpret_cast<const f4_t*>(p.parts + at);
-  for (int z = 1; z < p.splits; z++) sum += *reinterpret_cast<const f4_t*>(p.parts + z * all + at);
-  const int t = (int)(at / p.K);
-  const float r = p.r[t];
-  const int e = -p.e[t];
-  us4_t out;
-#pragma unroll
-  for (int q = 0; q < 4; q++)
-    out[q] = f32_to_elem(__builtin_amdgcn_ldexpf(sum[q] + r, e), p.bf16);
-  *reinterpret_cast<us4_t*>(static_cast<uint16_t*>(p.dx) + at) = out;
+// Joins the shares of the plan's rest, in their order: one wave for each
+// fragment of a tile.
+template <int MT, int KT, int WM, int WN>
+__global__ __launch_bounds__(256) void grad_join_kernel(const GradArgs p, const TilePlan plan,
+                                                        const f4_t* __restrict__ parts) {
+  constexpr int kWaves = WM * WN;
+  constexpr int MW = MT / WM, KW = KT / WN, FM = MW / 16, FK = KW / 16;
+  constexpr int kFragments = kWaves * FK * FM;
+  const int lane = threadIdx.x & 63;
+  const int at = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int tile = at / kFragments, f = at % kFragments;
+  if (tile >= plan.rest) return;
+  const int wave = f / (FK * FM), i = f / FM % FK, j = f % FM;
+  int tm, tn;
+  tile_of(plan.whole + tile, plan.whole, plan.tiles_m, plan.tiles_n, tm, tn);
+  const int k = tn * KT + wave / WM * KW + i * 16 + (lane >> 4) * 4;
+  const int t = tm * MT + wave % WM * MW + j * 16 + (lane & 15);
+  if (k >= p.K || t >= p.T) return;
+  f4_t sum = {0, 0, 0, 0};
+  for (int z = 0; z < plan.splits; z++)
+    sum += parts[((int64_t)(tile * plan.splits + z) * kWaves + wave) * (FK * FM * 64) +
+                 (i * FM + j) * 64 + lane];
+  store_dx(p, sum, p.r[t], -p.e[t], t, k);
 }
 
 template <int MT, int KT, int WM, int WN, int NB>
-hipError_t launch_tile(GradArgs p, hipStream_t stream) {
-  constexpr int bytes = NB * (MT * kStepN * 2 + kStepN * KT);
+hipError_t launch_tile(const GradArgs& p, const TilePlan& plan, f4_t* parts, hipStream_t stream) {
+  constexpr bool spare = kStepN * KT / 1024 % (WM * WN) != 0;
+  constexpr int bytes = NB * (MT * kStepN * 2 + kStepN * KT) + (spare ? 1024 : 0);
   auto kernel = grad_kernel<MT, KT, WM, WN, NB>;
   hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), bytes);
   if (e != hipSuccess) return e;
-  p.tiles_m = (p.T + MT - 1) / MT;
-  p.tiles_n = (p.K + KT - 1) / KT;
-  const int64_t total = (int64_t)p.tiles_m * p.tiles_n * p.splits;
-  if (total > INT32_MAX) return hipErrorInvalidValue;
-  kernel<<<dim3((unsigned)total), dim3(WM * WN * 64), bytes, stream>>>(p);
+  kernel<<<dim3((unsigned)plan.blocks()), dim3(WM * WN * 64), bytes, stream>>>(p, plan, parts);
   e = hipGetLastError();
-  if (e != hipSuccess || p.splits == 1) return e;
-  const int64_t quads = (int64_t)p.T * p.K / 4;
-  grad_join_kernel<<<dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream>>>(p);
+  if (e != hipSuccess || plan.rest == 0) return e;
+  constexpr int fragments = (MT / 16) * (KT / 16);
+  grad_join_kernel<MT, KT, WM, WN>
+      <<<dim3((unsigned)((plan.rest * fragments + 3) / 4)), dim3(256), 0, stream>>>(p, plan, parts);
   return hipGetLastError();
 }
 
@@ -444,24 +462,42 @@ void launch_prep(const PrepArgs& q, int64_t T, hipStream_t stream) {
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 int64_t padded(int64_t N) { return (N + kStepN - 1) / kStepN * kStepN; }
 
-// Token rows and columns of a tile for T tokens.
-void tile_shape(int64_t T, int& mt, int& kt) {
-  mt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 512 ? 128 : 256;
-  kt = mt == 256 ? 256 : 128;
-}
-
-// How many shares the steps of each tile are cut into: with few tiles, as
-// many as give each CU two workgroups, at least 8 steps each.  The shares'
-// sums are written and read again, so large problems, which have tiles
-// enough, are not split.
-int split_count(int64_t T, int64_t K, int64_t steps) {
+// Tile shapes: tokens, columns of dx, and what a step of 64 weight rows of one
+// tile takes of a CU's time when the CU has no other workgroup, and when it has
+// (us, measured).
+struct TileShape {
   int mt, kt;
-  tile_shape(T, mt, kt);
-  if (mt == 256) return 1;
-  const int64_t tiles = ((T + mt - 1) / mt) * ((K + kt - 1) / kt);
-  const int64_t want = 512 / tiles, most = steps / 8;
-  const int64_t z = want < most ? want : most;
-  return (int)(z < 1 ? 1 : z > 16 ? 16 : z);
+  double alone_us, shared_us;
+};
+constexpr TileShape kShapes[] = {{16, 128, 0.40, 0.32},  {32, 128, 0.40, 0.32},
+                                 {64, 128, 0.50, 0.40},  {128, 128, 0.74, 0.55},
+                                 {256, 256, 1.60, 1.60}, {256, 192, 1.20, 1.20}};
+
+// The shape that should finish first; of the first four, the least that holds
+// all tokens, or the last.
+struct GradPlan {
+  TilePlan tiles;
+  int shape;
+  size_t part_bytes() const {
+    return (size_t)tiles.rest * tiles.splits * kShapes[shape].mt * kShapes[shape].kt * 4;
+  }
+};
+GradPlan grad_plan(int64_t T, int64_t K, int steps) {
+  const int cus = device_cu_count();
+  GradPlan best{};
+  double least = 0;
+  for (int i = T <= 16 ? 0 : T <= 32 ? 1 : T <= 64 ? 2 : 3; i < 6; i++) {
+    const TileShape& t = kShapes[i];
+    double us;
+    const TilePlan plan = plan_tiles((T + t.mt - 1) / t.mt, (K + t.kt - 1) / t.kt, cus, steps,
+                                     t.alone_us, t.shared_us, (double)t.mt * t.kt * 4, &us);
+    if (least == 0 || us < least) {
+      best = {plan, i};
+      least = us;
+    }
+    if (T <= 64) break;
+  }
+  return best;
 }
 
 }  // namespace
@@ -469,9 +505,8 @@ int split_count(int64_t T, int64_t K, int64_t steps) {
 size_t w8a8_grad_workspace_bytes(int64_t T, int64_t N, int64_t K, bool gated) {
   if (T == 0) return 0;
   const int64_t pitch = padded(N) * (gated ? 2 : 1);
-  const int splits = split_count(T, K, pitch / kStepN);
   return up256((size_t)T * pitch * 2) + 2 * up256((size_t)T * 4) +
-         (splits > 1 ? (size_t)splits * T * K * 4 : 0);
+         grad_plan(T, K, (int)(pitch / kStepN)).part_bytes();
 }
 
 hipError_t launch_w8a8_grad(const void* dh, const void* gate, const void* up, int dtype, int64_t T,
@@ -516,15 +551,23 @@ hipError_t launch_w8a8_grad(const void* dh, const void* gate, const void* up, in
   p.half_steps = (int)(half / kStepN);
   p.steps = (int)(pitch / kStepN);
   p.bf16 = q.bf16;
-  p.splits = split_count(T, K, p.steps);
-  p.parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(q.e) + up256((size_t)T * 4));
-  int mt, kt;
-  tile_shape(T, mt, kt);
-  if (mt == 16) return launch_tile<16, 128, 1, 2, 4>(p, stream);
-  if (mt == 32) return launch_tile<32, 128, 1, 4, 4>(p, stream);
-  if (mt == 64) return launch_tile<64, 128, 1, 4, 4>(p, stream);
-  if (mt == 128) return launch_tile<128, 128, 2, 2, 3>(p, stream);
-  return launch_tile<256, 256, 2, 4, 3>(p, stream);
+  const GradPlan plan = grad_plan(T, K, p.steps);
+  auto* parts =
+      reinterpret_cast<f4_t*>(reinterpret_cast<uint8_t*>(q.e) + up256((size_t)T * 4));
+  switch (plan.shape) {
+    case 0:
+      return launch_tile<16, 128, 1, 2, 4>(p, plan.tiles, parts, stream);
+    case 1:
+      return launch_tile<32, 128, 1, 4, 4>(p, plan.tiles, parts, stream);
+    case 2:
+      return launch_tile<64, 128, 1, 4, 4>(p, plan.tiles, parts, stream);
+    case 3:
+      return launch_tile<128, 128, 2, 2, 3>(p, plan.tiles, parts, stream);
+    case 4:
+      return launch_tile<256, 256, 2, 4, 3>(p, plan.tiles, parts, stream);
+    default:
+      return launch_tile<256, 192, 2, 4, 3>(p, plan.tiles, parts, stream);
+  }
 }
 
 }  // namespace lowbit

@@ -18,8 +18,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 
-from . import (_check, _ptr, _require_gpu_tensor, _stream_handle, _torch,
-               load_library as _load_library)
+from . import _check, _ptr, _require_gpu_tensor, load_library as _load_library
 
 W8A8_MAX_K = 131072
 W8A8_MAX_TN = 1 << 20
@@ -32,6 +31,22 @@ EXPORTED_W8A8 = ("lowbit_quantize_act", "lowbit_linear_w8a8_workspace_bytes", "l
                  "lowbit_gated_w8a8_grad_workspace_bytes", "lowbit_gated_w8a8_grad")
 
 _declared = None
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+def _stream_handle(device) -> int:
+    """The current stream's handle, without the stream object where torch offers that (1.8 us less)."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _lib() -> ctypes.CDLL:
@@ -110,7 +125,8 @@ def gated_w8a8_grad_raw(dh, gate, up, dtype, T, packed_gate, scales_gate, zeros_
 
 
 # ---------------------------------------------------------------------------
-# tensor front end
+# tensor front end: a decoding step's kernels take some microseconds, so the
+# checks look at each tensor once and spell out what is wrong only when it is
 # ---------------------------------------------------------------------------
 def _float_type(t, name: str) -> int:
     torch = _torch()
@@ -121,81 +137,97 @@ def _float_type(t, name: str) -> int:
     return F16 if t.dtype == torch.float16 else BF16
 
 
-def _matrix(t, name: str, dtype, device=None, shape=None) -> None:
-    """``t`` is a dense GPU matrix of this type (and place and shape)."""
+def _wrong(t, name: str, dtype, device, shape) -> None:
+    """Says what is wrong with a tensor."""
     _require_gpu_tensor(t, name, dtype)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must live on {device}, got {t.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dim() != (2 if shape is None else len(shape)):
+        raise ValueError(f"{name} must have {2 if shape is None else len(shape)} dimensions")
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _check_tensor(t, name: str, dtype, device=None, shape=None) -> None:
+    """``t`` is a dense GPU tensor of this type, place and shape (any matrix where None)."""
+    try:
+        fine = (t.dtype == dtype and t.is_cuda and t.is_contiguous()
+                and (t.dim() == 2 if shape is None else t.shape == shape)
+                and (device is None or t.device == device))
+    except AttributeError:
+        fine = False
+    if not fine:
+        _wrong(t, name, dtype, device, shape)
 
 
 def _weights(packed, scales, zeros, device, N=None, K=None):
     """N, K of one 8-bit per-row weight matrix, checked."""
     torch = _torch()
-    _matrix(packed, "packed", torch.int32, device)
-    n, k = packed.shape[0], 4 * packed.shape[1]
-    if N is not None and (n, k) != (N, K):
-        raise ValueError(f"the two weight matrices must have one shape, got {[N, K]} and {[n, k]}")
-    _matrix(scales, "scales", torch.float16, device, (n, 1))
-    _matrix(zeros, "zeros", torch.int32, device, (n, 1))
-    return n, k
+    _check_tensor(packed, "packed", torch.int32, device)
+    n, words = packed.shape
+    if N is not None and (n, 4 * words) != (N, K):
+        raise ValueError(f"the two weight matrices must have one shape, got {[N, K]} and "
+                         f"{[n, 4 * words]}")
+    _check_tensor(scales, "scales", torch.float16, device, (n, 1))
+    _check_tensor(zeros, "zeros", torch.int32, device, (n, 1))
+    return n, 4 * words
 
 
 def _activations(x, out_dtype):
-    """(pointer, type, scales, sums, T, K, device, output type) of a tensor or a quantize_act dict."""
+    """(pointers and type), T, K, device, output type of a tensor or a quantize_act dict."""
     torch = _torch()
     if isinstance(x, dict):
         codes, scales, sums = x["codes"], x["scales"], x["sums"]
-        _matrix(codes, "codes", torch.int8)
+        _check_tensor(codes, "codes", torch.int8)
         T, K = codes.shape
-        for t, name, dtype in ((scales, "scales of x", torch.float32),
-                               (sums, "sums of x", torch.int32)):
-            _require_gpu_tensor(t, name, dtype)
-            if tuple(t.shape) != (T,) or t.device != codes.device:
-                raise ValueError(f"{name} must be [{T}] on {codes.device}")
+        dev = codes.device
+        _check_tensor(scales, "scales of x", torch.float32, dev, (T,))
+        _check_tensor(sums, "sums of x", torch.int32, dev, (T,))
         if out_dtype is None:
             out_dtype = torch.float16
         ptrs = (codes.data_ptr(), I8, scales.data_ptr(), sums.data_ptr())
-        dev = codes.device
     else:
         kind = _float_type(x, "x")
-        _matrix(x, "x", x.dtype)
+        _check_tensor(x, "x", x.dtype)
         T, K = x.shape
+        dev = x.device
         if out_dtype is None:
             out_dtype = x.dtype
         ptrs = (x.data_ptr(), kind, None, None)
-        dev = x.device
-    if out_dtype not in (torch.float16, torch.bfloat16):
+    if out_dtype == torch.float16:
+        out_kind = F16
+    elif out_dtype == torch.bfloat16:
+        out_kind = BF16
+    else:
         raise TypeError(f"out_dtype must be torch.float16 or torch.bfloat16, got {out_dtype}")
-    return ptrs, T, K, dev, out_dtype
+    return ptrs, T, K, dev, out_dtype, out_kind
 
 
 def _on(device):
     """Launches go to the current device: make it the tensors' one."""
     torch = _torch()
     if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+        return _HERE
     return torch.cuda.device(device)
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _workspace(need: int, what: str, device):
     """(tensor or None, address): scratch of at least ``need`` bytes, 256-byte aligned."""
-    if need < 0:
+    if need <= 0:
         _check(need, what)
-    if need == 0:
         return None, None
     # torch's caching allocator hands out blocks aligned to 512 bytes
-    t = _torch().empty(need, dtype=_torch().uint8, device=device)
+    torch = _torch()
+    t = torch.empty(need, dtype=torch.uint8, device=device)
     return t, t.data_ptr()
 
 
 def _out(out, name, shape, dtype, device):
     if out is None:
         return _torch().empty(shape, dtype=dtype, device=device)
-    _matrix(out, name, dtype, device, shape)
+    _check_tensor(out, name, dtype, device, shape)
     return out
 
 
@@ -211,30 +243,25 @@ def quantize_act(x, out: dict | None = None) -> dict:
     sum of a token's codes), which the products take in place of x."""
     torch = _torch()
     kind = _float_type(x, "x")
-    _matrix(x, "x", x.dtype)
+    _check_tensor(x, "x", x.dtype)
     T, K = x.shape
     dev = x.device
-    out = dict(out or {})
-    for name, shape, dtype in (("codes", (T, K), torch.int8), ("scales", (T,), torch.float32),
-                               ("sums", (T,), torch.int32)):
-        if name not in out:
-            out[name] = torch.empty(shape, dtype=dtype, device=dev)
-        else:
-            _require_gpu_tensor(out[name], name, dtype)
-            if tuple(out[name].shape) != shape or out[name].device != dev:
-                raise ValueError(f"{name} must be {list(shape)} on {dev}")
+    out = out or {}
+    codes = _out(out.get("codes"), "codes", (T, K), torch.int8, dev)
+    scales = _out(out.get("scales"), "scales", (T,), torch.float32, dev)
+    sums = _out(out.get("sums"), "sums", (T,), torch.int32, dev)
     with _on(dev):
-        _check(quantize_act_raw(x.data_ptr(), kind, T, K, out["codes"].data_ptr(),
-                                out["scales"].data_ptr(), out["sums"].data_ptr(),
-                                _stream_handle(dev)), "lowbit_quantize_act")
-    return out
+        status = quantize_act_raw(x.data_ptr(), kind, T, K, codes.data_ptr(), scales.data_ptr(),
+                                  sums.data_ptr(), _stream_handle(dev))
+    _check(status, "lowbit_quantize_act")
+    return {"codes": codes, "scales": scales, "sums": sums}
 
 
 def linear_w8a8(x, packed, scales, zeros, out_dtype=None, out=None):
     """y[T][N] = x * deq(packed)^T in 8-bit integers.  ``x``: fp16 or bf16
     [T][K], quantized on the way, or the dict of ``quantize_act``.  ``out_dtype``
     is x's type, or fp16 for a dict, unless given."""
-    ptrs, T, K, dev, out_dtype = _activations(x, out_dtype)
+    ptrs, T, K, dev, out_dtype, out_kind = _activations(x, out_dtype)
     N, k = _weights(packed, scales, zeros, dev)
     if k != K:
         raise ValueError("x and the weights must have the same K")
@@ -242,9 +269,10 @@ def linear_w8a8(x, packed, scales, zeros, out_dtype=None, out=None):
     with _on(dev):
         need = linear_w8a8_workspace_bytes(T, N, K, ptrs[1])
         ws, at = _workspace(need, "lowbit_linear_w8a8_workspace_bytes", dev)
-        _check(linear_w8a8_raw(*ptrs, T, packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
-                               N, K, y.data_ptr(), _float_type(y, "out"), at, need,
-                               _stream_handle(dev)), "lowbit_linear_w8a8")
+        status = linear_w8a8_raw(*ptrs, T, packed.data_ptr(), scales.data_ptr(),
+                                 zeros.data_ptr(), N, K, y.data_ptr(), out_kind, at, need,
+                                 _stream_handle(dev))
+    _check(status, "lowbit_linear_w8a8")
     return y
 
 
@@ -256,7 +284,7 @@ def gated_w8a8(x, packed_gate, scales_gate, zeros_gate, packed_up, scales_up, ze
     ``gated_w8a8_grad`` takes."""
     torch = _torch()
     kind = _act(act)
-    ptrs, T, K, dev, out_dtype = _activations(x, out_dtype)
+    ptrs, T, K, dev, out_dtype, out_kind = _activations(x, out_dtype)
     N, k = _weights(packed_gate, scales_gate, zeros_gate, dev)
     if k != K:
         raise ValueError("x and the weights must have the same K")
@@ -265,12 +293,13 @@ def gated_w8a8(x, packed_gate, scales_gate, zeros_gate, packed_up, scales_up, ze
     with _on(dev):
         need = gated_w8a8_workspace_bytes(T, N, K, ptrs[1])
         ws, at = _workspace(need, "lowbit_gated_w8a8_workspace_bytes", dev)
-        _check(gated_w8a8_raw(*ptrs, T, packed_gate.data_ptr(), scales_gate.data_ptr(),
-                              zeros_gate.data_ptr(), packed_up.data_ptr(), scales_up.data_ptr(),
-                              zeros_up.data_ptr(), N, K, kind, outs[0].data_ptr(),
-                              outs[1].data_ptr() if save else None,
-                              outs[2].data_ptr() if save else None, _float_type(outs[0], "h"), at,
-                              need, _stream_handle(dev)), "lowbit_gated_w8a8")
+        status = gated_w8a8_raw(*ptrs, T, packed_gate.data_ptr(), scales_gate.data_ptr(),
+                                zeros_gate.data_ptr(), packed_up.data_ptr(),
+                                scales_up.data_ptr(), zeros_up.data_ptr(), N, K, kind,
+                                outs[0].data_ptr(), outs[1].data_ptr() if save else None,
+                                outs[2].data_ptr() if save else None, out_kind, at, need,
+                                _stream_handle(dev))
+    _check(status, "lowbit_gated_w8a8")
     return tuple(outs) if save else outs[0]
 
 
@@ -278,7 +307,7 @@ def linear_w8a8_grad(dy, packed, scales, zeros, out=None):
     """dx[T][K] = dy[T][N] * deq(packed), of dy's type: the gradient of
     ``linear_w8a8`` with respect to x."""
     kind = _float_type(dy, "dy")
-    _matrix(dy, "dy", dy.dtype)
+    _check_tensor(dy, "dy", dy.dtype)
     dev = dy.device
     N, K = _weights(packed, scales, zeros, dev)
     T = dy.shape[0]
@@ -288,9 +317,10 @@ def linear_w8a8_grad(dy, packed, scales, zeros, out=None):
     with _on(dev):
         need = linear_w8a8_grad_workspace_bytes(T, N, K)
         ws, at = _workspace(need, "lowbit_linear_w8a8_grad_workspace_bytes", dev)
-        _check(linear_w8a8_grad_raw(dy.data_ptr(), kind, T, packed.data_ptr(), scales.data_ptr(),
-                                    zeros.data_ptr(), N, K, dx.data_ptr(), at, need,
-                                    _stream_handle(dev)), "lowbit_linear_w8a8_grad")
+        status = linear_w8a8_grad_raw(dy.data_ptr(), kind, T, packed.data_ptr(),
+                                      scales.data_ptr(), zeros.data_ptr(), N, K, dx.data_ptr(),
+                                      at, need, _stream_handle(dev))
+    _check(status, "lowbit_linear_w8a8_grad")
     return dx
 
 
@@ -303,25 +333,26 @@ def gated_w8a8_grad(dh, gate, up, packed_gate, scales_gate, zeros_gate, packed_u
     torch = _torch()
     code = _act(act)
     kind = _float_type(dh, "dh")
-    _matrix(dh, "dh", dh.dtype)
+    _check_tensor(dh, "dh", dh.dtype)
     dev = dh.device
     N, K = _weights(packed_gate, scales_gate, zeros_gate, dev)
     _weights(packed_up, scales_up, zeros_up, dev, N, K)
     T = dh.shape[0]
     if dh.shape[1] != N:
         raise ValueError("dh.shape[1] must be the weights' N")
-    _matrix(gate, "gate", dh.dtype, dev, dh.shape)
-    _matrix(up, "up", dh.dtype, dev, dh.shape)
+    _check_tensor(gate, "gate", dh.dtype, dev, dh.shape)
+    _check_tensor(up, "up", dh.dtype, dev, dh.shape)
     dx = torch.empty((T, K), dtype=dh.dtype, device=dev)
     dgate = torch.empty_like(dh) if parts else None
     dup = torch.empty_like(dh) if parts else None
     with _on(dev):
         need = gated_w8a8_grad_workspace_bytes(T, N, K)
         ws, at = _workspace(need, "lowbit_gated_w8a8_grad_workspace_bytes", dev)
-        _check(gated_w8a8_grad_raw(dh.data_ptr(), gate.data_ptr(), up.data_ptr(), kind, T,
-                                   packed_gate.data_ptr(), scales_gate.data_ptr(),
-                                   zeros_gate.data_ptr(), packed_up.data_ptr(),
-                                   scales_up.data_ptr(), zeros_up.data_ptr(), N, K, code,
-                                   dx.data_ptr(), _ptr(dgate), _ptr(dup), at, need,
-                                   _stream_handle(dev)), "lowbit_gated_w8a8_grad")
+        status = gated_w8a8_grad_raw(dh.data_ptr(), gate.data_ptr(), up.data_ptr(), kind, T,
+                                     packed_gate.data_ptr(), scales_gate.data_ptr(),
+                                     zeros_gate.data_ptr(), packed_up.data_ptr(),
+                                     scales_up.data_ptr(), zeros_up.data_ptr(), N, K, code,
+                                     dx.data_ptr(), _ptr(dgate), _ptr(dup), at, need,
+                                     _stream_handle(dev))
+    _check(status, "lowbit_gated_w8a8_grad")
     return (dx, dgate, dup) if parts else dx
