@@ -506,3 +506,183 @@ def test_refusals(lw):
              lw.LowbitError)]:
         with pytest.raises(error):
             call()
+
+
+# ---------------------------------------------------------------------------
+# larger sizes: every tile shape, whole and shared out, and long index ranges
+# (the 64-bit reference on the GPU)
+# ---------------------------------------------------------------------------
+LARGE = [(70, 21, 1504), (400, 8273, 1632), (644, 6956, 4416), (1289, 8336, 64), (2526, 6531, 992), (184, 8255, 5088),
+         (1035, 7325, 64), (2834, 8215, 3328), (133, 8211, 1600), (396, 5143, 4416), (545, 8245, 32),
+         (798, 8247, 1632), (399, 5628, 3680), (398, 8230, 128), (2072, 5437, 3104)]
+LARGE_GRAD = [(65, 917, 544), (1026, 1153, 3616), (689, 4793, 4064), (2314, 44, 4832), (3257, 1258, 5024),
+              (131, 4413, 4768), (1694, 46, 4640), (2339, 2268, 4832), (74, 496, 160), (773, 609, 4672),
+              (642, 2338, 4064), (3082, 839, 4896), (138, 2603, 3232), (2334, 1101, 4864)]
+
+
+def random_weights(g, N, K):
+    """Packed words, scales, zero points near the middle, on the GPU."""
+    import torch
+    codes = torch.randint(0, 256, (N, K), generator=g, device="cuda", dtype=torch.uint8)
+    scales = ((torch.rand(N, 1, generator=g, device="cuda") * 1.5 + 0.5) * 2e-4).half()
+    zeros = torch.randint(110, 146, (N, 1), generator=g, device="cuda", dtype=torch.int32)
+    return codes.view(torch.int32), scales, zeros
+
+
+def integers(w):
+    import torch
+    packed, _, zeros = w
+    return packed.view(torch.uint8).view(packed.shape[0], -1).double() - zeros.double()
+
+
+def inside(got, want, bound, what):
+    bad = ~((got.double() - want).abs() <= bound)
+    assert not bool(bad.any()), f"{what}: {int(bad.sum())} of {bad.numel()} outside, first {bad.nonzero()[:3].tolist()}"
+
+
+@pytest.mark.parametrize("shape", LARGE, ids=str)
+def test_every_tile_plan(lw, shape):
+    import torch
+    T, N, K = shape
+    say("tile plans", shape)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    wg, wu = random_weights(g, N, K), random_weights(g, N, K)
+    x = torch.randn(T, K, generator=g, device="cuda").half()
+    q = lw.quantize_act(x)
+    a, s = q["codes"].double(), q["scales"].double()[:, None]
+    gate = (a @ integers(wg).t()) * (s * wg[1].double().t())
+    bound = 2.0 ** -11 * 1.001 + 4 * ref.U32
+
+    def linear_bound(v):
+        return v.abs() * bound + ref.HALF_TINY["fp16"]
+
+    y = lw.linear_w8a8(x, *wg)
+    inside(y, gate, linear_bound(gate), f"linear {shape}")
+    assert bool((lw.linear_w8a8(q, *wg) == y).all())
+    up = (a @ integers(wu).t()) * (s * wu[1].double().t())
+    h, hg, hu = lw.gated_w8a8(x, *wg, *wu, save=True)
+    inside(hg, gate, linear_bound(gate), f"gate {shape}")
+    inside(hu, up, linear_bound(up), f"up {shape}")
+    want = gate * torch.sigmoid(gate) * up
+    r = (20 + 20 * gate.abs().clamp(max=104)) * ref.U32
+    inside(h, want, want.abs() * (2.0 ** -11 * 1.001 + r) + ref.HALF_TINY["fp16"], f"h {shape}")
+
+
+@pytest.mark.parametrize("shape", LARGE_GRAD, ids=str)
+def test_every_gradient_plan(lw, shape):
+    import torch
+    T, N, K = shape
+    say("gradient plans", shape)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    ws = [random_weights(g, N, K) for _ in range(2)]
+    dy = (torch.randn(T, N, generator=g, device="cuda") * 0.05).half()
+
+    def bound(want, parts, extra):
+        terms = N * len(parts)
+        out = want.abs() * 2.0 ** -11 * 1.01 + ref.HALF_TINY["fp16"]
+        top = torch.stack([(d.abs() * w[1].double().t()).amax(1) for d, w in parts]).amax(0)[:, None]
+        for (d, w), e in zip(parts, extra):
+            size = (integers(w) + w[2].double() - 128).abs() + (128 - w[2].double()).abs()
+            f = d.abs() * w[1].double().t()
+            out += (f * (2.0 ** -11 + 8 * ref.U32 + terms * 2.0 ** -23 + e) + top * 2.0 ** -39) @ size * 1.001
+        return out
+
+    def product(parts):
+        return sum((d * w[1].double().t()) @ integers(w) for d, w in parts)
+
+    parts = [(dy.double(), ws[0])]
+    want = product(parts)
+    dx = lw.linear_w8a8_grad(dy, *ws[0])
+    inside(dx, want, bound(want, parts, [0]), f"linear {shape}")
+    if N >= 512:     # sums of independent roundings: half a step each at the most, in the 2-norm
+        assert float((dx.double() - want).norm()) <= float(want.norm()) * 2.0 ** -10
+    assert bool((lw.linear_w8a8_grad(dy, *ws[0]) == dx).all())
+    gate = torch.randn(T, N, generator=g, device="cuda").half()
+    up = torch.randn(T, N, generator=g, device="cuda").half()
+    v = gate.double()
+    s = torch.sigmoid(v)
+    parts = [(dy.double() * up.double() * (s + v * s * (1 - s)), ws[0]), (dy.double() * v * s, ws[1])]
+    want = product(parts)
+    # the slope's relative error where its terms cancel is bounded by their size: 64 half steps of dy up
+    slope = (dy.double() * up.double()).abs() * 64 * ref.U32 / parts[0][0].abs().clamp(min=1e-30)
+    inside(lw.gated_w8a8_grad(dy, gate, up, *ws[0], *ws[1]), want, bound(want, parts, [slope, 64 * ref.U32]),
+           f"gated {shape}")
+
+
+@pytest.mark.parametrize("N", [32769, 40000, 65544])
+def test_gradients_of_long_rows(lw, N):
+    """More weight rows than a preparation holds in registers, whole 16-byte chunks and not."""
+    T, K = 3, 64
+    say("long rows", N)
+    rng = np.random.default_rng(N)
+    wg, wu = weights(rng, N, K, "minmax"), weights(rng, N, K, "minmax")
+    dh, gate, up = (gpu(rng.standard_normal((T, N)).astype(np.float32), "bf16") for _ in range(3))
+    dh = dh * 0.01
+    want = ref.linear_grad(f64(dh), *wg)
+    check(lw.linear_w8a8_grad(dh, *on_gpu(wg)), want, ref.grad_bound(want, [(f64(dh), *wg)], "bf16"), f"linear {N}")
+    dg, du = ref.gated_parts(f64(dh), f64(gate), f64(up), "silu")
+    dx, pg, pu = lw.gated_w8a8_grad(dh, gate, up, *on_gpu(wg), *on_gpu(wu), parts=True)
+    want = ref.linear_grad(dg, *wg) + ref.linear_grad(du, *wu)
+    size = np.abs(f64(dh) * f64(up)) * 64 * ref.U32
+    extra = [size / np.maximum(np.abs(dg), 1e-30), 64 * ref.U32]
+    check(dx, want, ref.grad_bound(want, [(dg, *wg), (du, *wu)], "bf16", extra), f"gated {N}")
+    check(pg, dg, np.abs(dg) * 2.0 ** -8 * 1.01 + 2 * size + ref.HALF_TINY["bf16"], "dgate")
+    check(pu, du, np.abs(du) * (2.0 ** -8 * 1.01 + 64 * ref.U32) + ref.HALF_TINY["bf16"], "dup")
+
+
+def test_more_outputs_than_32_bits_count(lw):
+    """T N and T K above 2^31 elements (offsets above 2^32 bytes): the last tokens and rows are right."""
+    import torch
+    T, N, K = 46000, 49153, 64
+    say("many outputs", T, N, K)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = random_weights(g, N, K)
+    x = torch.randn(T, K, generator=g, device="cuda").half()
+    y = lw.linear_w8a8(x, *w)
+    some = torch.tensor([0, 1, 22000, 43689, 43690, 43691, T - 2, T - 1], device="cuda")
+    q = lw.quantize_act(x[some])
+    want = (q["codes"].double() @ integers(w).t()) * (q["scales"].double()[:, None] * w[1].double().t())
+    inside(y[some], want, want.abs() * (2.0 ** -11 * 1.001 + 4 * ref.U32) + ref.HALF_TINY["fp16"], "linear")
+    dx = lw.linear_w8a8_grad(y, *w)
+    alone = lw.linear_w8a8_grad(y[some].contiguous(), *w)
+    # other tile shapes: the same sums in another order
+    assert float((dx[some] - alone).double().norm()) <= float(alone.double().norm()) * 2.0 ** -10
+    del dx, alone, y
+    torch.cuda.empty_cache()
+    w = random_weights(g, 64, 65536)
+    d = torch.randn(40000, 64, generator=g, device="cuda").half()
+    dx = lw.linear_w8a8_grad(d, *w)
+    rows = torch.tensor([0, 32767, 32768, 39999], device="cuda")
+    want = (d[rows].double() * w[1].double().t()) @ integers(w)
+    assert float((dx[rows].double() - want).norm()) <= float(want.norm()) * 2.0 ** -10
+
+
+def test_first_calls_captured():
+    """In a new process, the very first calls go into a graph."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    say("first calls captured")
+    code = """
+import torch, sys
+sys.path.insert(0, %r)
+import weight_only_bit_rtn_amd as lw
+g = torch.Generator(device="cuda").manual_seed(0)
+codes = torch.randint(0, 256, (256, 256), generator=g, device="cuda", dtype=torch.uint8)
+w = codes.view(torch.int32), torch.full((256, 1), 1e-3, device="cuda").half(), torch.full((256, 1), 128, device="cuda", dtype=torch.int32)
+xs = [torch.randn(T, 256, generator=g, device="cuda").half() for T in (1, 20, 300)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = [(lw.gated_w8a8(x, *w, *w), lw.linear_w8a8(x, *w), lw.linear_w8a8_grad(x, *w)) for x in xs]
+for _ in range(3):
+    graph.replay()
+    torch.cuda.synchronize()
+    for x, o in zip(xs, out):
+        for p, q in zip(o, (lw.gated_w8a8(x, *w, *w), lw.linear_w8a8(x, *w), lw.linear_w8a8_grad(x, *w))):
+            assert bool((p == q).all())
+print("captured")
+""" % root
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
