@@ -193,13 +193,27 @@ __global__ __launch_bounds__(256) void w8a8_join_kernel(const GemmArgs p, const 
   const int t = tm * MT + wave % WM * MW + j * 16 + (lane & 15);
   if (n >= p.N || t >= p.T) return;
   i4_t sum[2] = {i4_t{0, 0, 0, 0}, i4_t{0, 0, 0, 0}};
-  for (int z = 0; z < plan.splits; z++) {
-    const i4_t* from =
-        parts + ((int64_t)(tile * plan.splits + z) * kWaves + wave) * (FN * FM * 64) + lane;
-    sum[0] += from[(i * FM + j) * 64];
-    if constexpr (GATED) sum[1] += from[((FO + i) * FM + j) * 64];
+  const Columns<GATED> columns(p, n);
+  const float xs = p.xs[t];
+  const int total = p.xsum[t];
+  for (int z = 0; z < plan.splits; z += 4) {  // four shares' loads at a time
+    i4_t v[4][2];
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      const int zz = min(z + u, plan.splits - 1);
+      const i4_t* from =
+          parts + ((int64_t)(tile * plan.splits + zz) * kWaves + wave) * (FN * FM * 64) + lane;
+      v[u][0] = from[(i * FM + j) * 64];
+      if constexpr (GATED) v[u][1] = from[((FO + i) * FM + j) * 64];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; u++)
+      if (z + u < plan.splits) {
+        sum[0] += v[u][0];
+        if constexpr (GATED) sum[1] += v[u][1];
+      }
   }
-  store4<GATED>(p, Columns<GATED>(p, n), sum[0], sum[1], n, t, p.xs[t], p.xsum[t]);
+  store4<GATED>(p, columns, sum[0], sum[1], n, t, xs, total);
 }
 
 template <int MT, int NT, int WM, int WN, bool GATED>

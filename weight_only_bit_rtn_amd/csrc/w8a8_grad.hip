@@ -410,9 +410,18 @@ __global__ __launch_bounds__(256) void grad_join_kernel(const GradArgs p, const 
   const int t = tm * MT + wave % WM * MW + j * 16 + (lane & 15);
   if (k >= p.K || t >= p.T) return;
   f4_t sum = {0, 0, 0, 0};
-  for (int z = 0; z < plan.splits; z++)
-    sum += parts[((int64_t)(tile * plan.splits + z) * kWaves + wave) * (FK * FM * 64) +
-                 (i * FM + j) * 64 + lane];
+  for (int z = 0; z < plan.splits; z += 4) {  // four loads at a time
+    f4_t v[4];
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      const int zz = min(z + u, plan.splits - 1);
+      v[u] = parts[((int64_t)(tile * plan.splits + zz) * kWaves + wave) * (FK * FM * 64) +
+                   (i * FM + j) * 64 + lane];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; u++)
+      if (z + u < plan.splits) sum += v[u];
+  }
   store_dx(p, sum, p.r[t], -p.e[t], t, k);
 }
 
