@@ -514,7 +514,8 @@ def test_refusals(lw):
 # ---------------------------------------------------------------------------
 LARGE = [(70, 21, 1504), (400, 8273, 1632), (644, 6956, 4416), (1289, 8336, 64), (2526, 6531, 992), (184, 8255, 5088),
          (1035, 7325, 64), (2834, 8215, 3328), (133, 8211, 1600), (396, 5143, 4416), (545, 8245, 32),
-         (798, 8247, 1632), (399, 5628, 3680), (398, 8230, 128), (2072, 5437, 3104)]
+         (798, 8247, 1632), (399, 5628, 3680), (398, 8230, 128), (2072, 5437, 3104), (2322, 6432, 2304),
+         (812, 8211, 2432), (2074, 7217, 32), (3105, 7520, 1504), (784, 8508, 64), (1337, 8245, 1728)]
 LARGE_GRAD = [(65, 917, 544), (1026, 1153, 3616), (689, 4793, 4064), (2314, 44, 4832), (3257, 1258, 5024),
               (131, 4413, 4768), (1694, 46, 4640), (2339, 2268, 4832), (74, 496, 160), (773, 609, 4672),
               (642, 2338, 4064), (3082, 839, 4896), (138, 2603, 3232), (2334, 1101, 4864)]

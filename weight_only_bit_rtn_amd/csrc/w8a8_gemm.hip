@@ -13,17 +13,28 @@ namespace lowbit {
 namespace {
 
 constexpr int kStep = 64;    // bytes (values) of k per pipeline step
-constexpr int kBuffers = 4;  // LDS buffers of one step each
 
 // One workgroup of WM x WN waves computes MT tokens by NT weight rows (gated:
 // NT / 2 rows of each matrix, the wave's first half gate, its second half up,
-// so a lane holds both projections of an output).  Steps of 128 k are staged
-// in LDS by direct loads, two buffers: step i + 1 is on its way while step i
-// is multiplied, one barrier per step.  A row of a step is 8 chunks of 16
-// bytes; chunk c of row r lies at c ^ (r & 7), so the 16 rows of one operand
-// read spread over all banks.  Values past the row's end, tokens past T and
-// rows past N come as zeros from the buffers' range check.
-template <int MT, int NT, int WM, int WN, bool GATED>
+// so a lane holds both projections of an output).
+//
+// Steps of 64 k are staged in LDS by direct loads on a ring of NB buffers, one
+// barrier per step.  A row of a step is 4 chunks of 16 bytes; chunk c of row r
+// lies at c ^ (-(r / 4) & 3), so that the rows one operand read touches at a
+// time lie in different banks (no conflicts counted).  Values past the row's
+// end, tokens past T and rows past N come as zeros from the buffers' range
+// check.
+//
+// What bounds it is LDS: 64 bytes per clock and CU, measured for ds_read_b128
+// in any conflict-free pattern.  256 x 256 outputs want 96 KiB of operand reads
+// (eight waves of 128 x 64) and 32 KiB written per step, about 1800 clocks for
+// 1024 of matrix work; 256 x 384 (128 x 96 per wave, the most that 256
+// registers hold) 112 and 40 KiB for 1536.  Measured on 4096x12288x12288: 541
+// and 505 us (2.3 and 2.45 POP/s), on long runs at a clock that power holds
+// near 1.9 GHz.  Slower there: 128 x 128 per wave with one wave per SIMD (a
+// third fewer reads, but a lone wave cannot issue fast enough: 577 us), weights
+// straight from L2 into registers (750 us), 32x32x32 products (620 us).
+template <int MT, int NT, int WM, int WN, int NB, bool GATED>
 __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, const TilePlan plan,
                                                                  i4_t* __restrict__ parts) {
   constexpr int kWaves = WM * WN;
@@ -82,11 +93,11 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, 
     spare[i] = kB % kWaves != 0 && slot >= NT;
     const int row = GATED ? slot / NW * (NW / 2) + in % (NW / 2) : slot;
     ob[i] = spare[i] ? 0x80000000u : (row + r16) * K + chunk;
-    lb[i] = base + (spare[i] ? kBuffers * kBuf : (MT + slot) * kStep);
+    lb[i] = base + (spare[i] ? NB * kBuf : (MT + slot) * kStep);
   }
   // load i of the LA + LB of step s; past the share's last step it brings zeros
   auto load = [&](int s, int i) {
-    const uint32_t k0 = (uint32_t)s * kStep, buf = (uint32_t)(s % kBuffers) * kBuf;
+    const uint32_t k0 = (uint32_t)s * kStep, buf = (uint32_t)(s % NB) * kBuf;
     const uint32_t add = k0 + chunk < kend ? k0 : 0x80000000u;
     if (i < LA)
       load_to_lds(ra, la[i] + buf, oa[i] + add);
@@ -105,48 +116,52 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, 
   const uint32_t swizzled = (h ^ (-(i16 >> 2) & 3)) * 16;
   const uint32_t ra0 = (wm * MW + i16) * kStep + swizzled, rb0 = (MT + wn * NW + i16) * kStep + swizzled;
   auto tokens = [&](int s, int j) {
-    return *reinterpret_cast<const i4_t*>(lds + s % kBuffers * kBuf + ra0 + j * 16 * kStep);
+    return *reinterpret_cast<const i4_t*>(lds + s % NB * kBuf + ra0 + j * 16 * kStep);
   };
   auto rows = [&](int s, int i) {
-    return *reinterpret_cast<const i4_t*>(lds + s % kBuffers * kBuf + rb0 + i * 16 * kStep);
+    return *reinterpret_cast<const i4_t*>(lds + s % NB * kBuf + rb0 + i * 16 * kStep);
   };
-  // one step: its tokens are in fa and its first kAhead row operands in fb;
-  // reads the next step's tokens into fn and the row operands kAhead ahead
-  constexpr int kAhead = 2;
-  i4_t fb[kAhead];
-  auto step = [&](int s, const i4_t(&fa)[FM], i4_t(&fn)[FM]) {
-    lds_loads_left<(kBuffers - 3) * kLoads>();  // this wave's part of step s + 1 has landed
-    __syncthreads();                            // and everyone's; step s - 1 has been read
-    __builtin_amdgcn_sched_barrier(0);
+  // One step: its tokens are in fa and its first two row operands in fb.  The
+  // last row operand's products are the last to use the tokens; each token's is
+  // followed by the read of the next step's, behind the step's barrier.
+  i4_t fa[FM], fb[2];
+  auto step = [&](int s) {
 #pragma unroll
     for (int i = 0; i < FN; i++) {
+      if (i == FN - 1) {
+        lds_loads_left<(NB - 2) * kLoads>();  // this wave's part of the next step has landed
+        __syncthreads();                      // and everyone's; this step has been read
+        __builtin_amdgcn_sched_barrier(0);
+      } else {
 #pragma unroll
-      for (int l = i * kLoads / FN; l < (i + 1) * kLoads / FN; l++) load(s + kBuffers - 1, l);
-      const i4_t w = fb[i % kAhead] ^ (int)0x80808080;
-      fb[i % kAhead] = i + kAhead < FN ? rows(s, i + kAhead) : rows(s + 1, i + kAhead - FN);
+        for (int l = i * kLoads / (FN - 1); l < (i + 1) * kLoads / (FN - 1); l++)
+          load(s + NB - 1, l);
+      }
+      const i4_t w = fb[i % 2] ^ (int)0x80808080;
+      if (i + 2 < FN) fb[i % 2] = rows(s, i + 2);
+      if (i == FN - 1) {
+        fb[0] = rows(s + 1, 0);
+        fb[1] = rows(s + 1, 1);
+      }
 #pragma unroll
-      for (int j = i * FM / FN; j < (i + 1) * FM / FN; j++) fn[j] = tokens(s + 1, j);
-#pragma unroll
-      for (int j = 0; j < FM; j++)
+      for (int j = 0; j < FM; j++) {
         acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, fa[j], acc[i][j], 0, 0, 0);
+        if (i == FN - 1) fa[j] = tokens(s + 1, j);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  i4_t f0[FM], f1[FM];
 #pragma unroll
-  for (int s = 0; s < kBuffers - 1; s++)
+  for (int s = 0; s < NB - 1; s++)
 #pragma unroll
     for (int i = 0; i < kLoads; i++) load(s0 + s, i);
-  lds_loads_left<(kBuffers - 2) * kLoads>();
+  lds_loads_left<(NB - 2) * kLoads>();
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < FM; j++) f0[j] = tokens(s0, j);
-#pragma unroll
-  for (int i = 0; i < kAhead; i++) fb[i] = rows(s0, i);
-  for (int s = s0; s < s1; s += 2) {
-    step(s, f0, f1);
-    step(s + 1, f1, f0);  // past the end: zeros
-  }
+  for (int j = 0; j < FM; j++) fa[j] = tokens(s0, j);
+  fb[0] = rows(s0, 0);
+  fb[1] = rows(s0, 1);
+  for (int s = s0; s < s1; s++) step(s);
   lds_loads_left<0>();
 
   if (over >= 0) {
@@ -216,10 +231,10 @@ __global__ __launch_bounds__(256) void w8a8_join_kernel(const GemmArgs p, const 
   store4<GATED>(p, columns, sum[0], sum[1], n, t, xs, total);
 }
 
-template <int MT, int NT, int WM, int WN, bool GATED>
+template <int MT, int NT, int WM, int WN, int NB, bool GATED>
 hipError_t launch_tile(const GemmArgs& p, const TilePlan& plan, i4_t* parts, hipStream_t stream) {
-  constexpr int bytes = kBuffers * (MT + NT) * kStep + (NT / 16 % (WM * WN) ? 1024 : 0);
-  auto kernel = w8a8_kernel<MT, NT, WM, WN, GATED>;
+  constexpr int bytes = NB * (MT + NT) * kStep + (NT / 16 % (WM * WN) ? 1024 : 0);
+  auto kernel = w8a8_kernel<MT, NT, WM, WN, NB, GATED>;
   hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), bytes);
   if (e != hipSuccess) return e;
   kernel<<<dim3((unsigned)plan.blocks()), dim3(WM * WN * 64), bytes, stream>>>(p, plan, parts);
@@ -238,7 +253,8 @@ struct TileShape {
   int mt, nt;
   double step_us;
 };
-constexpr TileShape kShapes[] = {{128, 128, 0.40}, {256, 256, 1.03}, {256, 192, 0.90}};
+constexpr TileShape kShapes[] = {
+    {128, 128, 0.40}, {256, 256, 1.03}, {256, 192, 0.90}, {256, 384, 1.42}};
 
 // The shape that should finish first.
 struct GemmPlan {
@@ -253,7 +269,7 @@ GemmPlan gemm_plan(int64_t T, int64_t N, int64_t K, bool gated) {
   const int64_t rows = gated ? 2 * N : N;
   GemmPlan best{};
   double least = 0;
-  for (int i = 0; i < 3; i++) {
+  for (int i = 0; i < 4; i++) {
     const TileShape& t = kShapes[i];
     double us;
     const TilePlan plan =
@@ -315,9 +331,10 @@ hipError_t launch(const Activations& x, int64_t T, const W8& w0, const W8& w1, i
   const GemmPlan plan = gemm_plan(T, N, K, GATED);
   auto* parts = reinterpret_cast<i4_t*>(static_cast<uint8_t*>(workspace) +
                                         (x.dtype == kI8 ? 0 : code_bytes(T, K)));
-  if (plan.shape == 0) return launch_tile<128, 128, 2, 2, GATED>(p, plan.tiles, parts, stream);
-  if (plan.shape == 1) return launch_tile<256, 256, 2, 4, GATED>(p, plan.tiles, parts, stream);
-  return launch_tile<256, 192, 4, 2, GATED>(p, plan.tiles, parts, stream);
+  if (plan.shape == 0) return launch_tile<128, 128, 2, 2, 4, GATED>(p, plan.tiles, parts, stream);
+  if (plan.shape == 1) return launch_tile<256, 256, 2, 4, 4, GATED>(p, plan.tiles, parts, stream);
+  if (plan.shape == 2) return launch_tile<256, 192, 4, 2, 4, GATED>(p, plan.tiles, parts, stream);
+  return launch_tile<256, 384, 2, 4, 4, GATED>(p, plan.tiles, parts, stream);
 }
 
 }  // namespace
