@@ -10,8 +10,10 @@
 // quantizes x itself when that is little (T K <= kFusedMost), while its
 // first weights are on their way, and copies codes otherwise.  Wave w of
 // workgroup b takes rows w G + b, then 16 G further (G workgroups), so few
-// rows still spread over all CUs.  Eight loads per lane are in flight,
-// running ahead into the wave's next rows.
+// rows still spread over all CUs.  Two loads per lane are in flight, running
+// ahead into the wave's next rows: 16 waves cover the latency, and loads past
+// the last row only cost time (2 / 4 / 8 per lane: 1x4096x4096 5.9 / 6.1 / 7.4
+// us, gated 1x28672x8192 81.7 / 83.6 / 82.7, 1x49152x12288 106 / 105 / 108).
 #include "w8a8.h"
 
 namespace lowbit {
@@ -19,7 +21,7 @@ namespace {
 
 constexpr int kWaves = 16;
 constexpr int kChunk = 1024;   // bytes of a row per load
-constexpr int kInFlight = 8;   // loads per lane
+constexpr int kInFlight = 2;   // loads per lane
 
 // Bytes of one token's codes in LDS: whole chunks, zeros behind the last.
 __host__ __device__ constexpr int few_pitch(int K) {
