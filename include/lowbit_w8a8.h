@@ -48,7 +48,8 @@
  * T * N and T * K <= 2^36.  Any N, odd ones too.  T == 0 is an empty problem; N == 0 leaves a product empty and a
  * gradient zero.  A workspace smaller than the *_workspace_bytes value, or not
  * 256-byte aligned, returns LOWBIT_ERR_ARG; calls on one workspace must not
- * overlap.  Workspace sizes of zero allow a null workspace.
+ * overlap.  Workspace sizes of zero allow a null workspace; sizes are those of
+ * the current device, on which the call has to be made too.
  */
 #ifndef LOWBIT_W8A8_H
 #define LOWBIT_W8A8_H
