@@ -11,8 +11,6 @@ enum ElemType { kF16 = 0, kBF16 = 1, kI8 = 2 };
 enum ActKind { kSilu = 0, kGeluTanh = 1 };
 
 typedef int i4_t __attribute__((ext_vector_type(4)));
-typedef int i16_t __attribute__((ext_vector_type(16)));
-typedef float f16_t __attribute__((ext_vector_type(16)));
 typedef int i2_t __attribute__((ext_vector_type(2)));
 typedef uint16_t us4_t __attribute__((ext_vector_type(4)));
 typedef uint16_t us8_t __attribute__((ext_vector_type(8)));
@@ -59,12 +57,18 @@ __device__ __forceinline__ void act_value_slope(float v, int act, float& f, floa
   df = s + s * (1.0f - s) * w;
 }
 
-// Buffer descriptor (raw, range-checked) of `bytes` bytes at a wave-uniform address.
+// Buffer descriptor (raw, range-checked) of `bytes` bytes at a wave-uniform
+// address.  A memory instruction may read a scalar register five wait states
+// after a vector instruction (readfirstlane) wrote it; the compiler does not
+// see to that for the assembly of load_to_lds(), so it is waited for here, once
+// a descriptor (in each load it cost 4% at 4096 x 12288 x 12288).
 __device__ __forceinline__ i4_t buffer_of(const void* base, uint32_t bytes) {
   const uint64_t at = reinterpret_cast<uint64_t>(base);
-  return i4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)at),
-              __builtin_amdgcn_readfirstlane((int)((uint32_t)(at >> 32) & 0xffffu)),
-              __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+  i4_t rs{__builtin_amdgcn_readfirstlane((int)(uint32_t)at),
+          __builtin_amdgcn_readfirstlane((int)((uint32_t)(at >> 32) & 0xffffu)),
+          __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+  asm volatile("s_nop 4" : "+s"(rs));
+  return rs;
 }
 
 // The LDS address of a pointer into shared memory.
@@ -78,25 +82,20 @@ __device__ __forceinline__ uint32_t lds_address(void* p) {
 // the builtin the compiler waits for every such load in flight before a
 // transposing LDS read (large gradient 4.1 -> 3.1 ms without those waits).
 // The caller waits with lds_loads_left() before the barrier that publishes
-// them, and for all of them before its wave ends.
+// them, and for all of them before its wave ends.  A kernel that keeps
+// descriptors in spilled scalar registers has SPILLED: they come back through a
+// vector instruction, perhaps right before the load (see buffer_of()).
+template <bool SPILLED = false>
 __device__ __forceinline__ void load_to_lds(i4_t rs, uint32_t at, uint32_t offset) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop %3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
-               : "s"(at), "v"(offset), "s"(rs)
+               : "s"(at), "v"(offset), "s"(rs), "n"(SPILLED ? 3 : 0)
                : "memory", "m0");
 }
 // Waits until at most N of the wave's loads are on their way (they land in order).
 template <int N>
 __device__ __forceinline__ void lds_loads_left() {
   asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
-}
-
-// Workgroup barrier that waits for nothing but the other waves: not for LDS
-// reads on their way, as __syncthreads() does.
-__device__ __forceinline__ void bare_barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
 }
 
 // 16 bytes per lane from a range-checked buffer into registers; zeros from

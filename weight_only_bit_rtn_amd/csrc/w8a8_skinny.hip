@@ -74,7 +74,7 @@ __global__ __launch_bounds__((Ring<NT, GATED>::W * 64)) void skinny_kernel(const
       for (int q = 0; q < kLoads; q++) {
         uint32_t at = off[q] + k0 + (o < FR ? 0 : (o - FR) * 16 * K);
         if (k0 + kc[q] >= K) at = 0x80000000u;
-        load_to_lds(rs, to + o * R::kOp + q * 1024, at);
+        load_to_lds<true>(rs, to + o * R::kOp + q * 1024, at);
       }
     }
     if (++ls == steps) {
