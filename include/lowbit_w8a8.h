@@ -33,7 +33,8 @@
  *    [2^14, 2^15); a factor below 2^-29 of the largest loses bits), the sums are fp32,
  *    dx is rounded once.  For the gated block  du = dh act(g),
  *    dg = dh u act'(g)  in fp32 from the given 16-bit g and u.  A token whose
- *    dy (dg, du) holds an infinity or a NaN has an all-NaN dx.
+ *    dy (dg, du) holds an infinity or a NaN, or whose factors dy s_n leave
+ *    fp32's range, has an all-NaN dx.
  *    Sums over n may be split; their order is fixed by the sizes alone, so
  *    results repeat bit for bit.
  *
@@ -45,11 +46,12 @@
  *
  * Shape rules (violations return LOWBIT_ERR_SHAPE): K > 0, K % 32 == 0,
  * K <= LOWBIT_W8A8_MAX_K (the sums are 32-bit); T, N <= LOWBIT_W8A8_MAX_TN,
- * T * N and T * K <= 2^36.  Any N, odd ones too.  T == 0 is an empty problem; N == 0 leaves a product empty and a
- * gradient zero.  A workspace smaller than the *_workspace_bytes value, or not
- * 256-byte aligned, returns LOWBIT_ERR_ARG; calls on one workspace must not
- * overlap.  Workspace sizes of zero allow a null workspace; sizes are those of
- * the current device, on which the call has to be made too.
+ * T * N and T * K <= 2^36.  Any N, odd ones too.  T == 0 is an empty problem;
+ * N == 0 leaves a product empty and a gradient zero.  A workspace smaller than
+ * the *_workspace_bytes value, or not 256-byte aligned, returns LOWBIT_ERR_ARG;
+ * calls on one workspace must not overlap.  Workspace sizes of zero allow a
+ * null workspace; sizes are those of the current device, on which the call has
+ * to be made too.
  */
 #ifndef LOWBIT_W8A8_H
 #define LOWBIT_W8A8_H

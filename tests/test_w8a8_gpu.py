@@ -687,3 +687,37 @@ print("captured")
 """ % root
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=100)
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_outputs_that_share_memory_are_refused(lw):
+    rng = np.random.default_rng(0)
+    w = on_gpu(weights(rng, 64, 64, "sym"))
+    x = activations(rng, 64, 64, "fp16")
+    q = lw.quantize_act(x)
+    both = activations(rng, 96, 64, "fp16")
+    for call in [lambda: lw.linear_w8a8(x, *w, out=x), lambda: lw.linear_w8a8_grad(x, *w, out=x),
+                 lambda: lw.linear_w8a8(both[:64], *w, out=both[32:]),
+                 lambda: lw.quantize_act(x, out={"codes": q["codes"], "scales": q["sums"].view(q["scales"].dtype),
+                                                 "sums": q["sums"]}),
+                 lambda: lw.quantize_act(x, out={"codes": x.view(q["codes"].dtype).view(-1)[:4096].view(64, 64)})]:
+        with pytest.raises(ValueError):
+            call()
+    want = lw.linear_w8a8(both[:32], *w)
+    assert bool((lw.linear_w8a8(both[:32], *w, out=both[64:]) == want).all())
+
+
+@pytest.mark.parametrize("T", [3, 70])
+def test_factors_past_the_range(lw, T):
+    """A token whose factors dy s leave fp32's range is NaN; the others are as ever."""
+    import torch
+    rng = np.random.default_rng(1)
+    codes, scales, zeros = weights(rng, 40, 64, "sym")
+    scales[7] = 4.0
+    w = on_gpu((codes, scales, zeros))
+    dy = activations(rng, T, 40, "bf16")
+    want = lw.linear_w8a8_grad(dy, *w)
+    dy[1, 7] = 3e38
+    got = lw.linear_w8a8_grad(dy, *w)
+    assert bool(got[1].isnan().all())
+    keep = torch.arange(T, device="cuda") != 1
+    assert bool((got[keep] == want[keep]).all()) and not bool(got[keep].isnan().any())

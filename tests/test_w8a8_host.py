@@ -225,3 +225,15 @@ def test_gradients_against_differences(act):
             step[t, k] = e
             d = (loss(x + step) - loss(x - step)) / (2 * e)
             assert abs(d - dx[t, k]) <= 1e-7 * np.abs(dx).max()
+
+
+def test_outputs_apart_from_inputs():
+    """Sharing a byte is refused, lying next to each other is not."""
+    import torch
+    from weight_only_bit_rtn_amd import w8a8
+    buf = torch.zeros(64, dtype=torch.float16)
+    w8a8._apart(buf[:32], "out", buf[32:], torch.zeros(64))
+    w8a8._apart(buf[32:], "out", buf[:32])
+    for out, x in [(buf, buf), (buf[:33], buf[32:]), (buf[10:12], buf), (buf.view(torch.int8)[63:64], buf[31:40])]:
+        with pytest.raises(ValueError):
+            w8a8._apart(out, "out", x)

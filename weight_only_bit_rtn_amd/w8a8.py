@@ -231,6 +231,14 @@ def _out(out, name, shape, dtype, device):
     return out
 
 
+def _apart(out, name, *inputs) -> None:
+    """Refuses an output that shares memory with an input."""
+    lo, hi = out.data_ptr(), out.data_ptr() + out.nbytes
+    for t in inputs:
+        if t.device == out.device and lo < t.data_ptr() + t.nbytes and t.data_ptr() < hi:
+            raise ValueError(f"{name} must not share memory with an input")
+
+
 def _act(act) -> int:
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
@@ -240,7 +248,8 @@ def _act(act) -> int:
 def quantize_act(x, out: dict | None = None) -> dict:
     """Per-token int8 quantization of fp16 or bf16 ``x[T][K]``: a dict with
     ``codes`` (int8 [T][K]), ``scales`` (fp32 [T]) and ``sums`` (int32 [T], the
-    sum of a token's codes), which the products take in place of x."""
+    sum of a token's codes), which the products take instead of x.  ``out``: such
+    a dict to write into."""
     torch = _torch()
     kind = _float_type(x, "x")
     _check_tensor(x, "x", x.dtype)
@@ -250,6 +259,10 @@ def quantize_act(x, out: dict | None = None) -> dict:
     codes = _out(out.get("codes"), "codes", (T, K), torch.int8, dev)
     scales = _out(out.get("scales"), "scales", (T,), torch.float32, dev)
     sums = _out(out.get("sums"), "sums", (T,), torch.int32, dev)
+    if out:
+        _apart(codes, "codes", x)
+        _apart(scales, "scales", x, codes)
+        _apart(sums, "sums", x, codes, scales)
     with _on(dev):
         status = quantize_act_raw(x.data_ptr(), kind, T, K, codes.data_ptr(), scales.data_ptr(),
                                   sums.data_ptr(), _stream_handle(dev))
@@ -266,6 +279,9 @@ def linear_w8a8(x, packed, scales, zeros, out_dtype=None, out=None):
     if k != K:
         raise ValueError("x and the weights must have the same K")
     y = _out(out, "out", (T, N), out_dtype, dev)
+    if out is not None:
+        _apart(y, "out", *((x["codes"], x["scales"], x["sums"]) if isinstance(x, dict) else (x,)),
+               packed, scales, zeros)
     with _on(dev):
         need = linear_w8a8_workspace_bytes(T, N, K, ptrs[1])
         ws, at = _workspace(need, "lowbit_linear_w8a8_workspace_bytes", dev)
@@ -314,6 +330,8 @@ def linear_w8a8_grad(dy, packed, scales, zeros, out=None):
     if dy.shape[1] != N:
         raise ValueError("dy.shape[1] must be the weights' N")
     dx = _out(out, "out", (T, K), dy.dtype, dev)
+    if out is not None:
+        _apart(dx, "out", dy, packed, scales, zeros)
     with _on(dev):
         need = linear_w8a8_grad_workspace_bytes(T, N, K)
         ws, at = _workspace(need, "lowbit_linear_w8a8_grad_workspace_bytes", dev)
