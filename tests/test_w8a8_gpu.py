@@ -721,3 +721,10 @@ def test_factors_past_the_range(lw, T):
     assert bool(got[1].isnan().all())
     keep = torch.arange(T, device="cuda") != 1
     assert bool((got[keep] == want[keep]).all()) and not bool(got[keep].isnan().any())
+
+
+@pytest.mark.parametrize("shape", [(516, 8057, 3200), (130, 5497, 3424), (396, 8456, 32), (147, 9000, 4448),
+                                   (132, 2715, 3424), (131, 8564, 32), (533, 8187, 3136)], ids=str)
+def test_every_plan_of_small_tiles(lw, shape):
+    """192 x 192 tiles: whole and shared out, linear and gated."""
+    test_every_tile_plan(lw, shape)

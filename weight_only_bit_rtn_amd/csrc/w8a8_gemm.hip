@@ -41,11 +41,11 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, 
   constexpr int MW = MT / WM, NW = NT / WN;  // wave tile
   constexpr int FM = MW / 16, FN = NW / 16;  // its fragments
   constexpr int NO = GATED ? NT / 2 : NT;    // output columns of a tile
-  // 1 KiB loads per wave and step; where the rows do not come out even, the
-  // last go to a place of their own, so that every wave counts as many
+  // 1 KiB loads per wave and step; where an operand's rows do not come out even,
+  // the last go to a place of their own, so that every wave counts as many
   constexpr int kA = MT / 16, kB = NT / 16;
-  constexpr int LA = kA / kWaves, LB = (kB + kWaves - 1) / kWaves, kLoads = LA + LB;
-  static_assert(LA * kWaves == kA && MT % (16 * WM) == 0 && NT % (16 * WN) == 0, "whole loads");
+  constexpr int LA = (kA + kWaves - 1) / kWaves, LB = (kB + kWaves - 1) / kWaves, kLoads = LA + LB;
+  static_assert(MT % (16 * WM) == 0 && NT % (16 * WN) == 0, "whole loads");
   static_assert(!GATED || FN % 2 == 0, "gate and up halves");
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   constexpr int kBuf = (MT + NT) * kStep;
@@ -75,15 +75,16 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, 
   const uint32_t r16 = lane >> 2, chunk = ((lane & 3) ^ (-(lane >> 4) & 3)) * 16;
   uint32_t oa[LA], ob[LB];
   uint32_t la[LA], lb[LB];
+  bool up[LB], spare[LB], spare_a[LA];
   const uint32_t base = lds_address(lds);
   const uint32_t kend = min((uint32_t)s1 * kStep, K);
 #pragma unroll
   for (int i = 0; i < LA; i++) {
     const int row = (wave + i * kWaves) * 16;
-    oa[i] = (row + r16) * K + chunk;
-    la[i] = base + row * kStep;
+    spare_a[i] = kA % kWaves != 0 && row >= MT;
+    oa[i] = spare_a[i] ? 0x80000000u : (row + r16) * K + chunk;
+    la[i] = base + (spare_a[i] ? NB * kBuf : row * kStep);
   }
-  bool up[LB], spare[LB];
 #pragma unroll
   for (int i = 0; i < LB; i++) {
     // LDS rows of the weight tile, in order; of each wave's NW rows the first
@@ -100,7 +101,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, 
     const uint32_t k0 = (uint32_t)s * kStep, buf = (uint32_t)(s % NB) * kBuf;
     const uint32_t add = k0 + chunk < kend ? k0 : 0x80000000u;
     if (i < LA)
-      load_to_lds(ra, la[i] + buf, oa[i] + add);
+      load_to_lds(ra, la[i] + (spare_a[i] ? 0 : buf), spare_a[i] ? oa[i] : oa[i] + add);
     else
       load_to_lds(up[i - LA] ? ru : rg, lb[i - LA] + (spare[i - LA] ? 0 : buf),
                   spare[i - LA] ? ob[i - LA] : ob[i - LA] + add);
@@ -233,7 +234,8 @@ __global__ __launch_bounds__(256) void w8a8_join_kernel(const GemmArgs p, const 
 
 template <int MT, int NT, int WM, int WN, int NB, bool GATED>
 hipError_t launch_tile(const GemmArgs& p, const TilePlan& plan, i4_t* parts, hipStream_t stream) {
-  constexpr int bytes = NB * (MT + NT) * kStep + (NT / 16 % (WM * WN) ? 1024 : 0);
+  constexpr bool spare = MT / 16 % (WM * WN) != 0 || NT / 16 % (WM * WN) != 0;
+  constexpr int bytes = NB * (MT + NT) * kStep + (spare ? 1024 : 0);
   auto kernel = w8a8_kernel<MT, NT, WM, WN, NB, GATED>;
   hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), bytes);
   if (e != hipSuccess) return e;
@@ -253,8 +255,12 @@ struct TileShape {
   int mt, nt;
   double step_us;
 };
+// The less LDS traffic per output the larger the tile; the smaller ones are for
+// sizes that would leave CUs idle or pad much (with the last shape and without:
+// gated 333x11008x4096 51.4 / 58.1 us, linear 2000x4096x4096 59.0 / 65.1; six
+// waves instead of its eight: 55.9 on the first).
 constexpr TileShape kShapes[] = {
-    {128, 128, 0.40}, {256, 256, 1.03}, {256, 192, 0.90}, {256, 384, 1.42}};
+    {128, 128, 0.40}, {256, 256, 1.03}, {256, 192, 0.90}, {256, 384, 1.42}, {192, 192, 0.79}};
 
 // The shape that should finish first.
 struct GemmPlan {
@@ -269,7 +275,7 @@ GemmPlan gemm_plan(int64_t T, int64_t N, int64_t K, bool gated) {
   const int64_t rows = gated ? 2 * N : N;
   GemmPlan best{};
   double least = 0;
-  for (int i = 0; i < 4; i++) {
+  for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); i++) {
     const TileShape& t = kShapes[i];
     double us;
     const TilePlan plan =
@@ -334,7 +340,8 @@ hipError_t launch(const Activations& x, int64_t T, const W8& w0, const W8& w1, i
   if (plan.shape == 0) return launch_tile<128, 128, 2, 2, 4, GATED>(p, plan.tiles, parts, stream);
   if (plan.shape == 1) return launch_tile<256, 256, 2, 4, 4, GATED>(p, plan.tiles, parts, stream);
   if (plan.shape == 2) return launch_tile<256, 192, 4, 2, 4, GATED>(p, plan.tiles, parts, stream);
-  return launch_tile<256, 384, 2, 4, 4, GATED>(p, plan.tiles, parts, stream);
+  if (plan.shape == 3) return launch_tile<256, 384, 2, 4, 4, GATED>(p, plan.tiles, parts, stream);
+  return launch_tile<192, 192, 4, 2, 4, GATED>(p, plan.tiles, parts, stream);
 }
 
 }  // namespace
