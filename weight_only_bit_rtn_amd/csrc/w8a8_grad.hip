@@ -476,10 +476,11 @@ struct TileShape {
 };
 constexpr TileShape kShapes[] = {{16, 128, 0.40, 0.32},  {32, 128, 0.40, 0.32},
                                  {64, 128, 0.50, 0.40},  {128, 128, 0.74, 0.55},
-                                 {256, 256, 1.60, 1.60}, {256, 192, 1.20, 1.20}};
+                                 {256, 256, 1.60, 1.60}, {256, 192, 1.20, 1.20},
+                                 {64, 256, 0.64, 0.64}};
 
-// The shape that should finish first; of the first four, the least that holds
-// all tokens, or the last.
+// The shape that should finish first, of those that hold T tokens without
+// waste: the first or the second, the third and the last, or the fourth and on.
 struct GradPlan {
   TilePlan tiles;
   int shape;
@@ -489,9 +490,11 @@ struct GradPlan {
 };
 GradPlan grad_plan(int64_t T, int64_t K, int steps) {
   const int cus = device_cu_count();
+  const int from = T <= 16 ? 0 : T <= 32 ? 1 : T <= 64 ? 2 : 3;
+  const int shapes[] = {from, from == 2 ? 6 : from == 3 ? 4 : from, from == 3 ? 5 : from};
   GradPlan best{};
   double least = 0;
-  for (int i = T <= 16 ? 0 : T <= 32 ? 1 : T <= 64 ? 2 : 3; i < 6; i++) {
+  for (int i : shapes) {
     const TileShape& t = kShapes[i];
     double us;
     const TilePlan plan = plan_tiles((T + t.mt - 1) / t.mt, (K + t.kt - 1) / t.kt, cus, steps,
@@ -500,7 +503,6 @@ GradPlan grad_plan(int64_t T, int64_t K, int steps) {
       best = {plan, i};
       least = us;
     }
-    if (T <= 64) break;
   }
   return best;
 }
@@ -570,8 +572,10 @@ hipError_t launch_w8a8_grad(const void* dh, const void* gate, const void* up, in
       return launch_tile<128, 128, 2, 2, 3>(p, plan.tiles, parts, stream);
     case 4:
       return launch_tile<256, 256, 2, 4, 3>(p, plan.tiles, parts, stream);
-    default:
+    case 5:
       return launch_tile<256, 192, 2, 4, 3>(p, plan.tiles, parts, stream);
+    default:
+      return launch_tile<64, 256, 1, 8, 3>(p, plan.tiles, parts, stream);
   }
 }
 
