@@ -32,7 +32,7 @@ struct PrepArgs {
   int32_t* e;
   uint16_t* dgate;
   uint16_t* dup;
-  int N, pitch, half, act, bf16;
+  int N, pitch, half;
 };
 
 __device__ __forceinline__ float block_sum(float v, float* red, int tid) {
@@ -54,26 +54,30 @@ __device__ __forceinline__ float block_max(float v, float* red, int tid) {
   return v;
 }
 
-// Eight values of a row from chunk c on; WHOLE: N % 8 == 0, so that rows and
-// chunks lie at 16 bytes.  Positions past N: zeros read, nothing written.
+// Eight values of a row from chunk c on.  WHOLE (N % 8 == 0): rows and chunks
+// lie at 16 bytes.  Otherwise a row may lie at any 2-byte address, and its last
+// chunk is not full.  Positions past N: zeros read, nothing written.
 template <bool WHOLE>
-__device__ __forceinline__ us8_t get8(const uint16_t* row, int c, int N) {
-  if constexpr (WHOLE) return reinterpret_cast<const us8_t*>(row)[c];
+__device__ __forceinline__ us8_t get8(const uint16_t* row, int c, int N, bool full) {
   us8_t v = {};
-  if (c * 8 + 8 <= N) {  // a row of odd length: 16 bytes at any 2-byte address
+  if (WHOLE) {
+    v = reinterpret_cast<const us8_t*>(row)[c];
+  } else if (full) {
     __builtin_memcpy(&v, row + c * 8, 16);
-  } else {
+  } else {  // no branches: all loads under way together
 #pragma unroll
-    for (int j = 0; j < 8; j++)
-      if (c * 8 + j < N) v[j] = row[c * 8 + j];
+    for (int j = 0; j < 8; j++) {
+      const uint16_t x = row[min(c * 8 + j, N - 1)];
+      v[j] = c * 8 + j < N ? x : 0;
+    }
   }
   return v;
 }
 template <bool WHOLE>
-__device__ __forceinline__ void put8(uint16_t* row, int c, int N, us8_t v) {
+__device__ __forceinline__ void put8(uint16_t* row, int c, int N, bool full, us8_t v) {
   if constexpr (WHOLE) {
     reinterpret_cast<us8_t*>(row)[c] = v;
-  } else if (c * 8 + 8 <= N) {
+  } else if (full) {
     __builtin_memcpy(row + c * 8, &v, 16);
   } else {
 #pragma unroll
@@ -84,26 +88,32 @@ __device__ __forceinline__ void put8(uint16_t* row, int c, int N, us8_t v) {
 
 // The factors d s of chunk c (gated: of the gate and the up part), in fp32, the
 // largest |d s| so far and whether every d is finite; `write`: dg and du go out.
-template <bool GATED, bool WHOLE>
+template <int ACT, bool BF, bool WHOLE>
 __device__ __forceinline__ void factors8(const PrepArgs& p, int64_t row, int c, bool write,
-                                         float (&a)[GATED ? 2 : 1][8], float& top, bool& finite) {
+                                         float (&a)[ACT < 0 ? 1 : 2][8], float& top, bool& finite) {
+  constexpr bool GATED = ACT >= 0, bf = BF;
   constexpr int M = GATED ? 2 : 1;
-  const bool bf = p.bf16;
-  const us8_t d = get8<WHOLE>(p.d + row * p.N, c, p.N);
-  us8_t g, u, og, ou;
-  if constexpr (GATED) {
-    g = get8<WHOLE>(p.gate + row * p.N, c, p.N);
-    u = get8<WHOLE>(p.up + row * p.N, c, p.N);
-  }
-  us8_t sc[M];
+  const bool full = WHOLE || c * 8 + 8 <= p.N;
+  us8_t d, g, u, og, ou, sc[M];
+  auto read = [&](bool f) {  // one branch for all, so that they are under way together
+    d = get8<WHOLE>(p.d + row * p.N, c, p.N, f);
+    if constexpr (GATED) {
+      g = get8<WHOLE>(p.gate + row * p.N, c, p.N, f);
+      u = get8<WHOLE>(p.up + row * p.N, c, p.N, f);
+    }
 #pragma unroll
-  for (int m = 0; m < M; m++) sc[m] = get8<WHOLE>(p.w[m].scales, c, p.N);
+    for (int m = 0; m < M; m++) sc[m] = get8<WHOLE>(p.w[m].scales, c, p.N, f);
+  };
+  if (full)
+    read(true);
+  else
+    read(false);
 #pragma unroll
   for (int j = 0; j < 8; j++) {
     float d0 = elem_to_f32(d[j], bf), d1 = 0;
     if constexpr (GATED) {
       float f, df;
-      act_value_slope(elem_to_f32(g[j], bf), p.act, f, df);
+      act_value_slope(elem_to_f32(g[j], bf), ACT, f, df);
       d1 = d0 * f;
       d0 = d0 * elem_to_f32(u[j], bf) * df;
       og[j] = f32_to_elem(d0, bf);
@@ -116,20 +126,24 @@ __device__ __forceinline__ void factors8(const PrepArgs& p, int64_t row, int c, 
     for (int m = 0; m < M; m++) top = fmaxf(top, fabsf(a[m][j]));
   }
   if (GATED && write) {
-    put8<WHOLE>(p.dgate + row * p.N, c, p.N, og);
-    put8<WHOLE>(p.dup + row * p.N, c, p.N, ou);
+    put8<WHOLE>(p.dgate + row * p.N, c, p.N, full, og);
+    put8<WHOLE>(p.dup + row * p.N, c, p.N, full, ou);
   }
 }
 
-// One workgroup per token.  NC > 0: its factors stay in registers, NC chunks
-// per thread, between their largest and their rounding, so the inputs are read
-// once; NC == 0 (rows longer than that): they are made twice.  Bound by HBM;
-// each row's scales and zero points come from L2.  4096 tokens of 2 x 28672:
-// 340 us, 4.8 TB/s.
-template <bool GATED, int NC, bool WHOLE>
+// One workgroup per token.  ACT: the gated block's activation, or -1 for the
+// linear layer.  NC > 0: the factors stay in registers, NC chunks per thread,
+// between their largest and their rounding, so the inputs are read once; NC == 0
+// (rows longer than that): they are made twice.  Bound by HBM with many tokens
+// (4096 of 2 x 28672, dg and du written too: 340 us, 4.8 TB/s), by the vector
+// ALUs of a token's CU with few (64 of 2 x 28672 14.7 us; 17.6 with the
+// activation and the type decided at run time, whose branches part the values).
+// Each row's scales and zero points come from L2.  Rows that lie at 2 bytes:
+// 61 of 2 x 11007 15.8 us, of 2 x 11008 7.2.
+template <int ACT, bool BF, int NC, bool WHOLE>
 __global__ __launch_bounds__(1024) void grad_prep_kernel(const PrepArgs p) {
   __shared__ float red[16];
-  constexpr int M = GATED ? 2 : 1;
+  constexpr int M = ACT < 0 ? 1 : 2;
   const int tid = threadIdx.x, nt = blockDim.x, chunks = (p.N + 7) / 8, all = p.half / 8;
   const int64_t row = blockIdx.x;
   float held[NC > 0 ? NC : 1][M][8];
@@ -140,11 +154,11 @@ __global__ __launch_bounds__(1024) void grad_prep_kernel(const PrepArgs p) {
 #pragma unroll
     for (int i = 0; i < NC; i++) {
       const int c = tid + i * nt;
-      if (c < chunks) factors8<GATED, WHOLE>(p, row, c, write, held[i], top, finite);
+      if (c < chunks) factors8<ACT, BF, WHOLE>(p, row, c, write, held[i], top, finite);
     }
   } else {
     for (int c = tid; c < chunks; c += nt)
-      factors8<GATED, WHOLE>(p, row, c, write, held[0], top, finite);
+      factors8<ACT, BF, WHOLE>(p, row, c, write, held[0], top, finite);
   }
   top = block_max(finite ? top : INFINITY, red, tid);
   const bool ok = top < INFINITY;
@@ -180,7 +194,7 @@ __global__ __launch_bounds__(1024) void grad_prep_kernel(const PrepArgs p) {
     }
   } else {
     for (int c = tid; c < all; c += nt) {
-      if (c < chunks) factors8<GATED, WHOLE>(p, row, c, false, held[0], top, finite);
+      if (c < chunks) factors8<ACT, BF, WHOLE>(p, row, c, false, held[0], top, finite);
       round8(c, held[0]);
     }
   }
@@ -441,27 +455,30 @@ hipError_t launch_tile(const GradArgs& p, const TilePlan& plan, f4_t* parts, hip
   return hipGetLastError();
 }
 
-template <bool GATED, bool WHOLE>
+template <int ACT, bool BF, bool WHOLE>
 void launch_prep_rows(const PrepArgs& q, int64_t T, hipStream_t stream) {
   const dim3 grid((unsigned)T);
   const int chunks = q.half / 8;
   int nt = 64;
   while (nt < 1024 && nt < chunks) nt *= 2;
   if (chunks <= nt)
-    grad_prep_kernel<GATED, 1, WHOLE><<<grid, dim3(nt), 0, stream>>>(q);
+    grad_prep_kernel<ACT, BF, 1, WHOLE><<<grid, dim3(nt), 0, stream>>>(q);
   else if (chunks <= 2 * nt)
-    grad_prep_kernel<GATED, 2, WHOLE><<<grid, dim3(nt), 0, stream>>>(q);
+    grad_prep_kernel<ACT, BF, 2, WHOLE><<<grid, dim3(nt), 0, stream>>>(q);
   else if (chunks <= 4 * nt)
-    grad_prep_kernel<GATED, 4, WHOLE><<<grid, dim3(nt), 0, stream>>>(q);
+    grad_prep_kernel<ACT, BF, 4, WHOLE><<<grid, dim3(nt), 0, stream>>>(q);
   else
-    grad_prep_kernel<GATED, 0, WHOLE><<<grid, dim3(nt), 0, stream>>>(q);
+    grad_prep_kernel<ACT, BF, 0, WHOLE><<<grid, dim3(nt), 0, stream>>>(q);
 }
-template <bool GATED>
-void launch_prep(const PrepArgs& q, int64_t T, hipStream_t stream) {
-  if (q.N % 8 == 0)
-    launch_prep_rows<GATED, true>(q, T, stream);
+template <int ACT>
+void launch_prep(const PrepArgs& q, int64_t T, bool bf16, hipStream_t stream) {
+  const bool whole = q.N % 8 == 0;
+  if (bf16)
+    whole ? launch_prep_rows<ACT, true, true>(q, T, stream)
+          : launch_prep_rows<ACT, true, false>(q, T, stream);
   else
-    launch_prep_rows<GATED, false>(q, T, stream);
+    whole ? launch_prep_rows<ACT, false, true>(q, T, stream)
+          : launch_prep_rows<ACT, false, false>(q, T, stream);
 }
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -536,12 +553,13 @@ hipError_t launch_w8a8_grad(const void* dh, const void* gate, const void* up, in
   q.N = (int)N;
   q.pitch = (int)pitch;
   q.half = (int)half;
-  q.act = act;
-  q.bf16 = dtype == kBF16;
-  if (gated)
-    launch_prep<true>(q, T, stream);
+  const bool bf16 = dtype == kBF16;
+  if (!gated)
+    launch_prep<-1>(q, T, bf16, stream);
+  else if (act == kSilu)
+    launch_prep<kSilu>(q, T, bf16, stream);
   else
-    launch_prep<false>(q, T, stream);
+    launch_prep<kGeluTanh>(q, T, bf16, stream);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   GradArgs p{};
@@ -557,7 +575,7 @@ hipError_t launch_w8a8_grad(const void* dh, const void* gate, const void* up, in
   p.pitch = (int)pitch;
   p.half_steps = (int)(half / kStepN);
   p.steps = (int)(pitch / kStepN);
-  p.bf16 = q.bf16;
+  p.bf16 = bf16;
   const GradPlan plan = grad_plan(T, K, p.steps);
   auto* parts =
       reinterpret_cast<f4_t*>(reinterpret_cast<uint8_t*>(q.e) + up256((size_t)T * 4));
