@@ -232,10 +232,12 @@ def _out(out, name, shape, dtype, device):
 
 
 def _apart(out, name, *inputs) -> None:
-    """Refuses an output that shares memory with an input."""
-    lo, hi = out.data_ptr(), out.data_ptr() + out.nbytes
+    """Refuses an output that shares memory with an input of its device."""
+    lo = out.data_ptr()
+    hi = lo + out.nbytes
     for t in inputs:
-        if t.device == out.device and lo < t.data_ptr() + t.nbytes and t.data_ptr() < hi:
+        at = t.data_ptr()
+        if at < hi and lo < at + t.nbytes:
             raise ValueError(f"{name} must not share memory with an input")
 
 
