@@ -229,7 +229,7 @@ template <int KT>
 __device__ __forceinline__ int slot_of(int n, int c) {
   if constexpr (KT % 256 == 0) return c ^ (n & 15);
   if constexpr (KT == 128) return c ^ ((n >> 1) & 7);
-  return (c & ~3) | ((c + (n >> 2)) & 3);  // 64 and 192
+  return (c & ~3) | ((c + (n >> 2)) & 3);  // 192
 }
 template <int KT>
 __device__ __forceinline__ int chunk_at(int n, int slot) {
@@ -252,6 +252,13 @@ __device__ __forceinline__ void store_dx(const GradArgs& p, f4_t sum, float r, i
 // column per lane, which the transposing LDS read delivers (16 lanes read 8
 // rows of 16 bytes and get a column each).  A step is two halves of 32 rows:
 // while one half is multiplied, the operands of the next are read.
+//
+// 4096 x (2 x 28672) x 8192 takes 2.65-2.8 ms, 1.4 PFLOP/s: the matrix cores
+// are busy in 73% of the clocks, at 1.8 GHz, which is all that power allows here
+// (products from registers alone reach 2.0 PFLOP/s at 1.9 GHz), and LDS moves
+// 208 KiB per step and CU in 2800 clocks.  Slower there: four waves of 128 x 128
+// (2.92 ms), steps of 32 rows (3.1 ms).  The small tiles wait for the weights
+// from HBM: 61 x (2 x 11008) x 4096 takes 19.5 us, 4.6 TB/s.
 template <int MT, int KT, int WM, int WN, int NB>
 __global__ __launch_bounds__(WM* WN * 64, 2) void grad_kernel(const GradArgs p, const TilePlan plan,
                                                                  f4_t* __restrict__ parts) {
@@ -486,7 +493,10 @@ int64_t padded(int64_t N) { return (N + kStepN - 1) / kStepN * kStepN; }
 
 // Tile shapes: tokens, columns of dx, and what a step of 64 weight rows of one
 // tile takes of a CU's time when the CU has no other workgroup, and when it has
-// (us, measured).
+// (us, measured).  The last reads the tokens' factors half as often as the third
+// and pays where the weights are large (gated 64x28672x8192 125 / 145 us,
+// 61x11008x4096 33.1 / 33.4); for 16 or 32 tokens, whose factors are fewer, 256
+// columns gave nothing (16x28672x8192 117 / 122, 10x12288x12288 40.5 / 37.5).
 struct TileShape {
   int mt, kt;
   double alone_us, shared_us;
