@@ -728,3 +728,24 @@ def test_factors_past_the_range(lw, T):
 def test_every_plan_of_small_tiles(lw, shape):
     """192 x 192 tiles: whole and shared out, linear and gated."""
     test_every_tile_plan(lw, shape)
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("T,N,K", [(1, 2000, 512), (2, 1999, 544), (4, 1000, 96), (13, 1501, 544), (33, 1000, 544),
+                                   (64, 777, 1056), (100, 500, 320), (520, 1031, 4096), (516, 8057, 224)])
+def test_products_are_the_fp32_value(lw, T, N, K, kind):
+    """fl32(fl32(S s) d), rounded to the output type: one value, bit for bit, whichever kernel makes it."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(T)
+    w, wu = random_weights(g, N, K), random_weights(g, N, K)
+    x = torch.randn(T, K, generator=g, device="cuda").to(types()[kind])
+    q = lw.quantize_act(x)
+
+    def value(w):
+        d = q["codes"].double() @ integers(w).t()
+        return (q["scales"][:, None] * w[1].float().t() * d.float()).to(x.dtype)
+
+    assert bool((lw.linear_w8a8(x, *w) == value(w)).all())
+    assert bool((lw.linear_w8a8(q, *w, out_dtype=x.dtype) == value(w)).all())
+    _, gate, up = lw.gated_w8a8(x, *w, *wu, save=True)
+    assert bool((gate == value(w)).all()) and bool((up == value(wu)).all())

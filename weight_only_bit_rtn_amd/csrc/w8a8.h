@@ -25,8 +25,12 @@ struct W8 {
 __device__ __forceinline__ float elem_to_f32(uint16_t bits, bool bf16) {
   return bf16 ? __builtin_bit_cast(float, (uint32_t)bits << 16) : h_bits_to_f32(bits);
 }
-// Round to nearest even, once, to the output type.
+// Rounds an fp32 value to nearest even to the output type.  The value is one, in
+// every kernel: left alone the compiler joins some kernels' last product with the
+// conversion (v_fma_mixlo_f16), which rounds the exact product, and the same
+// output would differ from kernel to kernel in the last bit.
 __device__ __forceinline__ uint16_t f32_to_elem(float v, bool bf16) {
+  asm volatile("" : "+v"(v));
   return bf16 ? __builtin_bit_cast(uint16_t, (__bf16)v) : f32_to_h_bits(v);
 }
 
