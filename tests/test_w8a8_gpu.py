@@ -749,3 +749,23 @@ def test_products_are_the_fp32_value(lw, T, N, K, kind):
     assert bool((lw.linear_w8a8(q, *w, out_dtype=x.dtype) == value(w)).all())
     _, gate, up = lw.gated_w8a8(x, *w, *wu, save=True)
     assert bool((gate == value(w)).all()) and bool((up == value(wu)).all())
+
+
+@pytest.mark.parametrize("shape", [(85, 22, 2464), (630, 20, 32), (2562, 26, 4032), (205, 8807, 32), (407, 8200, 4256),
+                                   (670, 5380, 96), (528, 6586, 4128), (1287, 5405, 96), (520, 6782, 32),
+                                   (1366, 8139, 32), (2087, 7317, 32), (129, 5767, 32), (275, 5468, 4064),
+                                   (138, 8885, 96), (419, 8308, 3552), (129, 8218, 3744), (305, 8827, 96),
+                                   (523, 8348, 3552), (129, 8335, 32), (562, 8736, 32), (1371, 5479, 2016),
+                                   (806, 8360, 32), (1289, 8190, 1568), (21, 30, 32)], ids=str)
+def test_every_plan_of_long_steps(lw, shape):
+    """Steps of 64 and 128 values, every shape whole and shared out, linear and gated."""
+    test_every_tile_plan(lw, shape)
+
+
+@pytest.mark.parametrize("shape", [(24, 10852, 9568), (61, 8037, 8032), (19, 22688, 960), (52, 17920, 960),
+                                   (31, 36162, 4608), (60, 33771, 2560), (52, 39997, 992), (23, 8151, 9472),
+                                   (61, 4065, 12768), (32, 12369, 1024), (64, 10635, 1024), (30, 34159, 5120),
+                                   (54, 18606, 4480), (63, 24569, 1280)], ids=str)
+def test_few_tokens_by_large_weights(lw, shape):
+    """17 to 64 tokens where tiles take over from the rings, whole and shared out."""
+    test_every_tile_plan(lw, shape)

@@ -262,8 +262,10 @@ constexpr int kFusedMost = 16384;
 bool few_takes(int64_t T, int64_t K, bool gated);
 hipError_t launch_few(const GemmArgs& p, bool gated, hipStream_t stream);
 
-// Products of at most 64 tokens (w8a8_skinny.hip).
+// Products of at most 64 tokens (w8a8_skinny.hip), up to 16 in any case, and the
+// time that they should take.
 constexpr int kSkinnyMostT = 64;
+double skinny_us(int64_t T, int64_t N, int64_t K, bool gated);
 hipError_t launch_skinny(const GemmArgs& p, bool gated, hipStream_t stream);
 
 hipError_t launch_quantize_act(const void* x, int dtype, int64_t T, int64_t K, int8_t* codes,

@@ -12,20 +12,18 @@
 namespace lowbit {
 namespace {
 
-constexpr int kStep = 64;    // bytes (values) of k per pipeline step
-
 // One workgroup of WM x WN waves computes MT tokens by NT weight rows (gated:
 // NT / 2 rows of each matrix, the wave's first half gate, its second half up,
 // so a lane holds both projections of an output).
 //
-// Steps of 64 k are staged in LDS by direct loads on a ring of NB buffers, one
-// barrier per step.  A row of a step is 4 chunks of 16 bytes; chunk c of row r
-// lies at c ^ (-(r / 4) & 3), so that the rows one operand read touches at a
-// time lie in different banks (no conflicts counted).  Values past the row's
-// end, tokens past T and rows past N come as zeros from the buffers' range
-// check.
+// Steps of 64 SUB k are staged in LDS by direct loads on a ring of NB buffers,
+// one barrier per step.  A row of a step is 4 SUB chunks of 16 bytes; chunk c of
+// row r lies at c ^ (-(r / 4) & 3), or c ^ (r & 7) with SUB == 2, so that the
+// rows one operand read touches at a time lie in different banks (no conflicts
+// counted).  Values past the row's end, tokens past T and rows past N come as
+// zeros from the buffers' range check.
 //
-// What bounds it is LDS: 64 bytes per clock and CU, measured for ds_read_b128
+// What bounds the large tiles is LDS: 64 bytes per clock and CU, measured for ds_read_b128
 // in any conflict-free pattern.  256 x 256 outputs want 96 KiB of operand reads
 // (eight waves of 128 x 64) and 32 KiB written per step, about 1800 clocks for
 // 1024 of matrix work; 256 x 384 (128 x 96 per wave, the most that 256
@@ -34,16 +32,18 @@ constexpr int kStep = 64;    // bytes (values) of k per pipeline step
 // near 1.9 GHz.  Slower there: 128 x 128 per wave with one wave per SIMD (a
 // third fewer reads, but a lone wave cannot issue fast enough: 577 us), weights
 // straight from L2 into registers (750 us), 32x32x32 products (620 us).
-template <int MT, int NT, int WM, int WN, int NB, bool GATED>
+template <int MT, int NT, int WM, int WN, int NB, int SUB, bool GATED>
 __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, const TilePlan plan,
                                                                  i4_t* __restrict__ parts) {
   constexpr int kWaves = WM * WN;
   constexpr int MW = MT / WM, NW = NT / WN;  // wave tile
   constexpr int FM = MW / 16, FN = NW / 16;  // its fragments
   constexpr int NO = GATED ? NT / 2 : NT;    // output columns of a tile
-  // 1 KiB loads per wave and step; where an operand's rows do not come out even,
-  // the last go to a place of their own, so that every wave counts as many
-  constexpr int kA = MT / 16, kB = NT / 16;
+  constexpr int kStep = 64 * SUB, kChunks = 4 * SUB;  // bytes and chunks of a row per step
+  // 1 KiB loads of 16 / SUB rows; where an operand's do not come out even among the
+  // waves, the last go to a place of their own, so that every wave counts as many
+  constexpr int kRows = 16 / SUB;
+  constexpr int kA = MT / kRows, kB = NT / kRows;
   constexpr int LA = (kA + kWaves - 1) / kWaves, LB = (kB + kWaves - 1) / kWaves, kLoads = LA + LB;
   static_assert(MT % (16 * WM) == 0 && NT % (16 * WN) == 0, "whole loads");
   static_assert(!GATED || FN % 2 == 0, "gate and up halves");
@@ -71,8 +71,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, 
   const auto rg = buffer_of(p.w[0].codes + (int64_t)n0 * K, wbytes);
   const auto ru = GATED ? buffer_of(p.w[1].codes + (int64_t)n0 * K, wbytes) : rg;
 
-  // a load covers 16 rows of 64 bytes: lane l brings chunk (l & 3) ^ swizzle of row l >> 2
-  const uint32_t r16 = lane >> 2, chunk = ((lane & 3) ^ (-(lane >> 4) & 3)) * 16;
+  // lane l of a load brings the chunk that lies at slot l % kChunks of its row l / kChunks
+  auto swizzle = [](int r) { return SUB == 1 ? -(r >> 2) & 3 : r & 7; };
+  const uint32_t rl = lane / kChunks;
+  const uint32_t chunk = ((lane % kChunks) ^ swizzle(rl)) * 16;
   uint32_t oa[LA], ob[LB];
   uint32_t la[LA], lb[LB];
   bool up[LB], spare[LB], spare_a[LA];
@@ -80,20 +82,20 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, 
   const uint32_t kend = min((uint32_t)s1 * kStep, K);
 #pragma unroll
   for (int i = 0; i < LA; i++) {
-    const int row = (wave + i * kWaves) * 16;
+    const int row = (wave + i * kWaves) * kRows;
     spare_a[i] = kA % kWaves != 0 && row >= MT;
-    oa[i] = spare_a[i] ? 0x80000000u : (row + r16) * K + chunk;
+    oa[i] = spare_a[i] ? 0x80000000u : (row + rl) * K + chunk;
     la[i] = base + (spare_a[i] ? NB * kBuf : row * kStep);
   }
 #pragma unroll
   for (int i = 0; i < LB; i++) {
     // LDS rows of the weight tile, in order; of each wave's NW rows the first
     // half is gate rows, the second up rows
-    const int slot = (wave + i * kWaves) * 16, in = slot % NW;
+    const int slot = (wave + i * kWaves) * kRows, in = slot % NW;
     up[i] = GATED && in >= NW / 2;
     spare[i] = kB % kWaves != 0 && slot >= NT;
     const int row = GATED ? slot / NW * (NW / 2) + in % (NW / 2) : slot;
-    ob[i] = spare[i] ? 0x80000000u : (row + r16) * K + chunk;
+    ob[i] = spare[i] ? 0x80000000u : (row + rl) * K + chunk;
     lb[i] = base + (spare[i] ? NB * kBuf : (MT + slot) * kStep);
   }
   // load i of the LA + LB of step s; past the share's last step it brings zeros
@@ -113,41 +115,46 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, 
 #pragma unroll
     for (int j = 0; j < FM; j++) acc[i][j] = i4_t{0, 0, 0, 0};
 
-  // operands from LDS: row lane % 16, chunk lane / 16
-  const uint32_t swizzled = (h ^ (-(i16 >> 2) & 3)) * 16;
-  const uint32_t ra0 = (wm * MW + i16) * kStep + swizzled, rb0 = (MT + wn * NW + i16) * kStep + swizzled;
-  auto tokens = [&](int s, int j) {
-    return *reinterpret_cast<const i4_t*>(lds + s % NB * kBuf + ra0 + j * 16 * kStep);
+  // operands from LDS: row lane % 16, chunk lane / 16 of each 64 bytes
+  const uint32_t ra0 = (wm * MW + i16) * kStep, rb0 = (MT + wn * NW + i16) * kStep;
+  uint32_t at[SUB];
+#pragma unroll
+  for (int q = 0; q < SUB; q++) at[q] = ((q * 4 + h) ^ swizzle(i16)) * 16;
+  auto tokens = [&](int s, int q, int j) {
+    return *reinterpret_cast<const i4_t*>(lds + s % NB * kBuf + ra0 + at[q] + j * 16 * kStep);
   };
-  auto rows = [&](int s, int i) {
-    return *reinterpret_cast<const i4_t*>(lds + s % NB * kBuf + rb0 + i * 16 * kStep);
+  auto rows = [&](int s, int q, int i) {
+    return *reinterpret_cast<const i4_t*>(lds + s % NB * kBuf + rb0 + at[q] + i * 16 * kStep);
   };
-  // One step: its tokens are in fa and its first two row operands in fb.  The
-  // last row operand's products are the last to use the tokens; each token's is
-  // followed by the read of the next step's, behind the step's barrier.
+  // One step: its first tokens are in fa and its first two row operands in fb.
+  // The last row operand's products of each 64 bytes are the last to use the
+  // tokens; each token's is followed by the read of the next, in the step's last
+  // products behind its barrier.
+  constexpr int kAll = SUB * FN;
   i4_t fa[FM], fb[2];
   auto step = [&](int s) {
 #pragma unroll
-    for (int i = 0; i < FN; i++) {
-      if (i == FN - 1) {
+    for (int o = 0; o < kAll; o++) {
+      const int q = o / FN, i = o % FN;
+      if (o == kAll - 1) {
         lds_loads_left<(NB - 2) * kLoads>();  // this wave's part of the next step has landed
         __syncthreads();                      // and everyone's; this step has been read
         __builtin_amdgcn_sched_barrier(0);
       } else {
 #pragma unroll
-        for (int l = i * kLoads / (FN - 1); l < (i + 1) * kLoads / (FN - 1); l++)
+        for (int l = o * kLoads / (kAll - 1); l < (o + 1) * kLoads / (kAll - 1); l++)
           load(s + NB - 1, l);
       }
-      const i4_t w = fb[i % 2] ^ (int)0x80808080;
-      if (i + 2 < FN) fb[i % 2] = rows(s, i + 2);
-      if (i == FN - 1) {
-        fb[0] = rows(s + 1, 0);
-        fb[1] = rows(s + 1, 1);
+      const i4_t w = fb[o % 2] ^ (int)0x80808080;
+      if (o + 2 < kAll) fb[o % 2] = rows(s, (o + 2) / FN, (o + 2) % FN);
+      if (o == kAll - 1) {
+        fb[0] = rows(s + 1, 0, 0);
+        fb[1] = rows(s + 1, 1 / FN, 1 % FN);
       }
 #pragma unroll
       for (int j = 0; j < FM; j++) {
         acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, fa[j], acc[i][j], 0, 0, 0);
-        if (i == FN - 1) fa[j] = tokens(s + 1, j);
+        if (i == FN - 1) fa[j] = q + 1 < SUB ? tokens(s, (q + 1) % SUB, j) : tokens(s + 1, 0, j);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -159,9 +166,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, 
   lds_loads_left<(NB - 2) * kLoads>();
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < FM; j++) fa[j] = tokens(s0, j);
-  fb[0] = rows(s0, 0);
-  fb[1] = rows(s0, 1);
+  for (int j = 0; j < FM; j++) fa[j] = tokens(s0, 0, j);
+  fb[0] = rows(s0, 0, 0);
+  fb[1] = rows(s0, 1 / FN, 1 % FN);
   for (int s = s0; s < s1; s++) step(s);
   lds_loads_left<0>();
 
@@ -232,11 +239,11 @@ __global__ __launch_bounds__(256) void w8a8_join_kernel(const GemmArgs p, const 
   store4<GATED>(p, columns, sum[0], sum[1], n, t, xs, total);
 }
 
-template <int MT, int NT, int WM, int WN, int NB, bool GATED>
+template <int MT, int NT, int WM, int WN, int NB, int SUB, bool GATED>
 hipError_t launch_tile(const GemmArgs& p, const TilePlan& plan, i4_t* parts, hipStream_t stream) {
-  constexpr bool spare = MT / 16 % (WM * WN) != 0 || NT / 16 % (WM * WN) != 0;
-  constexpr int bytes = NB * (MT + NT) * kStep + (spare ? 1024 : 0);
-  auto kernel = w8a8_kernel<MT, NT, WM, WN, NB, GATED>;
+  constexpr bool spare = MT * SUB / 16 % (WM * WN) != 0 || NT * SUB / 16 % (WM * WN) != 0;
+  constexpr int bytes = NB * (MT + NT) * 64 * SUB + (spare ? 1024 : 0);
+  auto kernel = w8a8_kernel<MT, NT, WM, WN, NB, SUB, GATED>;
   hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), bytes);
   if (e != hipSuccess) return e;
   kernel<<<dim3((unsigned)plan.blocks()), dim3(WM * WN * 64), bytes, stream>>>(p, plan, parts);
@@ -248,40 +255,50 @@ hipError_t launch_tile(const GemmArgs& p, const TilePlan& plan, i4_t* parts, hip
   return hipGetLastError();
 }
 
-// Tile shapes: tokens, weight rows, and what a step of 64 k of one tile takes
-// of a CU's time (us, measured; two workgroups of the first share a CU at twice
-// that).
+// Tile shapes: tokens, weight rows, bytes of k per step, and what a step of one
+// tile takes of a CU's time when there is one tile for each CU at most, and when
+// there are more (us, measured).  The larger the tile the less LDS traffic per
+// output; the smaller ones are for sizes that would leave CUs idle or pad much,
+// and for those that wait for the weights from HBM.  Steps of 128 bytes read
+// whole cache lines and halve the barriers; the last three have no LDS for three
+// buffers of them, and two are slower (gated 4096x28672x8192 1847 / 1670 us).
+// With a shape and without it, us: 64 x 128 on 64x49152x12288 148 / 217, gated
+// 64x11008x4096 21.4 / 26.4; 128 x 128 in eight waves and 128 bytes instead of
+// four and 64 on 128x28672x8192 45.8 / 55.6, 1000x4096x4096 31.1 / 38.2;
+// 256 x 128 on 250x28672x8192 69 / 101, 2000x4096x4096 51.0 / 58.6; 192 x 192 on
+// gated 333x11008x4096 46.4 / 58.1 (of 64 bytes 50.8, in six waves 55.9).
 struct TileShape {
-  int mt, nt;
-  double step_us;
+  int mt, nt, step;
+  double alone_us, shared_us;
 };
-// The less LDS traffic per output the larger the tile; the smaller ones are for
-// sizes that would leave CUs idle or pad much (with the last shape and without:
-// gated 333x11008x4096 51.4 / 58.1 us, linear 2000x4096x4096 59.0 / 65.1; six
-// waves instead of its eight: 55.9 on the first).
 constexpr TileShape kShapes[] = {
-    {128, 128, 0.40}, {256, 256, 1.03}, {256, 192, 0.90}, {256, 384, 1.42}, {192, 192, 0.79}};
+    {64, 128, 128, 0.55, 0.70},  {128, 128, 128, 0.63, 0.80}, {256, 128, 128, 1.15, 1.32},
+    {192, 192, 128, 1.35, 1.50}, {256, 192, 64, 0.90, 0.90},  {256, 256, 64, 1.03, 1.03},
+    {256, 384, 64, 1.42, 1.42}};
 
-// The shape that should finish first.
+// The kernel and shape that should finish first.
 struct GemmPlan {
   TilePlan tiles;
-  int shape;
+  int shape;  // -1: the rings of w8a8_skinny.hip
   size_t part_bytes() const {
-    return (size_t)tiles.rest * tiles.splits * kShapes[shape].mt * kShapes[shape].nt * 4;
+    return shape < 0 ? 0
+                     : (size_t)tiles.rest * tiles.splits * kShapes[shape].mt * kShapes[shape].nt * 4;
   }
 };
 GemmPlan gemm_plan(int64_t T, int64_t N, int64_t K, bool gated) {
-  const int cus = device_cu_count(), steps = (int)((K + kStep - 1) / kStep);
+  const int cus = device_cu_count();
   const int64_t rows = gated ? 2 * N : N;
-  GemmPlan best{};
-  double least = 0;
+  GemmPlan best{{}, -1};
+  if (T <= 16) return best;
+  double least = T <= kSkinnyMostT ? skinny_us(T, N, K, gated) : 1e30;
   for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); i++) {
     const TileShape& t = kShapes[i];
     double us;
-    const TilePlan plan =
-        plan_tiles((T + t.mt - 1) / t.mt, (rows + t.nt - 1) / t.nt, cus, steps, t.step_us, t.step_us,
-                   (double)t.mt * t.nt * 4, &us);
-    if (i == 0 || us < least) {
+    const int steps = (int)((K + t.step - 1) / t.step);
+    const TilePlan plan = plan_tiles((T + t.mt - 1) / t.mt, (rows + t.nt - 1) / t.nt, cus, steps,
+                                     t.alone_us, t.shared_us, (double)t.mt * t.nt * 4, &us);
+    us += 2;  // the ring's first filling, and the outputs
+    if (us < least) {
       best = {plan, i};
       least = us;
     }
@@ -333,15 +350,26 @@ hipError_t launch(const Activations& x, int64_t T, const W8& w0, const W8& w1, i
   p.act = act;
   p.bf16 = out_dtype == kBF16;
   if (few_takes(T, K, GATED)) return launch_few(p, GATED, stream);
-  if (T <= kSkinnyMostT) return launch_skinny(p, GATED, stream);
   const GemmPlan plan = gemm_plan(T, N, K, GATED);
+  if (plan.shape < 0) return launch_skinny(p, GATED, stream);
   auto* parts = reinterpret_cast<i4_t*>(static_cast<uint8_t*>(workspace) +
                                         (x.dtype == kI8 ? 0 : code_bytes(T, K)));
-  if (plan.shape == 0) return launch_tile<128, 128, 2, 2, 4, GATED>(p, plan.tiles, parts, stream);
-  if (plan.shape == 1) return launch_tile<256, 256, 2, 4, 4, GATED>(p, plan.tiles, parts, stream);
-  if (plan.shape == 2) return launch_tile<256, 192, 4, 2, 4, GATED>(p, plan.tiles, parts, stream);
-  if (plan.shape == 3) return launch_tile<256, 384, 2, 4, 4, GATED>(p, plan.tiles, parts, stream);
-  return launch_tile<192, 192, 4, 2, 4, GATED>(p, plan.tiles, parts, stream);
+  switch (plan.shape) {
+    case 0:
+      return launch_tile<64, 128, 2, 4, 3, 2, GATED>(p, plan.tiles, parts, stream);
+    case 1:
+      return launch_tile<128, 128, 2, 4, 3, 2, GATED>(p, plan.tiles, parts, stream);
+    case 2:
+      return launch_tile<256, 128, 4, 2, 3, 2, GATED>(p, plan.tiles, parts, stream);
+    case 3:
+      return launch_tile<192, 192, 4, 2, 3, 2, GATED>(p, plan.tiles, parts, stream);
+    case 4:
+      return launch_tile<256, 192, 4, 2, 4, 1, GATED>(p, plan.tiles, parts, stream);
+    case 5:
+      return launch_tile<256, 256, 2, 4, 4, 1, GATED>(p, plan.tiles, parts, stream);
+    default:
+      return launch_tile<256, 384, 2, 4, 4, 1, GATED>(p, plan.tiles, parts, stream);
+  }
 }
 
 }  // namespace
@@ -349,7 +377,7 @@ hipError_t launch(const Activations& x, int64_t T, const W8& w0, const W8& w1, i
 size_t w8a8_workspace_bytes(int64_t T, int64_t N, int64_t K, int dtype, bool gated) {
   if (T == 0 || N == 0) return 0;
   const size_t codes = dtype == kI8 || fused(T, K, dtype, gated) ? 0 : code_bytes(T, K);
-  return codes + (T > kSkinnyMostT ? gemm_plan(T, N, K, gated).part_bytes() : 0);
+  return codes + (few_takes(T, K, gated) ? 0 : gemm_plan(T, N, K, gated).part_bytes());
 }
 
 hipError_t launch_linear_w8a8(const Activations& x, int64_t T, const W8& w, int64_t N, int64_t K,
