@@ -769,3 +769,12 @@ def test_every_plan_of_long_steps(lw, shape):
 def test_few_tokens_by_large_weights(lw, shape):
     """17 to 64 tokens where tiles take over from the rings, whole and shared out."""
     test_every_tile_plan(lw, shape)
+
+
+@pytest.mark.parametrize("shape", [(1, 2614, 32), (1, 174, 32), (17, 1468, 32), (24, 22, 32), (33, 1473, 32), (35, 61, 32),
+                                   (34, 2117, 6624), (139, 1009, 64), (113, 49, 32), (391, 1249, 8224),
+                                   (133, 1849, 5504), (588, 21, 6624), (2363, 5107, 160), (1258, 20, 7296),
+                                   (129, 8681, 8160), (1844, 24, 6368), (2199, 1241, 7200)], ids=str)
+def test_every_gradient_shape(lw, shape):
+    """Every tile shape of the gradients, whole and shared out."""
+    test_every_gradient_plan(lw, shape)

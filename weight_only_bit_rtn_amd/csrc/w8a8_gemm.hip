@@ -40,12 +40,12 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, 
   constexpr int FM = MW / 16, FN = NW / 16;  // its fragments
   constexpr int NO = GATED ? NT / 2 : NT;    // output columns of a tile
   constexpr int kStep = 64 * SUB, kChunks = 4 * SUB;  // bytes and chunks of a row per step
-  // 1 KiB loads of 16 / SUB rows; where an operand's do not come out even among the
+  // 1 KiB loads of 16 / SUB rows; where the weights' do not come out even among the
   // waves, the last go to a place of their own, so that every wave counts as many
   constexpr int kRows = 16 / SUB;
   constexpr int kA = MT / kRows, kB = NT / kRows;
-  constexpr int LA = (kA + kWaves - 1) / kWaves, LB = (kB + kWaves - 1) / kWaves, kLoads = LA + LB;
-  static_assert(MT % (16 * WM) == 0 && NT % (16 * WN) == 0, "whole loads");
+  constexpr int LA = kA / kWaves, LB = (kB + kWaves - 1) / kWaves, kLoads = LA + LB;
+  static_assert(LA * kWaves == kA && MT % (16 * WM) == 0 && NT % (16 * WN) == 0, "whole loads");
   static_assert(!GATED || FN % 2 == 0, "gate and up halves");
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   constexpr int kBuf = (MT + NT) * kStep;
@@ -77,15 +77,14 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, 
   const uint32_t chunk = ((lane % kChunks) ^ swizzle(rl)) * 16;
   uint32_t oa[LA], ob[LB];
   uint32_t la[LA], lb[LB];
-  bool up[LB], spare[LB], spare_a[LA];
+  bool up[LB], spare[LB];
   const uint32_t base = lds_address(lds);
   const uint32_t kend = min((uint32_t)s1 * kStep, K);
 #pragma unroll
   for (int i = 0; i < LA; i++) {
     const int row = (wave + i * kWaves) * kRows;
-    spare_a[i] = kA % kWaves != 0 && row >= MT;
-    oa[i] = spare_a[i] ? 0x80000000u : (row + rl) * K + chunk;
-    la[i] = base + (spare_a[i] ? NB * kBuf : row * kStep);
+    oa[i] = (row + rl) * K + chunk;
+    la[i] = base + row * kStep;
   }
 #pragma unroll
   for (int i = 0; i < LB; i++) {
@@ -103,7 +102,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, 
     const uint32_t k0 = (uint32_t)s * kStep, buf = (uint32_t)(s % NB) * kBuf;
     const uint32_t add = k0 + chunk < kend ? k0 : 0x80000000u;
     if (i < LA)
-      load_to_lds(ra, la[i] + (spare_a[i] ? 0 : buf), spare_a[i] ? oa[i] : oa[i] + add);
+      load_to_lds(ra, la[i] + buf, oa[i] + add);
     else
       load_to_lds(up[i - LA] ? ru : rg, lb[i - LA] + (spare[i - LA] ? 0 : buf),
                   spare[i - LA] ? ob[i - LA] : ob[i - LA] + add);
@@ -241,7 +240,7 @@ __global__ __launch_bounds__(256) void w8a8_join_kernel(const GemmArgs p, const 
 
 template <int MT, int NT, int WM, int WN, int NB, int SUB, bool GATED>
 hipError_t launch_tile(const GemmArgs& p, const TilePlan& plan, i4_t* parts, hipStream_t stream) {
-  constexpr bool spare = MT * SUB / 16 % (WM * WN) != 0 || NT * SUB / 16 % (WM * WN) != 0;
+  constexpr bool spare = NT * SUB / 16 % (WM * WN) != 0;
   constexpr int bytes = NB * (MT + NT) * 64 * SUB + (spare ? 1024 : 0);
   auto kernel = w8a8_kernel<MT, NT, WM, WN, NB, SUB, GATED>;
   hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), bytes);

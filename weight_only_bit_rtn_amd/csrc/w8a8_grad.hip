@@ -493,7 +493,7 @@ int64_t padded(int64_t N) { return (N + kStepN - 1) / kStepN * kStepN; }
 
 // Tile shapes: tokens, columns of dx, and what a step of 64 weight rows of one
 // tile takes of a CU's time when the CU has no other workgroup, and when it has
-// (us, measured).  The last reads the tokens' factors half as often as the third
+// (us, measured).  64 x 256 reads the tokens' factors half as often as 64 x 128
 // and pays where the weights are large (gated 64x28672x8192 125 / 145 us,
 // 61x11008x4096 33.1 / 33.4); for 16 or 32 tokens, whose factors are fewer, 256
 // columns gave nothing (16x28672x8192 117 / 122, 10x12288x12288 40.5 / 37.5).
@@ -501,13 +501,13 @@ struct TileShape {
   int mt, kt;
   double alone_us, shared_us;
 };
-constexpr TileShape kShapes[] = {{16, 128, 0.40, 0.32},  {32, 128, 0.40, 0.32},
-                                 {64, 128, 0.50, 0.40},  {128, 128, 0.74, 0.55},
-                                 {256, 256, 1.60, 1.60}, {256, 192, 1.20, 1.20},
-                                 {64, 256, 0.64, 0.64}};
+// 128 x 256 beside 128 x 128: 2000x4096x4096 83 / 87, gated 128x28672x8192 168 /
+// 178, but 1000x1024x1024 24.9 / 22.1.
+constexpr TileShape kShapes[] = {
+    {16, 128, 0.40, 0.32},  {32, 128, 0.40, 0.32},  {64, 128, 0.50, 0.40},  {64, 256, 0.64, 0.64},
+    {128, 128, 0.74, 0.55}, {128, 256, 1.06, 1.06}, {256, 192, 1.20, 1.20}, {256, 256, 1.60, 1.60}};
 
-// The shape that should finish first, of those that hold T tokens without
-// waste: the first or the second, the third and the last, or the fourth and on.
+// The shape that should finish first, of those that hold T tokens without waste.
 struct GradPlan {
   TilePlan tiles;
   int shape;
@@ -517,11 +517,11 @@ struct GradPlan {
 };
 GradPlan grad_plan(int64_t T, int64_t K, int steps) {
   const int cus = device_cu_count();
-  const int from = T <= 16 ? 0 : T <= 32 ? 1 : T <= 64 ? 2 : 3;
-  const int shapes[] = {from, from == 2 ? 6 : from == 3 ? 4 : from, from == 3 ? 5 : from};
+  const int from = T <= 16 ? 0 : T <= 32 ? 1 : T <= 64 ? 2 : 4;
+  const int to = T <= 32 ? from : T <= 64 ? 3 : 7;
   GradPlan best{};
   double least = 0;
-  for (int i : shapes) {
+  for (int i = from; i <= to; i++) {
     const TileShape& t = kShapes[i];
     double us;
     const TilePlan plan = plan_tiles((T + t.mt - 1) / t.mt, (K + t.kt - 1) / t.kt, cus, steps,
@@ -597,13 +597,15 @@ hipError_t launch_w8a8_grad(const void* dh, const void* gate, const void* up, in
     case 2:
       return launch_tile<64, 128, 1, 4, 4>(p, plan.tiles, parts, stream);
     case 3:
-      return launch_tile<128, 128, 2, 2, 3>(p, plan.tiles, parts, stream);
+      return launch_tile<64, 256, 1, 8, 3>(p, plan.tiles, parts, stream);
     case 4:
-      return launch_tile<256, 256, 2, 4, 3>(p, plan.tiles, parts, stream);
+      return launch_tile<128, 128, 2, 2, 3>(p, plan.tiles, parts, stream);
     case 5:
+      return launch_tile<128, 256, 2, 4, 3>(p, plan.tiles, parts, stream);
+    case 6:
       return launch_tile<256, 192, 2, 4, 3>(p, plan.tiles, parts, stream);
     default:
-      return launch_tile<64, 256, 1, 8, 3>(p, plan.tiles, parts, stream);
+      return launch_tile<256, 256, 2, 4, 3>(p, plan.tiles, parts, stream);
   }
 }
 
