@@ -15,7 +15,6 @@ rounding of the activations is passed through unchanged.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 from . import _check, _ptr, _require_gpu_tensor, load_library as _load_library
@@ -150,9 +149,9 @@ def _wrong(t, name: str, dtype, device, shape) -> None:
 def _check_tensor(t, name: str, dtype, device=None, shape=None) -> None:
     """``t`` is a dense GPU tensor of this type, place and shape (any matrix where None)."""
     try:
-        fine = (t.dtype == dtype and t.is_cuda and t.is_contiguous()
+        fine = (t.dtype is dtype and t.is_contiguous()
                 and (t.dim() == 2 if shape is None else t.shape == shape)
-                and (device is None or t.device == device))
+                and (t.is_cuda if device is None else t.get_device() == device.index))
     except AttributeError:
         fine = False
     if not fine:
@@ -202,26 +201,26 @@ def _activations(x, out_dtype):
     return ptrs, T, K, dev, out_dtype, out_kind
 
 
-def _on(device):
-    """Launches go to the current device: make it the tensors' one."""
+def _run(name: str, sizes, args, device) -> None:
+    """Calls an entry point on ``args``, its workspace (for ``sizes``; None: it
+    takes none) and the current stream of the tensors' device, which it makes
+    the current one: launches go there."""
     torch = _torch()
-    if device.index == torch.cuda.current_device():
-        return _HERE
-    return torch.cuda.device(device)
-
-
-_HERE = contextlib.nullcontext()
-
-
-def _workspace(need: int, what: str, device):
-    """(tensor or None, address): scratch of at least ``need`` bytes, 256-byte aligned."""
-    if need <= 0:
-        _check(need, what)
-        return None, None
-    # torch's caching allocator hands out blocks aligned to 512 bytes
-    torch = _torch()
-    t = torch.empty(need, dtype=torch.uint8, device=device)
-    return t, t.data_ptr()
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _run(name, sizes, args, device)
+    lib = _lib()
+    if sizes is None:
+        return _check(getattr(lib, name)(*args, _stream_handle(device)), name)
+    need = getattr(lib, name + "_workspace_bytes")(*sizes)
+    if need > 0:
+        # torch's caching allocator hands out blocks aligned to 512 bytes
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        at = workspace.data_ptr()
+    else:
+        _check(need, name + "_workspace_bytes")
+        at = None
+    _check(getattr(lib, name)(*args, at, need, _stream_handle(device)), name)
 
 
 def _out(out, name, shape, dtype, device):
@@ -265,10 +264,8 @@ def quantize_act(x, out: dict | None = None) -> dict:
         _apart(codes, "codes", x)
         _apart(scales, "scales", x, codes)
         _apart(sums, "sums", x, codes, scales)
-    with _on(dev):
-        status = quantize_act_raw(x.data_ptr(), kind, T, K, codes.data_ptr(), scales.data_ptr(),
-                                  sums.data_ptr(), _stream_handle(dev))
-    _check(status, "lowbit_quantize_act")
+    _run("lowbit_quantize_act", None,
+         (x.data_ptr(), kind, T, K, codes.data_ptr(), scales.data_ptr(), sums.data_ptr()), dev)
     return {"codes": codes, "scales": scales, "sums": sums}
 
 
@@ -284,13 +281,9 @@ def linear_w8a8(x, packed, scales, zeros, out_dtype=None, out=None):
     if out is not None:
         _apart(y, "out", *((x["codes"], x["scales"], x["sums"]) if isinstance(x, dict) else (x,)),
                packed, scales, zeros)
-    with _on(dev):
-        need = linear_w8a8_workspace_bytes(T, N, K, ptrs[1])
-        ws, at = _workspace(need, "lowbit_linear_w8a8_workspace_bytes", dev)
-        status = linear_w8a8_raw(*ptrs, T, packed.data_ptr(), scales.data_ptr(),
-                                 zeros.data_ptr(), N, K, y.data_ptr(), out_kind, at, need,
-                                 _stream_handle(dev))
-    _check(status, "lowbit_linear_w8a8")
+    _run("lowbit_linear_w8a8", (T, N, K, ptrs[1]),
+         (*ptrs, T, packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(), N, K, y.data_ptr(),
+          out_kind), dev)
     return y
 
 
@@ -308,16 +301,11 @@ def gated_w8a8(x, packed_gate, scales_gate, zeros_gate, packed_up, scales_up, ze
         raise ValueError("x and the weights must have the same K")
     _weights(packed_up, scales_up, zeros_up, dev, N, K)
     outs = [torch.empty((T, N), dtype=out_dtype, device=dev) for _ in range(3 if save else 1)]
-    with _on(dev):
-        need = gated_w8a8_workspace_bytes(T, N, K, ptrs[1])
-        ws, at = _workspace(need, "lowbit_gated_w8a8_workspace_bytes", dev)
-        status = gated_w8a8_raw(*ptrs, T, packed_gate.data_ptr(), scales_gate.data_ptr(),
-                                zeros_gate.data_ptr(), packed_up.data_ptr(),
-                                scales_up.data_ptr(), zeros_up.data_ptr(), N, K, kind,
-                                outs[0].data_ptr(), outs[1].data_ptr() if save else None,
-                                outs[2].data_ptr() if save else None, out_kind, at, need,
-                                _stream_handle(dev))
-    _check(status, "lowbit_gated_w8a8")
+    _run("lowbit_gated_w8a8", (T, N, K, ptrs[1]),
+         (*ptrs, T, packed_gate.data_ptr(), scales_gate.data_ptr(), zeros_gate.data_ptr(),
+          packed_up.data_ptr(), scales_up.data_ptr(), zeros_up.data_ptr(), N, K, kind,
+          outs[0].data_ptr(), outs[1].data_ptr() if save else None,
+          outs[2].data_ptr() if save else None, out_kind), dev)
     return tuple(outs) if save else outs[0]
 
 
@@ -334,13 +322,9 @@ def linear_w8a8_grad(dy, packed, scales, zeros, out=None):
     dx = _out(out, "out", (T, K), dy.dtype, dev)
     if out is not None:
         _apart(dx, "out", dy, packed, scales, zeros)
-    with _on(dev):
-        need = linear_w8a8_grad_workspace_bytes(T, N, K)
-        ws, at = _workspace(need, "lowbit_linear_w8a8_grad_workspace_bytes", dev)
-        status = linear_w8a8_grad_raw(dy.data_ptr(), kind, T, packed.data_ptr(),
-                                      scales.data_ptr(), zeros.data_ptr(), N, K, dx.data_ptr(),
-                                      at, need, _stream_handle(dev))
-    _check(status, "lowbit_linear_w8a8_grad")
+    _run("lowbit_linear_w8a8_grad", (T, N, K),
+         (dy.data_ptr(), kind, T, packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(), N, K,
+          dx.data_ptr()), dev)
     return dx
 
 
@@ -365,14 +349,9 @@ def gated_w8a8_grad(dh, gate, up, packed_gate, scales_gate, zeros_gate, packed_u
     dx = torch.empty((T, K), dtype=dh.dtype, device=dev)
     dgate = torch.empty_like(dh) if parts else None
     dup = torch.empty_like(dh) if parts else None
-    with _on(dev):
-        need = gated_w8a8_grad_workspace_bytes(T, N, K)
-        ws, at = _workspace(need, "lowbit_gated_w8a8_grad_workspace_bytes", dev)
-        status = gated_w8a8_grad_raw(dh.data_ptr(), gate.data_ptr(), up.data_ptr(), kind, T,
-                                     packed_gate.data_ptr(), scales_gate.data_ptr(),
-                                     zeros_gate.data_ptr(), packed_up.data_ptr(),
-                                     scales_up.data_ptr(), zeros_up.data_ptr(), N, K, code,
-                                     dx.data_ptr(), _ptr(dgate), _ptr(dup), at, need,
-                                     _stream_handle(dev))
-    _check(status, "lowbit_gated_w8a8_grad")
+    _run("lowbit_gated_w8a8_grad", (T, N, K),
+         (dh.data_ptr(), gate.data_ptr(), up.data_ptr(), kind, T, packed_gate.data_ptr(),
+          scales_gate.data_ptr(), zeros_gate.data_ptr(), packed_up.data_ptr(),
+          scales_up.data_ptr(), zeros_up.data_ptr(), N, K, code, dx.data_ptr(), _ptr(dgate),
+          _ptr(dup)), dev)
     return (dx, dgate, dup) if parts else dx
