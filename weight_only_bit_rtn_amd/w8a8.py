@@ -11,7 +11,10 @@ package's other functions.  Weights are the 8-bit per-row codes of
   gated_w8a8_grad(dh, gate, up, gate's three, up's three, act) -> dx
 
 The gradients are with respect to x; the weights are constants, and the
-rounding of the activations is passed through unchanged.
+rounding of the activations is passed through unchanged.  The calls are outside
+autograd: where gradients are recorded, a tensor that requires grad is refused,
+as its gradient would end there.  An autograd function's forward and backward,
+and torch.no_grad(), take any tensor.
 """
 from __future__ import annotations
 
@@ -138,6 +141,10 @@ def _float_type(t, name: str) -> int:
 
 def _wrong(t, name: str, dtype, device, shape) -> None:
     """Says what is wrong with a tensor."""
+    torch = _torch()
+    if isinstance(t, torch.Tensor) and t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires grad, and the call is outside autograd: its gradient would end "
+                         "here; make the call under torch.no_grad() and the *_grad call for the gradient")
     _require_gpu_tensor(t, name, dtype)
     if device is not None and t.device != device:
         raise ValueError(f"{name} must live on {device}, got {t.device}")
@@ -147,9 +154,11 @@ def _wrong(t, name: str, dtype, device, shape) -> None:
 
 
 def _check_tensor(t, name: str, dtype, device=None, shape=None) -> None:
-    """``t`` is a dense GPU tensor of this type, place and shape (any matrix where None)."""
+    """``t`` is a dense GPU tensor of this type, place and shape (any matrix where None)
+    whose gradient nobody waits for."""
     try:
         fine = (t.dtype is dtype and t.is_contiguous()
+                and not (t.requires_grad and _torch().is_grad_enabled())
                 and (t.dim() == 2 if shape is None else t.shape == shape)
                 and (t.is_cuda if device is None else t.get_device() == device.index))
     except AttributeError:
