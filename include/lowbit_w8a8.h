@@ -30,9 +30,10 @@
  *    weights are constants:  dx = sum_n (dy s_n) (code - z_n).  The factor
  *    dy s_n is rounded to 11 significant bits (fp16, after a power of two
  *    chosen for each token that makes the token's largest factor lie in
- *    [2^14, 2^15); a factor below 2^-29 of the largest loses bits), the sums are fp32,
- *    dx is rounded once.  For the gated block  du = dh act(g),
- *    dg = dh u act'(g)  in fp32 from the given 16-bit g and u.  A token whose
+ *    [2^14, 2^15); a factor below 2^-29 of the largest loses bits; factors below
+ *    fp32's normal range lose no others), the sums are fp32, dx is rounded once.
+ *    For the gated block  du = dh act(g),  dg = dh u act'(g)  in fp32 from the
+ *    given 16-bit g and u.  A token whose
  *    dy (dg, du) holds an infinity or a NaN, or whose factors dy s_n leave
  *    fp32's range, has an all-NaN dx.
  *    Sums over n may be split; their order is fixed by the sizes alone, so

@@ -8,9 +8,11 @@
 //   dx[t][k] = 2^-e_t (sum_n a'[t][n] c'[n][k] + r_t),
 //   a' = fp16(2^e_t a),  r_t = sum_n a'[t][n] (128 - z_n).
 // e_t makes a token's largest |a'| lie in [2^14, 2^15): gradients of any size
-// keep their 11 significant bits.  Rounding a to fp16 is the one rounding
-// between the inputs and the output: the matrix cores take 16-bit operands at
-// the rate measured here, and bf16 would keep 8 bits.
+// keep their 11 significant bits, down to factors of 2^-29 of the token's largest.
+// (a is formed in fp32; where a token's are so small that bits would be lost
+// there, with scales 2^100 times as large.)  Rounding a to fp16 is the one
+// rounding between the inputs and the output: the matrix cores take 16-bit
+// operands at the rate measured here, and bf16 would keep 8 bits.
 //
 // Two kernels: one makes a', e and r (and, for the gated block, the gradients
 // of both projections on the way), one multiplies.  The gated block's two
@@ -54,6 +56,10 @@ __device__ __forceinline__ float block_max(float v, float* red, int tid) {
   return v;
 }
 
+// A condition that is the same for the whole workgroup: a branch on it is one for
+// the compiler too.
+__device__ __forceinline__ bool uniform(int v) { return __builtin_amdgcn_readfirstlane(v) != 0; }
+
 // Eight values of a row from chunk c on.  WHOLE (N % 8 == 0): rows and chunks
 // lie at 16 bytes.  Otherwise a row may lie at any 2-byte address, and its last
 // chunk is not full.  Positions past N: zeros read, nothing written.
@@ -86,12 +92,35 @@ __device__ __forceinline__ void put8(uint16_t* row, int c, int N, bool full, us8
   }
 }
 
-// The factors d s of chunk c (gated: of the gate and the up part), in fp32, the
-// largest |d s| so far and whether every d is finite; `write`: dg and du go out.
+// What a token's factors have shown so far: the largest, which bits are set in any
+// of its d (none: all are zero), and whether all of d (dg, du) are finite.
+struct Seen {
+  float top = 0;
+  int bits = 0;
+  bool finite = true;
+};
+
+// The gradient that a row's scale multiplies: d itself (d0) or, of the gated
+// block, the gate's dg (d0) and the up projection's du (d1).
+template <int ACT, bool BF>
+__device__ __forceinline__ void gradients(uint16_t d, uint16_t g, uint16_t u, float& d0,
+                                          float& d1) {
+  d0 = elem_to_f32(d, BF);
+  d1 = 0;
+  if constexpr (ACT >= 0) {
+    float f, df;
+    act_value_slope(elem_to_f32(g, BF), ACT, f, df);
+    d1 = d0 * f;
+    d0 = d0 * elem_to_f32(u, BF) * df;
+  }
+}
+
+// The factors d s of chunk c (gated: of the gate and the up part), in fp32;
+// `write`: dg and du go out.
 template <int ACT, bool BF, bool WHOLE>
 __device__ __forceinline__ void factors8(const PrepArgs& p, int64_t row, int c, bool write,
-                                         float (&a)[ACT < 0 ? 1 : 2][8], float& top, bool& finite) {
-  constexpr bool GATED = ACT >= 0, bf = BF;
+                                         float (&a)[ACT < 0 ? 1 : 2][8], Seen& seen) {
+  constexpr bool GATED = ACT >= 0;
   constexpr int M = GATED ? 2 : 1;
   const bool full = WHOLE || c * 8 + 8 <= p.N;
   us8_t d, g, u, og, ou, sc[M];
@@ -108,26 +137,66 @@ __device__ __forceinline__ void factors8(const PrepArgs& p, int64_t row, int c, 
     read(true);
   else
     read(false);
+  const i4_t bits = __builtin_bit_cast(i4_t, d);
+  seen.bits |= bits[0] | bits[1] | bits[2] | bits[3];
 #pragma unroll
   for (int j = 0; j < 8; j++) {
-    float d0 = elem_to_f32(d[j], bf), d1 = 0;
+    float d0, d1;
+    gradients<ACT, BF>(d[j], GATED ? g[j] : 0, GATED ? u[j] : 0, d0, d1);
+    a[0][j] = d0 * h_bits_to_f32(sc[0][j]);
     if constexpr (GATED) {
-      float f, df;
-      act_value_slope(elem_to_f32(g[j], bf), ACT, f, df);
-      d1 = d0 * f;
-      d0 = d0 * elem_to_f32(u[j], bf) * df;
-      og[j] = f32_to_elem(d0, bf);
-      ou[j] = f32_to_elem(d1, bf);
+      og[j] = f32_to_elem(d0, BF);
+      ou[j] = f32_to_elem(d1, BF);
       a[M - 1][j] = d1 * h_bits_to_f32(sc[M - 1][j]);
     }
-    a[0][j] = d0 * h_bits_to_f32(sc[0][j]);
-    finite = finite && fabsf(d0) < INFINITY && fabsf(d1) < INFINITY;
+    seen.finite = seen.finite && fabsf(d0) < INFINITY && fabsf(d1) < INFINITY;
 #pragma unroll
-    for (int m = 0; m < M; m++) top = fmaxf(top, fabsf(a[m][j]));
+    for (int m = 0; m < M; m++) seen.top = fmaxf(seen.top, fabsf(a[m][j]));
   }
   if (GATED && write) {
     put8<WHOLE>(p.dgate + row * p.N, c, p.N, full, og);
     put8<WHOLE>(p.dup + row * p.N, c, p.N, full, ou);
+  }
+}
+
+// The preparation of a token whose factors are below 2^-110 (bf16 gradients near
+// the end of its range), one value at a time: with scales 2^100 times as large no
+// factor is subnormal (d is 2^-133 or more, s 2^-24), and none above 2^-10.
+template <int ACT, bool BF>
+__device__ __forceinline__ void tiny_factors(const PrepArgs& p, int64_t row, float* red) {
+  constexpr int M = ACT < 0 ? 1 : 2, kMore = 100;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  auto factors = [&](int n, float(&a)[M]) {
+    const int64_t at = row * p.N + n;
+    float d[2];
+    gradients<ACT, BF>(p.d[at], ACT < 0 ? 0 : p.gate[at], ACT < 0 ? 0 : p.up[at], d[0], d[1]);
+    for (int m = 0; m < M; m++)
+      a[m] = d[m] * __builtin_amdgcn_ldexpf(h_bits_to_f32(p.w[m].scales[n]), kMore);
+  };
+  float a[M], top = 0, r = 0;
+#pragma unroll 1
+  for (int n = tid; n < p.N; n += nt) {
+    factors(n, a);
+    for (int m = 0; m < M; m++) top = fmaxf(top, fabsf(a[m]));
+  }
+  top = block_max(top, red, tid);
+  const int e = top > 0 ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
+#pragma unroll 1
+  for (int n = tid; n < p.half; n += nt) {
+    if (n < p.N) factors(n, a);
+    for (int m = 0; m < M; m++) {
+      uint16_t out = 0;
+      if (n < p.N) {
+        out = f32_to_h_bits(__builtin_amdgcn_ldexpf(a[m], e));
+        r += h_bits_to_f32(out) * (float)(128 - p.w[m].zeros[n]);
+      }
+      p.a[row * p.pitch + m * p.half + n] = out;
+    }
+  }
+  r = block_sum(r, red, tid);
+  if (tid == 0) {
+    p.r[row] = r;
+    p.e[row] = e + kMore;
   }
 }
 
@@ -147,20 +216,28 @@ __global__ __launch_bounds__(1024) void grad_prep_kernel(const PrepArgs p) {
   const int tid = threadIdx.x, nt = blockDim.x, chunks = (p.N + 7) / 8, all = p.half / 8;
   const int64_t row = blockIdx.x;
   float held[NC > 0 ? NC : 1][M][8];
-  float top = 0;
-  bool finite = true;
+  Seen seen;
   const bool write = p.dgate != nullptr;
   if constexpr (NC > 0) {
 #pragma unroll
     for (int i = 0; i < NC; i++) {
       const int c = tid + i * nt;
-      if (c < chunks) factors8<ACT, BF, WHOLE>(p, row, c, write, held[i], top, finite);
+      if (c < chunks) factors8<ACT, BF, WHOLE>(p, row, c, write, held[i], seen);
     }
   } else {
     for (int c = tid; c < chunks; c += nt)
-      factors8<ACT, BF, WHOLE>(p, row, c, write, held[0], top, finite);
+      factors8<ACT, BF, WHOLE>(p, row, c, write, held[0], seen);
   }
-  top = block_max(finite ? top : INFINITY, red, tid);
+  const float top = block_max(seen.finite ? seen.top : INFINITY, red, tid);
+  // Below 2^-139 fp32 has less than 11 bits, and factors are to keep theirs down to
+  // 2^-29 of the largest.  Tokens of zeros need no second look, and an fp16 value
+  // by an fp16 scale is 2^-48 or more.
+  if constexpr (BF || ACT >= 0) {
+    if (uniform(top < 0x1p-110f) && uniform(__syncthreads_or(seen.bits & 0x7fff7fff))) {
+      tiny_factors<ACT, BF>(p, row, red);
+      return;
+    }
+  }
   const bool ok = top < INFINITY;
   const int e = ok && top > 0 ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
   float r = 0;
@@ -194,7 +271,7 @@ __global__ __launch_bounds__(1024) void grad_prep_kernel(const PrepArgs p) {
     }
   } else {
     for (int c = tid; c < all; c += nt) {
-      if (c < chunks) factors8<ACT, BF, WHOLE>(p, row, c, false, held[0], top, finite);
+      if (c < chunks) factors8<ACT, BF, WHOLE>(p, row, c, false, held[0], seen);
       round8(c, held[0]);
     }
   }
