@@ -49,8 +49,11 @@ template <int TT>
 __device__ __forceinline__ void quantize_here(const GemmArgs& p, int8_t* codes, int* meta,
                                               int* red) {
   constexpr int W = kWaves / TT;  // waves per token
-  // T K <= 16384 in chunks of 8 over 64 W lanes; TT is T or the next power of two
-  constexpr int NC = kFusedMost / 8 / (64 * kWaves) * 2;
+  // Chunks of 8 values per lane: T K <= kFusedMost, and TT is the smallest power of
+  // two that holds T, so T is TT / 2 + 1 at least and a row with its padding at most
+  // few_pitch(kFusedMost / T) long.
+  constexpr int NC = TT <= 2 ? 2 : 3;
+  static_assert(few_pitch(kFusedMost / (TT / 2 + 1)) <= NC * 64 * W * 8, "whole rows");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int t = wave / W, part = wave % W;
   const bool mine = t < p.T;
@@ -94,10 +97,6 @@ __device__ __forceinline__ void quantize_here(const GemmArgs& p, int8_t* codes, 
     if (mine && c < all)
       *reinterpret_cast<uint2*>(codes + t * few_pitch(p.K) + c * 8) = make_uint2(w[0], w[1]);
   }
-  // zeros up to whole chunks of the products, where the loop above ends before
-  if (mine)
-    for (int c = part * 64 + lane + NC * (64 * W); c < all; c += 64 * W)
-      *reinterpret_cast<uint2*>(codes + t * few_pitch(p.K) + c * 8) = make_uint2(0, 0);
   sum = wave_sum_last(sum);
   if (lane == 63) red[kWaves + wave] = sum;
   __syncthreads();
@@ -112,12 +111,12 @@ __device__ __forceinline__ void quantize_here(const GemmArgs& p, int8_t* codes, 
   __syncthreads();
 }
 
-// TT tokens (those past T repeat the last), RR rows per item; gated: RR / 2
-// rows of each matrix.
-template <int TT, int RR, bool GATED, bool FUSED>
+// TT tokens (those past T repeat the last).  An item is one output column: one
+// weight row, or (gated) the same row of both matrices.
+template <int TT, bool GATED, bool FUSED>
 __global__ __launch_bounds__(kWaves * 64) void few_kernel(const GemmArgs p) {
-  constexpr int D = kInFlight / RR;
-  constexpr int RO = GATED ? RR / 2 : RR;  // output columns per item
+  constexpr int M = GATED ? 2 : 1;
+  constexpr int D = kInFlight / M;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   int* meta = reinterpret_cast<int*>(lds);  // scales, sums, scratch: 64 words
   int8_t* codes = reinterpret_cast<int8_t*>(lds + 256);
@@ -125,43 +124,36 @@ __global__ __launch_bounds__(kWaves * 64) void few_kernel(const GemmArgs p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t K = (uint32_t)p.K;
   const int steps = (p.K + kChunk - 1) / kChunk, pitch = few_pitch(p.K);
-  const int items = (p.N + RO - 1) / RO, stride = gridDim.x * kWaves;
+  const int stride = gridDim.x * kWaves;
   const int first = wave * gridDim.x + blockIdx.x;
 
-  i4_t w[D][RR];
+  i4_t w[D][M];
   int li = first, ls = 0;  // item and step of the next load
   // positions past a row's end and rows past the last come as zeros
-  auto load = [&](i4_t(&wd)[RR]) {
+  auto load = [&](i4_t(&wd)[M]) {
     const uint32_t k = (uint32_t)ls * kChunk + lane * 16;
     const uint32_t at = k < K ? k : 0x80000000u;
 #pragma unroll
-    for (int m = 0; m < (GATED ? 2 : 1); m++) {
-      const int n = li * RO;
-      const auto rs = checked_buffer(p.w[m].codes + (int64_t)n * K,
-                              (uint32_t)max(0, min(RO, p.N - n)) * K);
-#pragma unroll
-      for (int r = 0; r < RO; r++) wd[m * RO + r] = load16(rs, at + r * K);
-    }
+    for (int m = 0; m < M; m++)
+      wd[m] = load16(checked_buffer(p.w[m].codes + (int64_t)li * K, li < p.N ? K : 0), at);
     if (++ls == steps) {
       ls = 0;
       li += stride;
     }
   };
-  // the lane that finishes output (r, t) of an item is lane r TT + t; it has
-  // the row's scale and zero point loaded by then
-  const int fr = lane / TT % RO, ft = lane % TT;
-  const bool finishes = lane < RO * TT && ft < p.T;
-  float sc[2];
-  int z[2];
+  // lane t finishes token t's output of an item; it has the row's scale and zero
+  // point loaded by then
+  float sc[M];
+  int z[M];
   auto load_params = [&](int item) {
-    const int n = min(item * RO + fr, p.N - 1);
+    const int n = min(item, p.N - 1);
 #pragma unroll
-    for (int m = 0; m < (GATED ? 2 : 1); m++) {
+    for (int m = 0; m < M; m++) {
       sc[m] = h_bits_to_f32(p.w[m].scales[n]);
       z[m] = p.w[m].zeros[n];
     }
   };
-  load_params(min(first, items - 1));
+  load_params(first);
 #pragma unroll
   for (int d = 0; d < D; d++) load(w[d]);
   if constexpr (FUSED) {
@@ -180,52 +172,50 @@ __global__ __launch_bounds__(kWaves * 64) void few_kernel(const GemmArgs p) {
     __syncthreads();
   }
 
-  const float xs = __builtin_bit_cast(float, meta[min(ft, p.T - 1)]);
-  const int total = meta[8 + min(ft, p.T - 1)];
-  int acc[RR][TT];
-  for (int item = first, step = 0; item < items;) {
+  const float xs = __builtin_bit_cast(float, meta[min(lane, p.T - 1)]);
+  const int total = meta[8 + min(lane, p.T - 1)];
+  int acc[M][TT];
+  for (int item = first, step = 0; item < p.N;) {
 #pragma unroll
     for (int d = 0; d < D; d++) {
       if (step == 0) {
 #pragma unroll
-        for (int r = 0; r < RR; r++)
+        for (int m = 0; m < M; m++)
 #pragma unroll
-          for (int t = 0; t < TT; t++) acc[r][t] = 0;
+          for (int t = 0; t < TT; t++) acc[m][t] = 0;
       }
-      i4_t wx[RR];
+      i4_t wx[M];
 #pragma unroll
-      for (int r = 0; r < RR; r++) wx[r] = w[d][r] ^ (int)0x80808080;
+      for (int m = 0; m < M; m++) wx[m] = w[d][m] ^ (int)0x80808080;
 #pragma unroll
       for (int t = 0; t < TT; t++) {
         const i4_t a = *reinterpret_cast<const i4_t*>(codes + min(t, p.T - 1) * pitch +
                                                       step * kChunk + lane * 16);
 #pragma unroll
-        for (int r = 0; r < RR; r++)
+        for (int m = 0; m < M; m++)
 #pragma unroll
           for (int q = 0; q < 4; q++)
-            acc[r][t] = __builtin_amdgcn_sdot4(wx[r][q], a[q], acc[r][t], false);
+            acc[m][t] = __builtin_amdgcn_sdot4(wx[m][q], a[q], acc[m][t], false);
       }
       load(w[d]);
       __builtin_amdgcn_sched_barrier(0);  // keeps the other loads in flight
       if (++step == steps) {
-        if (item < items) {
-          const int n = item * RO + fr;
-          const bool last = finishes && n < p.N;
-          int mine[2] = {0, 0};
+        if (item < p.N) {
+          int mine[M] = {};
 #pragma unroll
-          for (int r = 0; r < RR; r++)
+          for (int m = 0; m < M; m++)
 #pragma unroll
             for (int t = 0; t < TT; t++) {
-              const int v = __builtin_amdgcn_readlane(wave_sum_last(acc[r][t]), 63);
-              if (lane == r % RO * TT + t) mine[r / RO] = v;
+              const int v = __builtin_amdgcn_readlane(wave_sum_last(acc[m][t]), 63);
+              if (lane == t) mine[m] = v;
             }
-          if (last) {
-            float v[2];
+          if (lane < p.T) {
+            float v[M];
 #pragma unroll
-            for (int m = 0; m < (GATED ? 2 : 1); m++)
+            for (int m = 0; m < M; m++)
               v[m] = exact_sum(mine[m], 128 - z[m], total,
                                p.K <= 65536 && (uint32_t)z[m] < 256u) * (xs * sc[m]);
-            const int64_t at = (int64_t)ft * p.N + n;
+            const int64_t at = (int64_t)lane * p.N + item;
             auto put = [&](void* base, float f) {
               static_cast<uint16_t*>(base)[at] = f32_to_elem(f, p.bf16);
             };
@@ -242,30 +232,28 @@ __global__ __launch_bounds__(kWaves * 64) void few_kernel(const GemmArgs p) {
         }
         step = 0;
         item += stride;
-        load_params(min(item, items - 1));
+        load_params(item);
       }
     }
   }
 }
 
-template <int TT, int RR, bool GATED, bool FUSED>
+template <int TT, bool GATED, bool FUSED>
 hipError_t launch_one(const GemmArgs& p, hipStream_t stream) {
-  constexpr int RO = GATED ? RR / 2 : RR;
   constexpr int most = 256 + kFewMostCodes;
   const int bytes = 256 + p.T * few_pitch(p.K);
-  auto kernel = few_kernel<TT, RR, GATED, FUSED>;
+  auto kernel = few_kernel<TT, GATED, FUSED>;
   hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), most);
   if (e != hipSuccess) return e;
-  const int items = (p.N + RO - 1) / RO;
-  const int groups = items < device_cu_count() ? items : device_cu_count();
+  const int groups = p.N < device_cu_count() ? p.N : device_cu_count();
   kernel<<<dim3((unsigned)groups), dim3(kWaves * 64), bytes, stream>>>(p);
   return hipGetLastError();
 }
 
-template <int TT, int RR, bool GATED>
+template <int TT, bool GATED>
 hipError_t launch_x(const GemmArgs& p, hipStream_t stream) {
-  return p.a ? launch_one<TT, RR, GATED, false>(p, stream)
-             : launch_one<TT, RR, GATED, true>(p, stream);
+  return p.a ? launch_one<TT, GATED, false>(p, stream)
+             : launch_one<TT, GATED, true>(p, stream);
 }
 
 }  // namespace
@@ -279,12 +267,12 @@ bool few_takes(int64_t T, int64_t K, bool gated) {
 
 hipError_t launch_few(const GemmArgs& p, bool gated, hipStream_t stream) {
   if (gated) {
-    if (p.T <= 1) return launch_x<1, 2, true>(p, stream);
-    if (p.T <= 2) return launch_x<2, 2, true>(p, stream);
-    return launch_x<4, 2, true>(p, stream);
+    if (p.T <= 1) return launch_x<1, true>(p, stream);
+    if (p.T <= 2) return launch_x<2, true>(p, stream);
+    return launch_x<4, true>(p, stream);
   }
-  if (p.T <= 1) return launch_x<1, 1, false>(p, stream);
-  return launch_x<2, 1, false>(p, stream);
+  if (p.T <= 1) return launch_x<1, false>(p, stream);
+  return launch_x<2, false>(p, stream);
 }
 
 }  // namespace lowbit
