@@ -5,8 +5,8 @@ from __future__ import annotations
 
 import os
 
-import numpy as np
 import pytest
+import torch  # before the library, which takes the HIP runtime that torch has loaded
 
 import test_w8a8_host as host
 from test_w8a8_host import lw  # noqa: F401
@@ -51,7 +51,6 @@ def test_the_header_says_so(lw):  # noqa: F811
 @pytest.mark.gpu
 def test_one_workspace_of_the_largest_size_serves_all(lw):  # noqa: F811
     """Calls of many token counts in turn, each with what the others left in their one workspace."""
-    import torch
     if not torch.cuda.is_available():
         pytest.skip("no GPU")
     from test_w8a8_gpu import random_weights
