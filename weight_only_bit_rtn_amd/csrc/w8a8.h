@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.h"
+#include "w8a8_plan.h"
 
 namespace lowbit {
 
@@ -221,51 +222,11 @@ __device__ __forceinline__ void store4(const GemmArgs& p, const Columns<GATED>& 
   }
 }
 
-// Tiles of a product: `whole` of them, as many as fill the CUs some times over,
-// are computed by one workgroup each, and each of the `rest` by `splits`
-// workgroups that share its steps and leave their sums in the workspace for a
-// second kernel to join.
-struct TilePlan {
-  int tiles_m, tiles_n, whole, rest, splits;
-  int blocks() const { return whole + rest * splits; }
-};
-// The plan that should finish first, and when.  A CU takes alone_us for a step
-// of a tile that it has to itself, and shared_us for each tile's where it has
-// several workgroups; a join costs about 7 us, and the partial sums (tile_bytes
-// for each share) are written and read again at about 8 TB/s (they stay in the
-// caches).
-inline TilePlan plan_tiles(int64_t tm, int64_t tn, int cus, int steps, double alone_us,
-                           double shared_us, double tile_bytes, double* us) {
-  const int64_t tiles = tm * tn, rest = tiles % cus, whole = tiles - rest;
-  const int64_t rounds = (tiles + cus - 1) / cus;
-  TilePlan best{(int)tm, (int)tn, (int)tiles, 0, 1};
-  *us = rounds * steps * (rounds > 1 ? shared_us : alone_us);
-  for (int z = 2; rest > 0 && z <= 16 && z <= steps / 4; z++) {
-    const int64_t more = (rest * z + cus - 1) / cus;
-    const double work = (double)(whole / cus) * steps + (double)(more * ((steps + z - 1) / z));
-    const double t = work * (whole / cus + more > 1 ? shared_us : alone_us) + 7.0 +
-                     (double)rest * z * tile_bytes * 2 / 8e6;
-    if (t < *us) {
-      best.whole = (int)whole;
-      best.rest = (int)rest;
-      best.splits = z;
-      *us = t;
-    }
-  }
-  return best;
-}
-
 // Products of one or two tokens (gated: up to four) whose codes fit LDS
-// (w8a8_few.hip).  Without p.a the kernel quantizes p.x itself: T K <= kFusedMost.
-constexpr int kFewMostCodes = 128 * 1024;
-constexpr int kFusedMost = 16384;
-bool few_takes(int64_t T, int64_t K, bool gated);
+// (w8a8_few.hip).  Without p.a the kernel quantizes p.x itself.
 hipError_t launch_few(const GemmArgs& p, bool gated, hipStream_t stream);
 
-// Products of at most 64 tokens (w8a8_skinny.hip), up to 16 in any case, and the
-// time that they should take.
-constexpr int kSkinnyMostT = 64;
-double skinny_us(int64_t T, int64_t N, int64_t K, bool gated);
+// Products of at most kSkinnyMostT tokens (w8a8_skinny.hip).
 hipError_t launch_skinny(const GemmArgs& p, bool gated, hipStream_t stream);
 
 hipError_t launch_quantize_act(const void* x, int dtype, int64_t T, int64_t K, int8_t* codes,

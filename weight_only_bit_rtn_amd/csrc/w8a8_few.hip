@@ -20,13 +20,8 @@ namespace lowbit {
 namespace {
 
 constexpr int kWaves = 16;
-constexpr int kChunk = 1024;   // bytes of a row per load
+constexpr int kChunk = kFewChunk;  // bytes of a row per load
 constexpr int kInFlight = 2;   // loads per lane
-
-// Bytes of one token's codes in LDS: whole chunks, zeros behind the last.
-__host__ __device__ constexpr int few_pitch(int K) {
-  return (K + kChunk - 1) / kChunk * kChunk;
-}
 
 // Sum over the 64 lanes, in lane 63.
 __device__ __forceinline__ int wave_sum_last(int v) {
@@ -257,13 +252,6 @@ hipError_t launch_x(const GemmArgs& p, hipStream_t stream) {
 }
 
 }  // namespace
-
-// Up to here whole rows read this way beat the rings of w8a8_skinny.hip, in us:
-// linear 2x11008x4096 14.0 / 14.5, but 4x28672x8192 43.2 / 41.2 and 8x12288x12288
-// 33.6 / 28.3; gated 4x4096x4096 10.1 / 12.0, but 8x28672x8192 95.9 / 89.3.
-bool few_takes(int64_t T, int64_t K, bool gated) {
-  return T <= (gated ? 4 : 2) && T * few_pitch((int)K) <= kFewMostCodes;
-}
 
 hipError_t launch_few(const GemmArgs& p, bool gated, hipStream_t stream) {
   if (gated) {

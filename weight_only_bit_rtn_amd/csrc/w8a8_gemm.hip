@@ -254,57 +254,6 @@ hipError_t launch_tile(const GemmArgs& p, const TilePlan& plan, i4_t* parts, hip
   return hipGetLastError();
 }
 
-// Tile shapes: tokens, weight rows, bytes of k per step, and what a step of one
-// tile takes of a CU's time when there is one tile for each CU at most, and when
-// there are more (us, measured).  The larger the tile the less LDS traffic per
-// output; the smaller ones are for sizes that would leave CUs idle or pad much,
-// and for those that wait for the weights from HBM.  Steps of 128 bytes read
-// whole cache lines and halve the barriers; the last three have no LDS for three
-// buffers of them, and two are slower (gated 4096x28672x8192 1847 / 1670 us).
-// With a shape and without it, us: 64 x 128 on 64x49152x12288 148 / 217, gated
-// 64x11008x4096 21.4 / 26.4; 128 x 128 in eight waves and 128 bytes instead of
-// four and 64 on 128x28672x8192 45.8 / 55.6, 1000x4096x4096 31.1 / 38.2;
-// 256 x 128 on 250x28672x8192 69 / 101, 2000x4096x4096 51.0 / 58.6; 192 x 192 on
-// gated 333x11008x4096 46.4 / 58.1 (of 64 bytes 50.8, in six waves 55.9).
-struct TileShape {
-  int mt, nt, step;
-  double alone_us, shared_us;
-};
-constexpr TileShape kShapes[] = {
-    {64, 128, 128, 0.55, 0.70},  {128, 128, 128, 0.63, 0.80}, {256, 128, 128, 1.15, 1.32},
-    {192, 192, 128, 1.35, 1.50}, {256, 192, 64, 0.90, 0.90},  {256, 256, 64, 1.03, 1.03},
-    {256, 384, 64, 1.42, 1.42}};
-
-// The kernel and shape that should finish first.
-struct GemmPlan {
-  TilePlan tiles;
-  int shape;  // -1: the rings of w8a8_skinny.hip
-  size_t part_bytes() const {
-    return shape < 0 ? 0
-                     : (size_t)tiles.rest * tiles.splits * kShapes[shape].mt * kShapes[shape].nt * 4;
-  }
-};
-GemmPlan gemm_plan(int64_t T, int64_t N, int64_t K, bool gated) {
-  const int cus = device_cu_count();
-  const int64_t rows = gated ? 2 * N : N;
-  GemmPlan best{{}, -1};
-  if (T <= 16) return best;
-  double least = T <= kSkinnyMostT ? skinny_us(T, N, K, gated) : 1e30;
-  for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); i++) {
-    const TileShape& t = kShapes[i];
-    double us;
-    const int steps = (int)((K + t.step - 1) / t.step);
-    const TilePlan plan = plan_tiles((T + t.mt - 1) / t.mt, (rows + t.nt - 1) / t.nt, cus, steps,
-                                     t.alone_us, t.shared_us, (double)t.mt * t.nt * 4, &us);
-    us += 2;  // the ring's first filling, and the outputs
-    if (us < least) {
-      best = {plan, i};
-      least = us;
-    }
-  }
-  return best;
-}
-
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // Codes, scales and sums of the activations in the workspace.
@@ -349,7 +298,7 @@ hipError_t launch(const Activations& x, int64_t T, const W8& w0, const W8& w1, i
   p.act = act;
   p.bf16 = out_dtype == kBF16;
   if (few_takes(T, K, GATED)) return launch_few(p, GATED, stream);
-  const GemmPlan plan = gemm_plan(T, N, K, GATED);
+  const GemmPlan plan = gemm_plan(T, N, K, GATED, device_cu_count());
   if (plan.shape < 0) return launch_skinny(p, GATED, stream);
   auto* parts = reinterpret_cast<i4_t*>(static_cast<uint8_t*>(workspace) +
                                         (x.dtype == kI8 ? 0 : code_bytes(T, K)));
@@ -376,7 +325,7 @@ hipError_t launch(const Activations& x, int64_t T, const W8& w0, const W8& w1, i
 size_t w8a8_workspace_bytes(int64_t T, int64_t N, int64_t K, int dtype, bool gated) {
   if (T == 0 || N == 0) return 0;
   const size_t codes = dtype == kI8 || fused(T, K, dtype, gated) ? 0 : code_bytes(T, K);
-  return codes + (few_takes(T, K, gated) ? 0 : gemm_plan(T, N, K, gated).part_bytes());
+  return codes + (few_takes(T, K, gated) ? 0 : gemm_plan(T, N, K, gated, device_cu_count()).part_bytes());
 }
 
 hipError_t launch_linear_w8a8(const Activations& x, int64_t T, const W8& w, int64_t N, int64_t K,

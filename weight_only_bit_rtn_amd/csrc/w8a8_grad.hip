@@ -22,8 +22,6 @@
 namespace lowbit {
 namespace {
 
-constexpr int kStepN = 64;  // weight rows per pipeline step
-
 struct PrepArgs {
   const uint16_t* d;
   const uint16_t* gate;
@@ -568,56 +566,13 @@ void launch_prep(const PrepArgs& q, int64_t T, bool bf16, hipStream_t stream) {
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 int64_t padded(int64_t N) { return (N + kStepN - 1) / kStepN * kStepN; }
 
-// Tile shapes: tokens, columns of dx, and what a step of 64 weight rows of one
-// tile takes of a CU's time when the CU has no other workgroup, and when it has
-// (us, measured).  64 x 256 reads the tokens' factors half as often as 64 x 128
-// and pays where the weights are large (gated 64x28672x8192 125 / 145 us,
-// 61x11008x4096 33.1 / 33.4); for 16 or 32 tokens, whose factors are fewer, 256
-// columns gave nothing (16x28672x8192 117 / 122, 10x12288x12288 40.5 / 37.5).
-struct TileShape {
-  int mt, kt;
-  double alone_us, shared_us;
-};
-// 128 x 256 beside 128 x 128: 2000x4096x4096 83 / 87, gated 128x28672x8192 168 /
-// 178, but 1000x1024x1024 24.9 / 22.1.
-constexpr TileShape kShapes[] = {
-    {16, 128, 0.40, 0.32},  {32, 128, 0.40, 0.32},  {64, 128, 0.50, 0.40},  {64, 256, 0.64, 0.64},
-    {128, 128, 0.74, 0.55}, {128, 256, 1.06, 1.06}, {256, 192, 1.20, 1.20}, {256, 256, 1.60, 1.60}};
-
-// The shape that should finish first, of those that hold T tokens without waste.
-struct GradPlan {
-  TilePlan tiles;
-  int shape;
-  size_t part_bytes() const {
-    return (size_t)tiles.rest * tiles.splits * kShapes[shape].mt * kShapes[shape].kt * 4;
-  }
-};
-GradPlan grad_plan(int64_t T, int64_t K, int steps) {
-  const int cus = device_cu_count();
-  const int from = T <= 16 ? 0 : T <= 32 ? 1 : T <= 64 ? 2 : 4;
-  const int to = T <= 32 ? from : T <= 64 ? 3 : 7;
-  GradPlan best{};
-  double least = 0;
-  for (int i = from; i <= to; i++) {
-    const TileShape& t = kShapes[i];
-    double us;
-    const TilePlan plan = plan_tiles((T + t.mt - 1) / t.mt, (K + t.kt - 1) / t.kt, cus, steps,
-                                     t.alone_us, t.shared_us, (double)t.mt * t.kt * 4, &us);
-    if (least == 0 || us < least) {
-      best = {plan, i};
-      least = us;
-    }
-  }
-  return best;
-}
-
 }  // namespace
 
 size_t w8a8_grad_workspace_bytes(int64_t T, int64_t N, int64_t K, bool gated) {
   if (T == 0) return 0;
   const int64_t pitch = padded(N) * (gated ? 2 : 1);
   return up256((size_t)T * pitch * 2) + 2 * up256((size_t)T * 4) +
-         grad_plan(T, K, (int)(pitch / kStepN)).part_bytes();
+         grad_plan(T, K, (int)(pitch / kStepN), device_cu_count()).part_bytes();
 }
 
 hipError_t launch_w8a8_grad(const void* dh, const void* gate, const void* up, int dtype, int64_t T,
@@ -663,7 +618,7 @@ hipError_t launch_w8a8_grad(const void* dh, const void* gate, const void* up, in
   p.half_steps = (int)(half / kStepN);
   p.steps = (int)(pitch / kStepN);
   p.bf16 = bf16;
-  const GradPlan plan = grad_plan(T, K, p.steps);
+  const GradPlan plan = grad_plan(T, K, p.steps, device_cu_count());
   auto* parts =
       reinterpret_cast<f4_t*>(reinterpret_cast<uint8_t*>(q.e) + up256((size_t)T * 4));
   switch (plan.shape) {

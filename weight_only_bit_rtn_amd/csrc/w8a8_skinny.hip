@@ -178,17 +178,6 @@ hipError_t launch_tokens(const GemmArgs& p, hipStream_t stream) {
 
 }  // namespace
 
-// The kernel's time, fitted to measured ones: the tokens are read again with each
-// tile of 16 weight rows.  In us, against 64 x 128 tiles of w8a8_gemm.hip:
-// 64x28672x8192 69 / 42, gated 64x28672x8192 120 / 104, 64x12288x12288 45 / 33,
-// but 24x12288x12288 31.5 / 32.4 and, where those would have to share few tiles
-// out, 64x4096x4096 12.6 / 15.4, 45x4096x11008 from codes 13.8 / 14.5.
-double skinny_us(int64_t T, int64_t N, int64_t K, bool gated) {
-  const double bytes = (double)N * K * (gated ? 2 : 1);
-  const double tokens = (double)((T + 15) / 16) / (gated ? 2 : 1);
-  return 1.5 + bytes * (0.165 + 0.03 * tokens) * 1e-6;
-}
-
 hipError_t launch_skinny(const GemmArgs& p, bool gated, hipStream_t stream) {
   return gated ? launch_tokens<true>(p, stream) : launch_tokens<false>(p, stream);
 }
