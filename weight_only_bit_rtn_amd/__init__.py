@@ -50,7 +50,8 @@ class LowbitError(RuntimeError):
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
-    """Load liblowbit.so (raises if it has not been built)."""
+    """Load liblowbit.so (raises if it has not been built).  A program that uses torch imports it before:
+    the library then takes the HIP runtime that torch brings, and not a second one into the process."""
     global _lib
     if _lib is not None:
         return _lib

@@ -38,7 +38,10 @@ __device__ __forceinline__ uint16_t f32_to_elem(float v, bool bf16) {
 // sigma = 1 / (1 + e^-2q) with 2q = v (SiLU) or 2p (GELU, tanh form): both
 // activations are v * sigma.  e^-2q overflows to infinity for very negative
 // arguments and sigma is then 0, the limit.  GELU's cube is taken of v within
-// [-16, 16]: beyond, sigma is 0 or 1 in fp32 already and its slope 0.
+// [-16, 16]: beyond, sigma is 0 or 1 in fp32 already and its slope 0.  The
+// hardware's exp2 and reciprocal are off by some 2^-24 of sigma each, and by 2^-24 for
+// each unit of 2q, far below the 16-bit outputs' steps; the library's expf and a
+// division took 420 -> 483 us on gated 4096x28672x1024, 47.8 -> 50.3 on 333x11008x4096.
 __device__ __forceinline__ float act_sigma(float v, int act) {
   float e;
   if (act == kSilu) {

@@ -4,7 +4,7 @@
 // token), so each wave reads whole rows as they lie, 1 KiB per instruction,
 // and multiplies with v_dot4_i32_i8; the matrix cores would want 16 rows per
 // instruction, 64 bytes of each, and reading in such pieces ran at 5.0-5.6
-// TB/s where whole rows ran at 6.0 TB/s (1x28672x8192 gated, 79 us; 1x49152x12288, 100 us).
+// TB/s where whole rows run at 5.9.
 //
 // One workgroup of 16 waves per CU keeps the tokens' codes in LDS: it
 // quantizes x itself when that is little (T K <= kFusedMost), while its
@@ -12,8 +12,9 @@
 // workgroup b takes rows w G + b, then 16 G further (G workgroups), so few
 // rows still spread over all CUs.  Two loads per lane are in flight, running
 // ahead into the wave's next rows: 16 waves cover the latency, and loads past
-// the last row only cost time (2 / 4 / 8 per lane: 1x4096x4096 5.9 / 6.1 / 7.4
-// us, gated 1x28672x8192 81.7 / 83.6 / 82.7, 1x49152x12288 106 / 105 / 108).
+// the last row only cost time (2 / 4 / 8 per lane, kernel alone, on weights rotated
+// over 1 GiB: 1x256x256 4.6 / 5.1 / 6.3 us, 1x4096x4096 7.2 / 7.4 / 8.4, gated
+// 1x28672x8192 79 / 81 / 80, 1x49152x12288 103 / 101 / 101).
 #include "w8a8.h"
 
 namespace lowbit {

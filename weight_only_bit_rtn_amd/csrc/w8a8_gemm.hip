@@ -23,15 +23,21 @@ namespace {
 // counted).  Values past the row's end, tokens past T and rows past N come as
 // zeros from the buffers' range check.
 //
-// What bounds the large tiles is LDS: 64 bytes per clock and CU, measured for ds_read_b128
-// in any conflict-free pattern.  256 x 256 outputs want 96 KiB of operand reads
-// (eight waves of 128 x 64) and 32 KiB written per step, about 1800 clocks for
-// 1024 of matrix work; 256 x 384 (128 x 96 per wave, the most that 256
-// registers hold) 112 and 40 KiB for 1536.  Measured on 4096x12288x12288: 541
-// and 505 us (2.3 and 2.45 POP/s), on long runs at a clock that power holds
-// near 1.9 GHz.  Slower there: 128 x 128 per wave with one wave per SIMD (a
-// third fewer reads, but a lone wave cannot issue fast enough: 577 us), weights
-// straight from L2 into registers (750 us), 32x32x32 products (620 us).
+// What bounds the large tiles: no one thing.  4096x12288x12288 takes 500-533 us in
+// tiles of 256 x 384 (2.3-2.5 POP/s; 128 x 96 per wave is the most that 256
+// registers hold), the whole call 531, and 577 with tiles of 256 x 256 at most.
+// Power holds the clock at 1.9 GHz, and 63% of the clocks are products.  With a part
+// left out: 423 us without the direct loads (of 192 steps' 40 KiB a tile),
+// 501 without the operand reads (112 KiB a step; LDS gives 230 bytes a clock and CU
+// and is busy with them for a fifth of the time), 402 without both, 396 without the
+// products.  Slower there, against 541 us for 256 x 256 at the time: 128 x 128 per wave
+// with one wave per SIMD (a third fewer reads, but a lone wave cannot issue fast
+// enough: 577), weights straight from L2 into registers (750), 32x32x32 products (620).
+//
+// Short inputs pay as much around the steps: gated 333x11008x4096 with its
+// projections kept takes 44 us in 192 x 192 tiles, 0.88 us for each of 32 steps
+// (half of it products) and 16 us before and after them (the first loads, the
+// activation, three outputs of 7.3 MB); 12.5 where only h goes out.
 template <int MT, int NT, int WM, int WN, int NB, int SUB, bool GATED>
 __global__ __launch_bounds__(WM* WN * 64, 2) void w8a8_kernel(const GemmArgs p, const TilePlan plan,
                                                                  i4_t* __restrict__ parts) {
@@ -325,7 +331,8 @@ hipError_t launch(const Activations& x, int64_t T, const W8& w0, const W8& w1, i
 size_t w8a8_workspace_bytes(int64_t T, int64_t N, int64_t K, int dtype, bool gated) {
   if (T == 0 || N == 0) return 0;
   const size_t codes = dtype == kI8 || fused(T, K, dtype, gated) ? 0 : code_bytes(T, K);
-  return codes + (few_takes(T, K, gated) ? 0 : gemm_plan(T, N, K, gated, device_cu_count()).part_bytes());
+  if (few_takes(T, K, gated)) return codes;
+  return codes + gemm_plan(T, N, K, gated, device_cu_count()).part_bytes();
 }
 
 hipError_t launch_linear_w8a8(const Activations& x, int64_t T, const W8& w, int64_t N, int64_t K,

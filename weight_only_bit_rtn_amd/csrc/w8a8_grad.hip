@@ -11,8 +11,11 @@
 // keep their 11 significant bits, down to factors of 2^-29 of the token's largest.
 // (a is formed in fp32; where a token's are so small that bits would be lost
 // there, with scales 2^100 times as large.)  Rounding a to fp16 is the one
-// rounding between the inputs and the output: the matrix cores take 16-bit
-// operands at the rate measured here, and bf16 would keep 8 bits.
+// rounding between the inputs and the output, and a choice: dx of fp16 inputs is
+// 2.9e-4 off in the 2-norm where 32-bit factors give 2.1e-4, the output's own
+// rounding (bf16 outputs: 1.7e-3 either way).  Keeping 22 bits in two fp16 terms is
+// twice the products: 1000x4096x11008 92 -> 180 us, gated 64x28672x8192 116 -> 152,
+// gated 4096x28672x8192 3.06 -> 6.20 ms.  bf16 factors would keep 8 bits.
 //
 // Two kernels: one makes a', e and r (and, for the gated block, the gradients
 // of both projections on the way), one multiplies.  The gated block's two
@@ -202,11 +205,11 @@ __device__ __forceinline__ void tiny_factors(const PrepArgs& p, int64_t row, flo
 // linear layer.  NC > 0: the factors stay in registers, NC chunks per thread,
 // between their largest and their rounding, so the inputs are read once; NC == 0
 // (rows longer than that): they are made twice.  Bound by HBM with many tokens
-// (4096 of 2 x 28672, dg and du written too: 340 us, 4.8 TB/s), by the vector
-// ALUs of a token's CU with few (64 of 2 x 28672 14.7 us; 17.6 with the
+// (4096 of 2 x 28672, dg and du written too: 338 us, 4.9 TB/s), by the vector
+// ALUs of a token's CU with few (64 of 2 x 28672 13.9 us; a quarter more with the
 // activation and the type decided at run time, whose branches part the values).
 // Each row's scales and zero points come from L2.  Rows that lie at 2 bytes:
-// 61 of 2 x 11007 15.8 us, of 2 x 11008 7.2.
+// 61 of 2 x 11007 16.5 us, of 2 x 11008 8.5.
 template <int ACT, bool BF, int NC, bool WHOLE>
 __global__ __launch_bounds__(1024) void grad_prep_kernel(const PrepArgs p) {
   __shared__ float red[16];
@@ -328,12 +331,15 @@ __device__ __forceinline__ void store_dx(const GradArgs& p, f4_t sum, float r, i
 // rows of 16 bytes and get a column each).  A step is two halves of 32 rows:
 // while one half is multiplied, the operands of the next are read.
 //
-// 4096 x (2 x 28672) x 8192 takes 2.65-2.8 ms, 1.4 PFLOP/s: the matrix cores
+// 4096 x (2 x 28672) x 8192 takes 2.7-2.8 ms, 1.4 PFLOP/s: the matrix cores
 // are busy in 73% of the clocks, at 1.8 GHz, which is all that power allows here
-// (products from registers alone reach 2.0 PFLOP/s at 1.9 GHz), and LDS moves
-// 208 KiB per step and CU in 2800 clocks.  Slower there: four waves of 128 x 128
-// (2.92 ms), steps of 32 rows (3.1 ms).  The small tiles wait for the weights
-// from HBM: 61 x (2 x 11008) x 4096 takes 19.5 us, 4.6 TB/s.
+// (products from registers alone reach 2.0 PFLOP/s at 1.9 GHz).  With a part left
+// out, of 2.75 ms: 2.27 without the direct loads, 2.48 without the operand reads,
+// 2.12 without both, 1.49 without the products; of the 89 us of 1000x4096x11008
+// 81, 85, 76 and 53.  Slower there: four waves of 128 x 128 (2.92 ms), steps of 32
+// rows (3.1 ms).  The small tiles wait for the weights: 61 x (2 x 11008) x 4096
+// takes 26 us on weights rotated over 1 GiB (3.5 TB/s), 20 where they lie in the
+// last-level cache.
 template <int MT, int KT, int WM, int WN, int NB>
 __global__ __launch_bounds__(WM* WN * 64, 2) void grad_kernel(const GradArgs p, const TilePlan plan,
                                                                  f4_t* __restrict__ parts) {

@@ -56,9 +56,11 @@ constexpr int few_pitch(int K) {
   return (K + kFewChunk - 1) / kFewChunk * kFewChunk;
 }
 
-// Up to here whole rows read this way beat the rings of w8a8_skinny.hip, in us:
-// linear 2x11008x4096 14.0 / 14.5, but 4x28672x8192 43.2 / 41.2 and 8x12288x12288
-// 33.6 / 28.3; gated 4x4096x4096 10.1 / 12.0, but 8x28672x8192 95.9 / 89.3.
+// Up to here whole rows read this way beat the rings of w8a8_skinny.hip, in us a
+// call on weights rotated over 1 GiB: linear 2x11008x4096 12.1 / 16.3, 2x28672x8192
+// 42.6 / 44.5; gated 4x4096x4096 12.1 / 16.4, though 4x28672x8192 84.0 / 83.1.  With
+// kernels for more tokens, on weights in the last-level cache: linear 4x28672x8192
+// 43.2 / 41.2, 8x12288x12288 33.6 / 28.3, gated 8x28672x8192 95.9 / 89.3.
 inline bool few_takes(int64_t T, int64_t K, bool gated) {
   return T <= (gated ? 4 : 2) && T * few_pitch((int)K) <= kFewMostCodes;
 }
@@ -66,11 +68,13 @@ inline bool few_takes(int64_t T, int64_t K, bool gated) {
 // skinny_kernel takes up to 16 tokens in any case.
 constexpr int kSkinnyMostT = 64;
 
-// The kernel's time, fitted to measured ones: the tokens are read again with each
-// tile of 16 weight rows.  In us, against 64 x 128 tiles of w8a8_gemm.hip:
-// 64x28672x8192 69 / 42, gated 64x28672x8192 120 / 104, 64x12288x12288 45 / 33,
-// but 24x12288x12288 31.5 / 32.4 and, where those would have to share few tiles
-// out, 64x4096x4096 12.6 / 15.4, 45x4096x11008 from codes 13.8 / 14.5.
+// The rings' time, fitted to kernels on weights in the last-level cache: the tokens
+// are read again with each tile of 16 weight rows.  In us a call, against 64 x 128
+// tiles of w8a8_gemm.hip, on weights rotated over 1 GiB (in brackets: in the cache):
+// 64x28672x8192 84 / 57 (64 / 41), gated 64x28672x8192 115 / 98, 64x12288x12288
+// 60 / 46 (43 / 33), but 24x12288x12288 41.8 / 40.9 (30.9 / 31.4) and, where those
+// would have to share few tiles out, 64x4096x4096 16.1 / 19.4, 45x4096x11008 from
+// codes 17.4 / 17.0 (13.6 / 16.8).
 inline double skinny_us(int64_t T, int64_t N, int64_t K, bool gated) {
   const double bytes = (double)N * K * (gated ? 2 : 1);
   const double tokens = (double)((T + 15) / 16) / (gated ? 2 : 1);
@@ -79,16 +83,17 @@ inline double skinny_us(int64_t T, int64_t N, int64_t K, bool gated) {
 
 // Tile shapes: tokens, weight rows, bytes of k per step, and what a step of one
 // tile takes of a CU's time when there is one tile for each CU at most, and when
-// there are more (us, measured).  The larger the tile the less LDS traffic per
-// output; the smaller ones are for sizes that would leave CUs idle or pad much,
-// and for those that wait for the weights from HBM.  Steps of 128 bytes read
-// whole cache lines and halve the barriers; the last three have no LDS for three
-// buffers of them, and two are slower (gated 4096x28672x8192 1847 / 1670 us).
-// With a shape and without it, us: 64 x 128 on 64x49152x12288 148 / 217, gated
-// 64x11008x4096 21.4 / 26.4; 128 x 128 in eight waves and 128 bytes instead of
-// four and 64 on 128x28672x8192 45.8 / 55.6, 1000x4096x4096 31.1 / 38.2;
-// 256 x 128 on 250x28672x8192 69 / 101, 2000x4096x4096 51.0 / 58.6; 192 x 192 on
-// gated 333x11008x4096 46.4 / 58.1 (of 64 bytes 50.8, in six waves 55.9).
+// there are more (us; fitted to calls, so part of what lies around the steps is in
+// it: 192 x 192 takes 0.88 us a step and 13-16 us around them).  The larger the tile
+// the less is loaded per output; the smaller ones are for sizes that would leave CUs
+// idle or pad much, and for those that wait for the weights.  Steps of 128 bytes
+// read whole cache lines and halve the barriers; the last three have no LDS for three
+// buffers of them, and two are slower (gated 4096x28672x8192 by a tenth).
+// With a shape and without it, us a call on weights rotated over 1 GiB: 64 x 128 on
+// 64x49152x12288 143 / 155, gated 64x11008x4096 30.0 / 32.3; 128 x 128 on
+// 128x28672x8192 64 / 72, 1000x4096x4096 33.5 / 42; 256 x 128 on 250x28672x8192
+// 82 / 105, 2000x4096x4096 50.5 / 53; 192 x 192 on gated 333x11008x4096 47 / 58; 256 x
+// 384 on 4096x12288x12288 531 / 577, gated 4096x28672x8192 1822 / 1856.
 struct ProductShape {
   int mt, nt, step;
   double alone_us, shared_us;
@@ -135,16 +140,20 @@ constexpr int kStepN = 64;  // weight rows per pipeline step
 
 // Tile shapes: tokens, columns of dx, and what a step of 64 weight rows of one
 // tile takes of a CU's time when the CU has no other workgroup, and when it has
-// (us, measured).  64 x 256 reads the tokens' factors half as often as 64 x 128
-// and pays where the weights are large (gated 64x28672x8192 125 / 145 us,
-// 61x11008x4096 33.1 / 33.4); for 16 or 32 tokens, whose factors are fewer, 256
-// columns gave nothing (16x28672x8192 117 / 122, 10x12288x12288 40.5 / 37.5).
+// (us; fitted so that the shapes come out in the order of whole calls.  Steps alone
+// take 1.12 of 128 x 256, 1.39 of 256 x 192, 1.53 of 256 x 256, and with those
+// 2000x4096x4096 took 83 for 80 us and gated 128x28672x8192 168 for 152, though
+// gated 300x11008x4096 93 for 95).  64 x 256 reads the tokens' factors half as often
+// as 64 x 128 and pays where the weights are large (with and without it, on weights
+// rotated over 1 GiB: gated 64x28672x8192 117 / 138 us, 61x11008x4096 39 / 42); for 16
+// or 32 tokens, whose factors are fewer, 256 columns gave nothing (gated
+// 16x28672x8192 117 / 122, linear 10x12288x12288 40.5 / 37.5).
 struct GradShape {
   int mt, kt;
   double alone_us, shared_us;
 };
-// 128 x 256 beside 128 x 128: 2000x4096x4096 83 / 87, gated 128x28672x8192 168 /
-// 178, but 1000x1024x1024 24.9 / 22.1.
+// 128 x 256 beside 128 x 128: 2000x4096x4096 80 / 83, gated 128x28672x8192 152 / 168,
+// 300x11008x4096 95 / 101, but 1000x1024x1024 24.9 / 22.1, where it is not taken.
 constexpr GradShape kGradShapes[] = {
     {16, 128, 0.40, 0.32},  {32, 128, 0.40, 0.32},  {64, 128, 0.50, 0.40},  {64, 256, 0.64, 0.64},
     {128, 128, 0.74, 0.55}, {128, 256, 1.06, 1.06}, {256, 192, 1.20, 1.20}, {256, 256, 1.60, 1.60}};

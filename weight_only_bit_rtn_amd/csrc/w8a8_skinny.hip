@@ -9,10 +9,13 @@
 // matrix cores take 16 rows by up to four times 16 tokens from there.  The
 // waves' integer sums meet in LDS once per tile.
 //
-// Measured (with the token quantizer where it runs): 45x4096x11008 from codes
-// 13.7 us (3.3 TB/s; reading both operands into registers in 64-byte pieces
-// took 23-25), linear 8x28672x8192 41 us, gated 8x28672x8192 89 us (5.3 TB/s).
-// Short rows end the wave's stream before it is in full flow: 8x4096x4096 5 us.
+// Measured, kernel alone, on weights rotated over 1 GiB: linear 8x28672x8192 41 us
+// (5.7 TB/s), gated 8x28672x8192 78 (6.0).  Short rows end the wave's stream before
+// it is in full flow: 8x4096x4096 7.8 (2.1).  The more tokens, the more of what a
+// workgroup reads are their codes, again for each 16 weight rows: for 48 tokens
+// three bytes from L2 for each byte of weights, 45x4096x11008 from codes 18 us, or 14
+// where the weights lie in the last-level cache (reading both operands into
+// registers in 64-byte pieces took 23-25).
 #include "w8a8.h"
 
 namespace lowbit {
