@@ -367,3 +367,13 @@ from .w8a8 import (  # noqa: E402,F401
     gated_w8a8_grad_workspace_bytes, gated_w8a8_raw, gated_w8a8_workspace_bytes, linear_w8a8,
     linear_w8a8_grad, linear_w8a8_grad_raw, linear_w8a8_grad_workspace_bytes, linear_w8a8_raw,
     linear_w8a8_workspace_bytes, quantize_act, quantize_act_raw)
+
+# adapters beside the projections (include/lowbit_lora.h)
+from .adapters import (  # noqa: E402,F401
+    EXPORTED_LORA, LORA_MAX_L, LORA_MAX_R, lora, lora_grad, lora_grad_raw,
+    lora_grad_workspace_bytes, lora_plan, lora_plan_raw, lora_raw, lora_workspace_bytes)
+
+# the AdamW step (include/lowbit_adamw.h)
+from .optimizer import (  # noqa: E402,F401
+    ADAMW_BLOCK, EXPORTED_ADAMW, AdamwOptions, AdamwState, adamw, adamw_moments, adamw_moments_raw,
+    adamw_raw, adamw_state)

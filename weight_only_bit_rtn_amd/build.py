@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 SOURCES = ["abi.hip", "quantize.hip", "gemv.hip", "gemv2.hip", "gemv3.hip", "gemv4.hip", "gemv8.hip", "gemv_mma.hip", "gemm.hip", "gptq.hip",
            "abi_w8a8.hip", "act_quant.hip", "w8a8_few.hip", "w8a8_gemm.hip",
-           "w8a8_grad.hip", "w8a8_skinny.hip"]
+           "w8a8_grad.hip", "w8a8_skinny.hip",
+           "abi_lora.hip", "lora_plan.hip", "lora.hip", "lora_grad.hip", "abi_adamw.hip", "adamw.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
