@@ -42,8 +42,8 @@
  *
  * Shape rules (violations return LOWBIT_ERR_SHAPE): K > 0, K % 32 == 0,
  * K <= LOWBIT_W8A8_MAX_K; R > 0, R % 8 == 0, R <= LOWBIT_LORA_MAX_R;
- * 1 <= L <= LOWBIT_LORA_MAX_L; N > 0; T, N <= LOWBIT_W8A8_MAX_TN; T * N, T * K,
- * L * R * K and L * R * N <= 2^36.  Any N, odd ones too.  T == 0 is an empty
+ * 1 <= L <= LOWBIT_LORA_MAX_L; N >= LOWBIT_LORA_MIN_N; T, N <= LOWBIT_W8A8_MAX_TN;
+ * T * N, T * K, L * R * K and L * R * N <= 2^36.  Odd N too.  T == 0 is an empty
  * problem (da and db of it are zero).
  * An order that is not a permutation or starts that do not rise give unspecified
  * results, but no access outside the buffers.
@@ -62,6 +62,7 @@ extern "C" {
 
 #define LOWBIT_LORA_MAX_R 128
 #define LOWBIT_LORA_MAX_L 1024
+#define LOWBIT_LORA_MIN_N 8
 
 /*
  * The plan of a batch: order and starts from ids[T], each token's adapter.  An id

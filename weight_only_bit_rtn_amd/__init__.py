@@ -370,7 +370,7 @@ from .w8a8 import (  # noqa: E402,F401
 
 # adapters beside the projections (include/lowbit_lora.h)
 from .adapters import (  # noqa: E402,F401
-    EXPORTED_LORA, LORA_MAX_L, LORA_MAX_R, lora, lora_grad, lora_grad_raw,
+    EXPORTED_LORA, LORA_MAX_L, LORA_MAX_R, LORA_MIN_N, lora, lora_grad, lora_grad_raw,
     lora_grad_workspace_bytes, lora_plan, lora_plan_raw, lora_raw, lora_workspace_bytes)
 
 # the AdamW step (include/lowbit_adamw.h)

@@ -21,6 +21,7 @@ from .w8a8 import _apart, _check_tensor, _float_type, _out, _run, _torch
 
 LORA_MAX_R = 128
 LORA_MAX_L = 1024
+LORA_MIN_N = 8
 
 EXPORTED_LORA = ("lowbit_lora_plan", "lowbit_lora_workspace_bytes", "lowbit_lora",
                  "lowbit_lora_grad_workspace_bytes", "lowbit_lora_grad")

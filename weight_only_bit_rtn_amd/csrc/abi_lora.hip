@@ -20,7 +20,7 @@ int check_sizes(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L) {
   const int rc = check_plan(T, L);
   if (rc != LOWBIT_OK) return rc;
   if (N < 0 || K < 0 || R < 0) return LOWBIT_ERR_ARG;
-  if (N == 0 || N > LOWBIT_W8A8_MAX_TN || K == 0 || K % 32 != 0 || K > LOWBIT_W8A8_MAX_K) return LOWBIT_ERR_SHAPE;
+  if (N < LOWBIT_LORA_MIN_N || N > LOWBIT_W8A8_MAX_TN || K == 0 || K % 32 != 0 || K > LOWBIT_W8A8_MAX_K) return LOWBIT_ERR_SHAPE;
   if (R == 0 || R % 8 != 0 || R > LOWBIT_LORA_MAX_R) return LOWBIT_ERR_SHAPE;
   if (T * N > kMost || T * K > kMost || L * R * K > kMost || L * R * N > kMost) return LOWBIT_ERR_SHAPE;
   return LOWBIT_OK;

@@ -29,6 +29,18 @@ struct LoraArgs {
   int64_t T;
 };
 
+// A kernel launch with `lds` bytes of dynamic LDS.
+template <typename... P, typename... A>
+hipError_t launch_lds(void (*kernel)(P...), dim3 grid, int threads, int lds, hipStream_t stream,
+                      A... args) {
+  if (lds > 64 * 1024) {
+    const hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), lds);
+    if (e != hipSuccess) return e;
+  }
+  kernel<<<grid, threads, lds, stream>>>(args...);
+  return hipGetLastError();
+}
+
 hipError_t launch_lora_plan(const int32_t* ids, int64_t T, int64_t L, int32_t* order,
                             int32_t* starts, hipStream_t stream);
 hipError_t launch_lora(const void* x, int dtype, const LoraArgs& p, const void* y, void* out,
@@ -164,6 +176,172 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ starts, in
 __device__ __forceinline__ int64_t token_at(const int32_t* __restrict__ order, int64_t T, int at) {
   const uint32_t t = (uint32_t)order[at];
   return t < (uint64_t)T ? (int64_t)t : 0;
+}
+
+// The wave's number within its workgroup, as a scalar: branches on it are uniform.
+__device__ __forceinline__ int wave_of_group() {
+  return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+}
+
+// Keeps the loads of one step together and in order.  The counter of loads under way is
+// waited on in order, and where two paths meet for the worst of both: loads of two steps that
+// are mixed before a loop make every round of it wait for the second one's too.
+__device__ __forceinline__ void loads_stay() { __builtin_amdgcn_sched_barrier(0); }
+
+// Matrices on their way to the matrix cores pass through an LDS region of the wave's own.
+// An operand wants row lane % 16 in every lane, but the vector cache serves four
+// consecutive lanes at once only where they lie within 64 bytes: loads in the operands'
+// order took 64 of its cycles for 1 KB instead of 16, and x was read at 3 TB/s however
+// many loads were under way.  So eight lanes load the 128 bytes of one row, and the operands
+// are read from LDS.  LDS serves a wave's accesses in order, so a region of its own needs no
+// wait but for the compiler's order:
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+// Rows of 64 elements, 16-byte chunk c of a row in slot c ^ (row / 2) % 8: the 16 rows of an
+// operand's read, and the eight of a lane group's write, take all banks.
+__device__ __forceinline__ int row_slot(int row, int chunk) {
+  return row * 64 + ((chunk ^ ((row >> 1) & 7)) << 3);
+}
+// ROWS rows as they were loaded, row 8 q + lane / 8 chunk lane % 8 in v[q].
+template <int ROWS>
+__device__ __forceinline__ void put_rows(uint16_t* to, const us8_t (&v)[ROWS / 8]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int q = 0; q < ROWS / 8; q++)
+    *reinterpret_cast<us8_t*>(to + row_slot(q * 8 + (lane >> 3), lane & 7)) = v[q];
+}
+// The operand of rows 16 block.. and terms 32 half..
+__device__ __forceinline__ us8_t get_operand(const uint16_t* from, int block, int half) {
+  const int lane = threadIdx.x & 63;
+  return *reinterpret_cast<const us8_t*>(
+      from + row_slot(block * 16 + (lane & 15), half * 4 + (lane >> 4)));
+}
+
+// Adds up the waves' sums of a tile, RB x TB products each, into wave 0's, half of the
+// waves into the other half again and again; two blocks of ranks at a time pass through
+// `lds`, reduce_bytes() of it.
+template <int RB, int TB, int W>
+constexpr int reduce_bytes() {
+  return W / 2 * TB * 16 * ((RB < 2 ? 1 : 2) * 16 + 4) * 4;
+}
+template <int RB, int TB, int W>
+__device__ __forceinline__ void reduce_waves(f4_t (&acc)[RB][TB], int wave, char* lds) {
+  constexpr int G = RB < 2 ? 1 : 2, PITCH = G * 16 + 4;
+  float(*red)[TB * 16][PITCH] = reinterpret_cast<float(*)[TB * 16][PITCH]>(lds);
+  const int lane = threadIdx.x & 63, i16 = lane & 15, h = lane >> 4;
+#pragma unroll
+  for (int g = 0; g < RB; g += G)
+#pragma unroll
+    for (int left = W / 2; left > 0; left >>= 1) {
+      __syncthreads();
+      if (wave >= left && wave < 2 * left)
+#pragma unroll
+        for (int i = 0; i < G; i++)
+#pragma unroll
+          for (int j = 0; j < TB; j++)
+            *reinterpret_cast<f4_t*>(&red[wave - left][j * 16 + i16][i * 16 + h * 4]) =
+                acc[g + i][j];
+      __syncthreads();
+      if (wave < left)
+#pragma unroll
+        for (int i = 0; i < G; i++)
+#pragma unroll
+          for (int j = 0; j < TB; j++)
+            acc[g + i][j] +=
+                *reinterpret_cast<const f4_t*>(&red[wave][j * 16 + i16][i * 16 + h * 4]);
+    }
+}
+// Wave 0's sums of a tile as rows of ranks: out[token][R], `count` tokens, `ranks` ranks.
+template <int RB, int TB>
+__device__ __forceinline__ void store_shares(const f4_t (&acc)[RB][TB], float* out, int R,
+                                             int count, int ranks) {
+  const int lane = threadIdx.x & 63, i16 = lane & 15, h = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < RB; i++)
+#pragma unroll
+    for (int j = 0; j < TB; j++)
+      if (j * 16 + i16 < count && i * 16 + h * 4 < ranks)
+        *reinterpret_cast<f4_t*>(out + (j * 16 + i16) * R + i * 16 + h * 4) = acc[i][j];
+}
+
+// Four ranks' values of one token: the sum of `splits` shares that lie `next` apart.
+__device__ __forceinline__ f4_t add_shares(const float* at, int64_t next, int splits) {
+  f4_t sum = *reinterpret_cast<const f4_t*>(at);
+  int w = 1;
+  for (; w + 3 <= splits; w += 3) {
+    const f4_t s0 = *reinterpret_cast<const f4_t*>(at + w * next);
+    const f4_t s1 = *reinterpret_cast<const f4_t*>(at + (w + 1) * next);
+    const f4_t s2 = *reinterpret_cast<const f4_t*>(at + (w + 2) * next);
+    sum += s0;
+    sum += s1 + s2;
+  }
+  for (; w < splits; w++) sum += *reinterpret_cast<const f4_t*>(at + w * next);
+  return sum;
+}
+
+// A product with scale * value as one operand: its 32 terms are 32 ranks, once against the
+// upper and once against the lower part; or, of 16 ranks, both parts at once.  Lane h's
+// eight ranks of chunk c:
+template <int RB>
+struct Ranks {
+  static constexpr int kChunks = RB < 2 ? 1 : RB / 2;
+  static __device__ __forceinline__ int of(int c, int h) {
+    return RB < 2 ? (h & 1) * 8 : c * 32 + h * 8;
+  }
+};
+// acc[i] += rows[i] times the parts of one token's values, i < M.
+template <bool BF, int RB, int M>
+__device__ __forceinline__ void multiply_parts(const us8_t (&rows)[M][Ranks<RB>::kChunks],
+                                               const uint16_t* parts, int h, f4_t (&acc)[M]) {
+#pragma unroll
+  for (int q = 0; q < (RB < 2 ? 1 : 2); q++)
+#pragma unroll
+    for (int c = 0; c < Ranks<RB>::kChunks; c++) {
+      const us8_t f = *reinterpret_cast<const us8_t*>(parts + q * RB * 16 + c * 32 + h * 8);
+#pragma unroll
+      for (int i = 0; i < M; i++) acc[i] = Half16<BF>::mma(rows[i][c], f, acc[i]);
+    }
+}
+// The parts of a tile of TILE tokens, parts[token][2][RB * 16] (and 8 more), and each
+// token's exponent (fp16; a result is multiplied by 2^-exponent).  `values` gives
+// a token's four ranks from r on, and is called with valid ones only.
+template <bool BF, int RB, int TILE, int THREADS, typename F>
+__device__ __forceinline__ void spread_parts(F values, float scale, int count, int R,
+                                             uint16_t (*parts)[RB * 32 + 8], int* exponent) {
+  constexpr int kPerToken = THREADS / TILE;  // threads of a token
+  constexpr int kQuads = (RB * 4 + kPerToken - 1) / kPerToken;
+  const int t = threadIdx.x / kPerToken, s = threadIdx.x % kPerToken;
+  f4_t val[kQuads];
+  int top = 0;
+#pragma unroll
+  for (int i = 0; i < kQuads; i++) {
+    const int r = (s + i * kPerToken) * 4;
+    val[i] = f4_t{0, 0, 0, 0};
+    if (r < R && t < count) val[i] = values(t, r) * scale;
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      top = max(top, __builtin_bit_cast(int, (float)val[i][j]) & 0x7fffffff);
+  }
+  int e = 0;
+  if (!BF) {
+#pragma unroll
+    for (int off = 1; off < kPerToken; off <<= 1) top = max(top, __shfl_xor(top, off, kWave));
+    e = fp16_exponent(top);
+  }
+  if (s == 0) exponent[t] = e;
+#pragma unroll
+  for (int i = 0; i < kQuads; i++) {
+    const int r = (s + i * kPerToken) * 4;
+    if (r >= RB * 16) continue;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      uint16_t part[2];
+      split_parts<BF>(BF ? val[i][j] : times_power(val[i][j], e), part);
+      parts[t][r + j] = part[0];
+      parts[t][RB * 16 + r + j] = part[1];
+    }
+  }
 }
 
 #endif  // __HIPCC__

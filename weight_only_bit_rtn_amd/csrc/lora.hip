@@ -4,17 +4,16 @@
 // Two kernels.  The first contracts over K: a workgroup takes one tile of tokens of
 // one adapter and a share of K, and leaves v's share in the workspace.  The second
 // adds the shares up, and expands over N: it takes a tile and a range of outputs.
-// Both read the large operands (x and a; b and y) from memory straight into the
-// matrix cores' registers: a lane's operand is eight consecutive elements of a row,
-// which is how rows lie, and an element of x or y is used by one wave only.
 // Bound by HBM: for few tokens the adapters (2 R (K + N) bytes each), for many x, y
 // and out (2 T (K + 2 N) bytes).
 #include "lora.h"
 
+#include <type_traits>
+
 namespace lowbit {
 namespace {
 
-constexpr int kLoraWaves = 4;
+constexpr int kLoraWaves = 4;  // of the expansion
 
 // ---------------------------------------------------------------------------
 // v = a x
@@ -26,78 +25,92 @@ struct DownArgs {
   int k_share;    // a multiple of 64
 };
 
-// TB blocks of 16 tokens, RB of 16 ranks (blockIdx.z: which 64 ranks).  A wave's step
-// is 64 of K: lane h of a row's four takes 16 consecutive elements, so that the four
-// lanes read whole 128-byte lines.
-template <bool BF, int RB, int TB>
-__global__ __launch_bounds__(kLoraWaves * 64) void lora_down_kernel(const DownArgs g) {
-  constexpr int TILE = 16 * TB, PITCH = RB * 16 + 4;
-  __shared__ float red[kLoraWaves / 2][TILE][PITCH];
+// TB blocks of 16 tokens, RB of 16 ranks (blockIdx.z: which 64 ranks), W waves.  A wave's
+// step is 64 of K; the next step's rows are under way while one is multiplied.  No load
+// stands behind a lane's condition, which would make the compiler wait for it at once.
+template <int RB, int TB, int W>
+constexpr int down_bytes() {
+  constexpr int stage = W * (RB + TB) * 16 * 128, reduce = reduce_bytes<RB, TB, W>();
+  return stage > reduce ? stage : reduce;
+}
+template <bool BF, int RB, int TB, int W>
+__global__ __launch_bounds__(W * 64, W == 4 ? 2 : 1) void lora_down_kernel(const DownArgs g) {
+  constexpr int TILE = 16 * TB, RANKS = 16 * RB;
+  extern __shared__ __align__(16) char lds[];
   const LoraArgs& p = g.p;
   LoraTile tile;
   if (!find_tile(p.starts, p.L, (int)p.T, TILE, blockIdx.x, tile) || tile.l == p.L) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int i16 = lane & 15, h = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = wave_of_group();
+  const int row = lane >> 3, chunk = lane & 7;
   const int64_t K = p.K;
-  const int r0 = blockIdx.z * 64, ranks = min(p.R - r0, RB * 16);
-  const uint16_t* ar[RB];
-  const uint16_t* xr[TB];
+  const int r0 = blockIdx.z * 64, ranks = min(p.R - r0, RANKS);
+  uint16_t* const sx = reinterpret_cast<uint16_t*>(lds) + wave * (TILE + RANKS) * 64;
+  uint16_t* const sa = sx + TILE * 64;
+  const uint16_t *xr[TILE / 8], *ar[RANKS / 8];
 #pragma unroll
-  for (int i = 0; i < RB; i++)
-    ar[i] = p.a + ((int64_t)tile.l * p.R + r0 + min(i * 16 + i16, ranks - 1)) * K;
+  for (int q = 0; q < TILE / 8; q++)
+    xr[q] = g.x + token_at(p.order, p.T, tile.begin + min(q * 8 + row, tile.count - 1)) * K + chunk * 8;
 #pragma unroll
-  for (int j = 0; j < TB; j++)
-    xr[j] = g.x + token_at(p.order, p.T, tile.begin + min(j * 16 + i16, tile.count - 1)) * K;
+  for (int q = 0; q < RANKS / 8; q++)
+    ar[q] = p.a + ((int64_t)tile.l * p.R + r0 + min(q * 8 + row, ranks - 1)) * K + chunk * 8;
   f4_t acc[RB][TB];
 #pragma unroll
   for (int i = 0; i < RB; i++)
 #pragma unroll
     for (int j = 0; j < TB; j++) acc[i][j] = f4_t{0, 0, 0, 0};
   const int k0 = blockIdx.y * g.k_share, k1 = min(k0 + g.k_share, p.K);
-  for (int k = k0 + wave * 64; k < k1; k += kLoraWaves * 64) {
+  us8_t vx[TILE / 8], va[RANKS / 8];
+  auto load = [&](int k) {
+#pragma unroll
+    for (int q = 0; q < TILE / 8; q++) vx[q] = *reinterpret_cast<const us8_t*>(xr[q] + k);
+#pragma unroll
+    for (int q = 0; q < RANKS / 8; q++) va[q] = *reinterpret_cast<const us8_t*>(ar[q] + k);
+  };
+  auto stage = [&] {
+    put_rows<TILE>(sx, vx);
+    put_rows<RANKS>(sa, va);
+    wave_lds_order();
+  };
+  auto multiply = [&] {
 #pragma unroll
     for (int half = 0; half < 2; half++) {
-      const int at = k + h * 16 + half * 8;
-      const bool inside = at < k1;
-      us8_t fa[RB], fx[TB];
+      us8_t fa[RB];
 #pragma unroll
-      for (int i = 0; i < RB; i++)
-        fa[i] = inside ? *reinterpret_cast<const us8_t*>(ar[i] + at) : us8_t{};
+      for (int i = 0; i < RB; i++) fa[i] = get_operand(sa, i, half);
 #pragma unroll
-      for (int j = 0; j < TB; j++)
-        fx[j] = inside ? *reinterpret_cast<const us8_t*>(xr[j] + at) : us8_t{};
+      for (int j = 0; j < TB; j++) {
+        const us8_t fx = get_operand(sx, j, half);
 #pragma unroll
-      for (int i = 0; i < RB; i++)
-#pragma unroll
-        for (int j = 0; j < TB; j++) acc[i][j] = Half16<BF>::mma(fa[i], fx[j], acc[i][j]);
+        for (int i = 0; i < RB; i++) acc[i][j] = Half16<BF>::mma(fa[i], fx, acc[i][j]);
+      }
     }
+    wave_lds_order();
+  };
+  int k = k0 + wave * 64;
+  if (k + 64 <= k1) {
+    load(k);
+    for (; k + W * 64 + 64 <= k1; k += W * 64) {
+      stage();
+      load(k + W * 64);
+      multiply();
+    }
+    stage();
+    multiply();
+    k += W * 64;
   }
-  // the waves' sums in two steps, each half of them into the other
+  if (k < k1) {  // K is a multiple of 32: half a step, the other half's chunks are zero
+    load(chunk < 4 ? k : k - 32);
 #pragma unroll
-  for (int left = kLoraWaves / 2; left > 0; left >>= 1) {
-    if (wave >= left && wave < 2 * left)
+    for (int q = 0; q < TILE / 8; q++) vx[q] = chunk < 4 ? vx[q] : us8_t{};
 #pragma unroll
-      for (int i = 0; i < RB; i++)
-#pragma unroll
-        for (int j = 0; j < TB; j++)
-          *reinterpret_cast<f4_t*>(&red[wave - left][j * 16 + i16][i * 16 + h * 4]) = acc[i][j];
-    __syncthreads();
-    if (wave < left)
-#pragma unroll
-      for (int i = 0; i < RB; i++)
-#pragma unroll
-        for (int j = 0; j < TB; j++)
-          acc[i][j] += *reinterpret_cast<const f4_t*>(&red[wave][j * 16 + i16][i * 16 + h * 4]);
-    __syncthreads();
+    for (int q = 0; q < RANKS / 8; q++) va[q] = chunk < 4 ? va[q] : us8_t{};
+    stage();
+    multiply();
   }
-  if (wave > 0) return;
-  float* out = g.shares + ((int64_t)blockIdx.y * p.T + tile.begin) * p.R + r0;
-#pragma unroll
-  for (int i = 0; i < RB; i++)
-#pragma unroll
-    for (int j = 0; j < TB; j++)
-      if (j * 16 + i16 < tile.count && i * 16 + h * 4 < ranks)
-        *reinterpret_cast<f4_t*>(out + (j * 16 + i16) * p.R + i * 16 + h * 4) = acc[i][j];
+  reduce_waves<RB, TB, W>(acc, wave, lds);
+  if (wave == 0)
+    store_shares(acc, g.shares + ((int64_t)blockIdx.y * p.T + tile.begin) * p.R + r0, p.R,
+                 tile.count, ranks);
 }
 
 // ---------------------------------------------------------------------------
@@ -113,124 +126,161 @@ struct UpArgs {
   float* v;
 };
 
-// A product's 32 terms are 16 ranks twice: against the upper and the lower part of
-// s v.  A wave's step is 64 outputs; the rows of b are dealt to the products so that a
-// lane's results are eight consecutive outputs of one token.
+// A wave's step is 64 outputs.  The next step's rows of b and y are under way while one is
+// multiplied.  Results pass through LDS too, in fp32, 16 tokens at a time: eight lanes then
+// hold the 64 outputs of one token as y's rows lie.
+template <int RB>
+constexpr int up_wave_bytes() {
+  constexpr int b = 64 * RB * 32, result = 16 * 68 * 4;
+  return b > result ? b : result;
+}
+template <int RB, int TB>
+constexpr int up_bytes() {
+  return TB * 16 * ((RB * 32 + 8) * 2 + 4) + kLoraWaves * up_wave_bytes<RB>();
+}
 template <bool BF, int RB, int TB>
-__global__ __launch_bounds__(kLoraWaves * 64) void lora_up_kernel(const UpArgs g) {
-  constexpr int TILE = 16 * TB, PITCH = RB * 32 + 8;
-  constexpr int kPerToken = kLoraWaves * 64 / TILE;  // threads of a token
-  constexpr int kQuads = (RB * 4 + kPerToken - 1) / kPerToken;
-  __shared__ uint16_t parts[TILE][PITCH];
-  __shared__ int exponent[TILE];
+__global__ __launch_bounds__(kLoraWaves * 64, RB < 8 ? 2 : 1) void lora_up_kernel(const UpArgs g) {
+  constexpr int TILE = 16 * TB, PITCH = RB * 32 + 8, STEP = kLoraWaves * 64;
+  constexpr int C = Ranks<RB>::kChunks, CHUNKS = RB * 2;
+  extern __shared__ __align__(16) char lds[];
+  uint16_t(*const parts)[PITCH] = reinterpret_cast<uint16_t(*)[PITCH]>(lds);
+  int* const exponent = reinterpret_cast<int*>(lds + TILE * PITCH * 2);
   const LoraArgs& p = g.p;
   LoraTile tile;
   if (!find_tile(p.starts, p.L, (int)p.T, TILE, blockIdx.x, tile)) return;
   const bool none = tile.l == p.L;
   const bool in_place = g.y == g.out;
   if (none && in_place && !g.v) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int i16 = lane & 15, h = lane >> 4;
-  {
-    const int t = threadIdx.x / kPerToken, s = threadIdx.x % kPerToken;
-    const float scale = none ? 0.0f : p.scales[tile.l];
-    f4_t val[kQuads];
-    int top = 0;
+  const int lane = threadIdx.x & 63, wave = wave_of_group();
+  const int i16 = lane & 15, h = lane >> 4, row = lane >> 3, chunk = lane & 7;
+  char* const mine = lds + TILE * (PITCH * 2 + 4) + wave * up_wave_bytes<RB>();
+  uint16_t* const sb = reinterpret_cast<uint16_t*>(mine);             // [64][CHUNKS] chunks
+  float(*const result)[68] = reinterpret_cast<float(*)[68]>(mine);    // [16], after b is read
+  const int64_t N = p.N;
+  int64_t at[TILE / 8];  // of row 8 q + lane / 8, this lane's eight outputs
 #pragma unroll
-    for (int i = 0; i < kQuads; i++) {
-      const int r = (s + i * kPerToken) * 4;
-      val[i] = f4_t{0, 0, 0, 0};
-      if (r >= p.R || t >= tile.count) continue;
+  for (int q = 0; q < TILE / 8; q++)
+    at[q] = token_at(p.order, p.T, tile.begin + min(q * 8 + row, tile.count - 1)) * N + chunk * 8;
+  const int n1 = min((int)(blockIdx.y + 1) * g.n_share, p.N);
+  // b's 64 rows lie in one piece: 16-byte chunk 64 q + lane of it, and where it goes.
+  // Chunk c of row n is in slot c ^ (n / (8 / CHUNKS)) % CHUNKS, as in row_slot().
+  const int per_row = p.R / 8, count = per_row * 64;
+  auto slot = [&](int n, int c) {
+    constexpr int SHIFT = RB == 1 ? 3 : RB == 2 ? 2 : 1;
+    return n * RB * 16 + ((c ^ ((n >> SHIFT) & (CHUNKS - 1))) << 3);
+  };
+  int place[CHUNKS];
+#pragma unroll
+  for (int q = 0; q < CHUNKS; q++) {
+    const int i = q * 64 + lane;
+    place[q] = slot(i / per_row % 64, i % per_row);
+  }
+  us8_t vb[CHUNKS], had[TILE / 8], ahead[TILE / 8];
+  const uint16_t* const b = p.b + (int64_t)(none ? 0 : tile.l) * N * p.R;
+  auto load_b = [&](int n0) {
+#pragma unroll
+    for (int q = 0; q < CHUNKS; q++)
+      if (q < per_row)
+        vb[q] = *reinterpret_cast<const us8_t*>(b + (int64_t)n0 * p.R + (q * 64 + lane) * 8);
+  };
+  // without a y: read what out holds, to no one's use
+  const uint16_t* const y = g.y ? g.y : g.out;
+  auto load_y = [&](us8_t(&to)[TILE / 8], int n0) {
+#pragma unroll
+    for (int q = 0; q < TILE / 8; q++) to[q] = load8(y + at[q] + n0);
+  };
+  us8_t fb[4][C];
+  auto stage_b = [&] {
+#pragma unroll
+    for (int q = 0; q < CHUNKS; q++)
+      if (q < per_row) *reinterpret_cast<us8_t*>(sb + place[q]) = vb[q];
+    wave_lds_order();
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int c = 0; c < C; c++) {
+        const int r = Ranks<RB>::of(c, h);
+        fb[i][c] = *reinterpret_cast<const us8_t*>(sb + slot(i * 16 + i16, r / 8));
+        if (RB * 16 > p.R && r >= p.R) fb[i][c] = us8_t{};
+      }
+    wave_lds_order();
+  };
+  // the 64 outputs of token block j, `left` of this lane's eight inside
+  auto finish = [&](int j, int n0, auto whole, int left) {
+    f4_t acc[4] = {};
+    multiply_parts<BF, RB>(fb, parts[j * 16 + i16], h, acc);
+#pragma unroll
+    for (int i = 0; i < 4; i++) *reinterpret_cast<f4_t*>(&result[i16][i * 16 + h * 4]) = acc[i];
+    wave_lds_order();
+#pragma unroll
+    for (int q = 0; q < 2; q++) {
+      const int t = q * 8 + row;
+      const f4_t lo = *reinterpret_cast<const f4_t*>(&result[t][chunk * 8]);
+      const f4_t hi = *reinterpret_cast<const f4_t*>(&result[t][chunk * 8 + 4]);
+      const int e = BF ? 0 : exponent[j * 16 + t];
+      us8_t o = g.y ? had[j * 2 + q] : us8_t{};
+      // a token without an adapter keeps the bits it has
       if (!none)
-        for (int w = 0; w < g.splits; w++)
-          val[i] += *reinterpret_cast<const f4_t*>(
-              g.shares + ((int64_t)w * p.T + tile.begin + t) * p.R + r);
-      if (g.v && blockIdx.y == 0)
-        *reinterpret_cast<f4_t*>(g.v + token_at(p.order, p.T, tile.begin + t) * p.R + r) = val[i];
-      val[i] *= scale;
 #pragma unroll
-      for (int j = 0; j < 4; j++)
-        top = max(top, __builtin_bit_cast(int, (float)val[i][j]) & 0x7fffffff);
-    }
-    int e = 0;
-    if (!BF) {
-#pragma unroll
-      for (int off = 1; off < kPerToken; off <<= 1) top = max(top, __shfl_xor(top, off, kWave));
-      e = fp16_exponent(top);
-    }
-    if (s == 0) exponent[t] = e;
-#pragma unroll
-    for (int i = 0; i < kQuads; i++) {
-      const int r = (s + i * kPerToken) * 4;
-      if (r >= RB * 16) continue;
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        uint16_t part[2];
-        split_parts<BF>(BF ? val[i][j] : times_power(val[i][j], e), part);
-        const int at = r / 16 * 32 + r % 16 + j;
-        parts[t][at] = part[0];
-        parts[t][at + 16] = part[1];
+        for (int m = 0; m < 8; m++) {
+          float f = m < 4 ? lo[m % 4] : hi[m % 4];
+          if (!BF) f = times_power(f, -e);
+          if (g.y) f += Half16<BF>::to(o[m]);
+          o[m] = Half16<BF>::from(f);
+        }
+      if (j * 16 + t < tile.count) {
+        if (whole)
+          store8(g.out + at[j * 2 + q] + n0, o);
+        else
+          store8(g.out + at[j * 2 + q] + n0, o, left);
       }
     }
+    wave_lds_order();
+  };
+  int n0 = blockIdx.y * g.n_share + wave * 64;
+  // the first step's loads are under way while v's shares are added up
+  if (n0 + 64 <= n1) {
+    load_y(had, n0);
+    load_b(n0);
   }
+  spread_parts<BF, RB, TILE, kLoraWaves * 64>(
+      [&](int t, int r) {
+        f4_t val = {0, 0, 0, 0};
+        if (!none)
+          val = add_shares(g.shares + ((int64_t)tile.begin + t) * p.R + r, p.T * p.R, g.splits);
+        if (g.v && blockIdx.y == 0)
+          *reinterpret_cast<f4_t*>(g.v + token_at(p.order, p.T, tile.begin + t) * p.R + r) = val;
+        return val;
+      },
+      none ? 0.0f : p.scales[tile.l], tile.count, p.R, parts, exponent);
   __syncthreads();
   if (none && in_place) return;
-  const int64_t N = p.N;
-  const int blocks = (tile.count + 15) / 16;
-  int64_t row[TB];
-  int e[TB];
-#pragma unroll
-  for (int j = 0; j < TB; j++) {
-    const int t = j * 16 + i16;
-    row[j] = token_at(p.order, p.T, tile.begin + min(t, tile.count - 1)) * N;
-    e[j] = exponent[t];
-  }
-  const int n1 = min((int)(blockIdx.y + 1) * g.n_share, p.N);
-  for (int n0 = blockIdx.y * g.n_share + wave * 64; n0 < n1; n0 += kLoraWaves * 64) {
-    us8_t fb[4][RB];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      // pair i / 2 covers 32 outputs: row m of its product i % 2 is output 8 (m / 4) + 4 (i % 2) + m % 4
-      const int n = n0 + i / 2 * 32 + i16 / 4 * 8 + i % 2 * 4 + i16 % 4;
-      const uint16_t* br = p.b + ((int64_t)(none ? 0 : tile.l) * N + min(n, p.N - 1)) * p.R;
-#pragma unroll
-      for (int c = 0; c < RB; c++) {
-        const int r = c * 16 + (h & 1) * 8;
-        fb[i][c] = r < p.R && !none ? *reinterpret_cast<const us8_t*>(br + r) : us8_t{};
-      }
+  for (; n0 + 64 <= n1; n0 += STEP) {
+    stage_b();
+    if (n0 + STEP + 64 <= n1) {
+      load_y(ahead, n0 + STEP);
+      load_b(n0 + STEP);
     }
 #pragma unroll
     for (int j = 0; j < TB; j++) {
-      if (j >= blocks) break;
-      us8_t fv[RB];
-#pragma unroll
-      for (int c = 0; c < RB; c++)
-        fv[c] = *reinterpret_cast<const us8_t*>(&parts[j * 16 + i16][c * 32 + h * 8]);
-#pragma unroll
-      for (int pair = 0; pair < 2; pair++) {
-        f4_t acc[2] = {f4_t{0, 0, 0, 0}, f4_t{0, 0, 0, 0}};
-#pragma unroll
-        for (int i = 0; i < 2; i++)
-#pragma unroll
-          for (int c = 0; c < RB; c++)
-            acc[i] = Half16<BF>::mma(fb[pair * 2 + i][c], fv[c], acc[i]);
-        const int n = n0 + pair * 32 + h * 8;
-        if (j * 16 + i16 >= tile.count || n >= n1) continue;
-        const int left = p.N - n;
-        us8_t had = {};
-        if (g.y) had = load8(g.y + row[j] + n, left);
-        us8_t o;
-#pragma unroll
-        for (int q = 0; q < 8; q++) {
-          float f = acc[q / 4][q % 4];
-          if (!BF) f = times_power(f, -e[j]);
-          if (g.y) f += Half16<BF>::to(had[q]);
-          o[q] = Half16<BF>::from(f);
-        }
-        // a token without an adapter keeps the bits it has
-        store8(g.out + row[j] + n, none ? had : o, left);
-      }
+      if (j * 16 >= tile.count) break;
+      finish(j, n0, std::true_type(), 8);
     }
+#pragma unroll
+    for (int q = 0; q < TILE / 8; q++) had[q] = ahead[q];
+  }
+  if (n0 < n1) {  // the last outputs, fewer than 64
+    const int left = n1 - n0 - chunk * 8, most = (n1 - n0) * per_row - 1;
+#pragma unroll
+    for (int q = 0; q < CHUNKS; q++)  // beyond the last row: for outputs that nobody stores
+      if (q < per_row)
+        vb[q] = *reinterpret_cast<const us8_t*>(b + (int64_t)n0 * p.R + min(q * 64 + lane, most) * 8);
+#pragma unroll
+    for (int q = 0; q < TILE / 8; q++) had[q] = load8(y + at[q] + n0, left);
+    stage_b();
+#pragma unroll
+    for (int j = 0; j < TB; j++)
+      if (j * 16 < tile.count) finish(j, n0, std::false_type(), left);
   }
 }
 
@@ -245,28 +295,30 @@ Division divide(const LoraSizes& s) {
   Division d;
   d.tile = s.T <= 256 ? 16 : 64;
   d.tiles = lora_tiles(s.T, s.L, d.tile);
-  auto shares = [&](int64_t length, int64_t wanted, int& count, int& share) {
-    const int64_t most = (length + 255) / 256;
+  auto shares = [&](int64_t length, int64_t step, int64_t wanted, int& count, int& share) {
+    const int64_t most = (length + step - 1) / step;
     int64_t n = (wanted + d.tiles - 1) / d.tiles;
     if (n > most) n = most;
     share = (int)(((length + n - 1) / n + 63) / 64 * 64);
     count = (int)((length + share - 1) / share);
   };
-  shares(s.K, 512, d.splits, d.k_share);
-  shares(s.N, 1024, d.ranges, d.n_share);
+  if (d.tile == 16)
+    shares(s.K, 512, 256, d.splits, d.k_share);
+  else
+    shares(s.K, 256, 512, d.splits, d.k_share);
+  shares(s.N, 256, 1024, d.ranges, d.n_share);
   return d;
 }
 
 template <bool BF, int RB, int TB>
 hipError_t run(const DownArgs& down, const UpArgs& up, const Division& d, hipStream_t stream) {
-  constexpr int DOWN = RB < 4 ? RB : 4;
-  lora_down_kernel<BF, DOWN, TB><<<dim3((unsigned)d.tiles, d.splits, (down.p.R + 63) / 64),
-                                   kLoraWaves * 64, 0, stream>>>(down);
-  const hipError_t e = hipGetLastError();
+  constexpr int DOWN = RB < 4 ? RB : 4, W = TB == 1 && RB <= 2 ? 8 : 4;
+  const hipError_t e = launch_lds(lora_down_kernel<BF, DOWN, TB, W>,
+                                  dim3((unsigned)d.tiles, d.splits, (down.p.R + 63) / 64), W * 64,
+                                  down_bytes<DOWN, TB, W>(), stream, down);
   if (e != hipSuccess) return e;
-  lora_up_kernel<BF, RB, TB>
-      <<<dim3((unsigned)d.tiles, d.ranges), kLoraWaves * 64, 0, stream>>>(up);
-  return hipGetLastError();
+  return launch_lds(lora_up_kernel<BF, RB, TB>, dim3((unsigned)d.tiles, d.ranges), kLoraWaves * 64,
+                    up_bytes<RB, TB>(), stream, up);
 }
 template <bool BF, int RB>
 hipError_t run(const DownArgs& down, const UpArgs& up, const Division& d, hipStream_t stream) {

@@ -3,7 +3,7 @@
 //   u_t = b_l^T dy_t,  dx_t = base_t + s_l a_l^T u_t,
 //   da_l = s_l sum_t u_t x_t^T,  db_l = s_l sum_t dy_t v_t^T.
 //
-// Three launches: u; then dx, da and db side by side; then the join of da's and db's
+// Three launches: u; then da and db; then dx, and beside it the join of da's and db's
 // shares where an adapter has more than one chunk of tokens.  Bound by HBM: dy is read
 // twice, x and base once, dx is written, 2 T (2 N + 3 K) bytes.
 //
@@ -23,99 +23,133 @@ constexpr int kCols = kGradWaves * 128;  // columns of a workgroup of dx, da or 
 // ---------------------------------------------------------------------------
 // u = b^T dy
 // ---------------------------------------------------------------------------
+constexpr int kBackWaves = 4;
+constexpr int kMostSplits = 4;  // shares of u: the sums hold them in registers
+
 struct BackArgs {
   LoraArgs p;
   const uint16_t* dy;
   float* shares;  // [splits][T][R], rows in the plan's order
-  int n_share;    // a multiple of 256
+  int n_share;    // a multiple of 64
 };
 
-// A wave's step is 64 outputs: it turns b's 64 rows of RB * 16 ranks around in LDS
-// (rows of b hold the ranks of one output, an operand needs eight outputs of one rank).
+// A wave's step is 64 outputs: 64 tokens' rows of dy, and b's 64 rows of RB * 16 ranks, which
+// lie in one piece and are turned around on their way into LDS (rows of b hold the ranks of
+// one output, an operand needs eight outputs of one rank): a lane takes eight ranks of two
+// outputs and writes pairs.  The next step's are under way while one is multiplied.
+template <int RB>
+constexpr int back_bytes() {
+  constexpr int TB = kTile / 16;
+  constexpr int stage = kBackWaves * (kTile * 128 + RB * 16 * 144);
+  constexpr int reduce = reduce_bytes<RB, TB, kBackWaves>();
+  return stage > reduce ? stage : reduce;
+}
 template <bool BF, int RB>
-__global__ __launch_bounds__(kGradWaves * 64) void lora_back_kernel(const BackArgs g) {
-  constexpr int TB = kTile / 16, PITCH = RB * 16 + 4, TURN = 64 + 8;
-  constexpr int kTurned = kGradWaves * RB * 16 * TURN * 2;
-  constexpr int kReduced = kGradWaves / 2 * kTile * PITCH * 4;
-  __shared__ __align__(16) char lds[kTurned > kReduced ? kTurned : kReduced];
+__global__ __launch_bounds__(kBackWaves * 64, 2) void lora_back_kernel(const BackArgs g) {
+  constexpr int TB = kTile / 16, TURN = 64 + 8, RANKS = RB * 16;
+  extern __shared__ __align__(16) char lds[];
   const LoraArgs& p = g.p;
   LoraTile tile;
   if (!find_tile(p.starts, p.L, (int)p.T, kTile, blockIdx.x, tile) || tile.l == p.L) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int i16 = lane & 15, h = lane >> 4;
-  const int r0 = blockIdx.z * 64, ranks = min(p.R - r0, RB * 16);
-  uint16_t(*turn)[TURN] = reinterpret_cast<uint16_t(*)[TURN]>(lds + wave * RB * 16 * TURN * 2);
-  const int blocks = (tile.count + 15) / 16;
-  const uint16_t* dr[TB];
+  const int lane = threadIdx.x & 63, wave = wave_of_group();
+  const int i16 = lane & 15, h = lane >> 4, row = lane >> 3, chunk = lane & 7;
+  const int r0 = blockIdx.z * 64, ranks = min(p.R - r0, RANKS);
+  uint16_t* const sd = reinterpret_cast<uint16_t*>(lds + wave * (kTile * 128 + RANKS * 144));
+  uint16_t(*const turn)[TURN] = reinterpret_cast<uint16_t(*)[TURN]>(sd + kTile * 64);
+  const uint16_t* dr[kTile / 8];
 #pragma unroll
-  for (int j = 0; j < TB; j++)
-    dr[j] = g.dy +
-            token_at(p.order, p.T, tile.begin + min(j * 16 + i16, tile.count - 1)) * p.N;
+  for (int q = 0; q < kTile / 8; q++)
+    dr[q] = g.dy + chunk * 8 +
+            token_at(p.order, p.T, tile.begin + min(q * 8 + row, tile.count - 1)) * p.N;
+  // item 64 q + lane of a step: eight ranks from 8 (item % RB2) on, outputs 2 (item / RB2) and
+  // the next.  The slots of a row's 16-byte chunks are dealt by its eight ranks, so that the
+  // lanes' writes take different banks.
+  constexpr int RB2 = RB * 2, ITEMS = 32 * RB2 / 64;
+  const uint16_t* br[ITEMS];
+  int place[ITEMS];
+#pragma unroll
+  for (int q = 0; q < ITEMS; q++) {
+    const int item = q * 64 + lane, oct = item % RB2, pair = item / RB2;
+    // beyond the last rank: read within the row, and turned into rows of no one's results
+    br[q] = p.b + ((int64_t)tile.l * p.N + pair * 2) * p.R + r0 + min(oct * 8, ranks - 8);
+    place[q] = oct * 8 * TURN + ((((pair >> 2) ^ oct) & 7) << 3) + (pair & 3) * 2;
+  }
   f4_t acc[RB][TB];
 #pragma unroll
   for (int i = 0; i < RB; i++)
 #pragma unroll
     for (int j = 0; j < TB; j++) acc[i][j] = f4_t{0, 0, 0, 0};
-  const int n1 = min((int)(blockIdx.y + 1) * g.n_share, p.N);
-  for (int base = blockIdx.y * g.n_share; base < n1; base += kGradWaves * 64) {
-    const int n0 = base + wave * 64;
-    // two outputs' eight ranks to a lane, written as pairs
-    const int pair = lane & 31;
-    const uint16_t* br = p.b + ((int64_t)tile.l * p.N + n0 + pair * 2) * p.R + r0;
+  us8_t vd[kTile / 8], vb[ITEMS][2];
+  auto load = [&](int n) {
 #pragma unroll
-    for (int q = 0; q < RB; q++) {
-      const int r = (q * 2 + (lane >> 5)) * 8;
-      us8_t lo = {}, hi = {};
-      if (r < ranks && n0 + pair * 2 < n1) lo = *reinterpret_cast<const us8_t*>(br + r);
-      if (r < ranks && n0 + pair * 2 + 1 < n1) hi = *reinterpret_cast<const us8_t*>(br + p.R + r);
+    for (int q = 0; q < kTile / 8; q++) vd[q] = load8(dr[q] + n);
+#pragma unroll
+    for (int q = 0; q < ITEMS; q++) {
+      vb[q][0] = *reinterpret_cast<const us8_t*>(br[q] + (int64_t)n * p.R);
+      vb[q][1] = *reinterpret_cast<const us8_t*>(br[q] + (int64_t)n * p.R + p.R);
+    }
+  };
+  auto stage = [&] {
+    put_rows<kTile>(sd, vd);
+#pragma unroll
+    for (int q = 0; q < ITEMS; q++)
 #pragma unroll
       for (int i = 0; i < 8; i++)
-        *reinterpret_cast<uint32_t*>(&turn[r + i][pair * 2]) = lo[i] | (uint32_t)hi[i] << 16;
-    }
-    __syncthreads();
+        *reinterpret_cast<uint32_t*>(&turn[0][0] + place[q] + i * TURN) =
+            vb[q][0][i] | (uint32_t)vb[q][1][i] << 16;
+    wave_lds_order();
+  };
+  auto multiply = [&] {
 #pragma unroll
     for (int half = 0; half < 2; half++) {
-      const int at = half * 32 + h * 8;
       us8_t fb[RB];
 #pragma unroll
       for (int i = 0; i < RB; i++)
-        fb[i] = *reinterpret_cast<const us8_t*>(&turn[i * 16 + i16][at]);
+        fb[i] = *reinterpret_cast<const us8_t*>(
+            &turn[i * 16 + i16][((half * 4 + h) ^ ((i * 2 + (i16 >> 3)) & 7)) << 3]);
 #pragma unroll
       for (int j = 0; j < TB; j++) {
-        if (j >= blocks) break;
-        const us8_t fd = load8(dr[j] + n0 + at, n1 - n0 - at);
+        const us8_t fd = get_operand(sd, j, half);
 #pragma unroll
         for (int i = 0; i < RB; i++) acc[i][j] = Half16<BF>::mma(fb[i], fd, acc[i][j]);
       }
     }
-    __syncthreads();
+    wave_lds_order();
+  };
+  const int n0 = blockIdx.y * g.n_share, n1 = min(n0 + g.n_share, p.N);
+  constexpr int STEP = kBackWaves * 64;
+  int n = n0 + wave * 64;
+  if (n + 64 <= n1) {
+    load(n);
+    for (; n + STEP + 64 <= n1; n += STEP) {
+      stage();
+      load(n + STEP);
+      multiply();
+    }
+    stage();
+    multiply();
+    n += STEP;
   }
-  float(*red)[kTile][PITCH] = reinterpret_cast<float(*)[kTile][PITCH]>(lds);
+  if (n < n1) {  // the last outputs, fewer than 64
+    const int left = n1 - n;
 #pragma unroll
-  for (int left = kGradWaves / 2; left > 0; left >>= 1) {
-    if (wave >= left && wave < 2 * left)
+    for (int q = 0; q < kTile / 8; q++) vd[q] = load8(dr[q] + n, left - chunk * 8);
 #pragma unroll
-      for (int i = 0; i < RB; i++)
+    for (int q = 0; q < ITEMS; q++) {
+      const int pair = (q * 64 + lane) / RB2;
 #pragma unroll
-        for (int j = 0; j < TB; j++)
-          *reinterpret_cast<f4_t*>(&red[wave - left][j * 16 + i16][i * 16 + h * 4]) = acc[i][j];
-    __syncthreads();
-    if (wave < left)
-#pragma unroll
-      for (int i = 0; i < RB; i++)
-#pragma unroll
-        for (int j = 0; j < TB; j++)
-          acc[i][j] += *reinterpret_cast<const f4_t*>(&red[wave][j * 16 + i16][i * 16 + h * 4]);
-    __syncthreads();
+      for (int i = 0; i < 2; i++)
+        vb[q][i] = pair * 2 + i < left
+                       ? *reinterpret_cast<const us8_t*>(br[q] + ((int64_t)n + i) * p.R)
+                       : us8_t{};
+    }
+    stage();
+    multiply();
   }
-  if (wave > 0) return;
-  float* out = g.shares + ((int64_t)blockIdx.y * p.T + tile.begin) * p.R + r0;
-#pragma unroll
-  for (int i = 0; i < RB; i++)
-#pragma unroll
-    for (int j = 0; j < TB; j++)
-      if (j * 16 + i16 < tile.count && i * 16 + h * 4 < ranks)
-        *reinterpret_cast<f4_t*>(out + (j * 16 + i16) * p.R + i * 16 + h * 4) = acc[i][j];
+  reduce_waves<RB, TB, kBackWaves>(acc, wave, lds);
+  if (wave == 0)
+    store_shares(acc, g.shares + ((int64_t)blockIdx.y * p.T + tile.begin) * p.R + r0, p.R,
+                 tile.count, ranks);
 }
 
 // ---------------------------------------------------------------------------
@@ -151,113 +185,105 @@ __device__ __forceinline__ void transpose8(const us8_t (&rows)[8], us8_t (&cols)
   for (int j = 0; j < 8; j++) cols[j] = __builtin_bit_cast(us8_t, out[j]);
 }
 
-// dx of one tile and 512 columns, 128 to a wave.  As in the forward pass a product's
-// 32 terms are 16 ranks against the upper and lower part of s u.
+// dx of one tile and 512 columns, 128 to a wave, with s u in two parts as s v in the
+// forward pass.  Results pass through LDS as there: sixteen lanes then hold the 128
+// columns of one token.
+template <int RB>
+constexpr int dx_bytes() {
+  return kTile * ((RB * 32 + 8) * 2 + 4) + kGradWaves * 16 * 132 * 4;
+}
 template <bool BF, int RB>
 __device__ __forceinline__ void dx_part(const SpreadArgs& g, int index, int col, char* lds) {
-  constexpr int PITCH = RB * 32 + 8, TB = kTile / 16;
-  constexpr int kPerToken = kGradWaves * 64 / kTile;
-  uint16_t(*parts)[PITCH] = reinterpret_cast<uint16_t(*)[PITCH]>(lds);
-  int* exponent = reinterpret_cast<int*>(lds + kTile * PITCH * 2);
+  constexpr int PITCH = RB * 32 + 8, TB = kTile / 16, C = Ranks<RB>::kChunks;
+  uint16_t(*const parts)[PITCH] = reinterpret_cast<uint16_t(*)[PITCH]>(lds);
+  int* const exponent = reinterpret_cast<int*>(lds + kTile * PITCH * 2);
   const LoraArgs& p = g.p;
   LoraTile tile;
   if (!find_tile(p.starts, p.L, (int)p.T, kTile, index, tile)) return;
   const bool none = tile.l == p.L;
   if (none && g.base == g.dx) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = wave_of_group();
   const int i16 = lane & 15, h = lane >> 4;
-  {
-    const int t = threadIdx.x / kPerToken, s = threadIdx.x % kPerToken;
-    const float scale = none ? 0.0f : p.scales[tile.l];
-    f4_t val[RB];
-    int top = 0;
-#pragma unroll
-    for (int i = 0; i < RB; i++) {
-      const int r = (s + i * kPerToken) * 4;
-      val[i] = f4_t{0, 0, 0, 0};
-      if (r >= p.R || t >= tile.count || none) continue;
-      for (int w = 0; w < g.splits; w++)
-        val[i] += *reinterpret_cast<const f4_t*>(
-            g.shares + ((int64_t)w * p.T + tile.begin + t) * p.R + r);
-      val[i] *= scale;
-#pragma unroll
-      for (int j = 0; j < 4; j++)
-        top = max(top, __builtin_bit_cast(int, (float)val[i][j]) & 0x7fffffff);
-    }
-    int e = 0;
-    if (!BF) {
-#pragma unroll
-      for (int off = 1; off < kPerToken; off <<= 1) top = max(top, __shfl_xor(top, off, kWave));
-      e = fp16_exponent(top);
-    }
-    if (s == 0) exponent[t] = e;
-#pragma unroll
-    for (int i = 0; i < RB; i++) {
-      const int r = (s + i * kPerToken) * 4;
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        uint16_t part[2];
-        split_parts<BF>(BF ? val[i][j] : times_power(val[i][j], e), part);
-        const int at = r / 16 * 32 + r % 16 + j;
-        parts[t][at] = part[0];
-        parts[t][at + 16] = part[1];
-      }
-    }
-  }
-  __syncthreads();
+  float(*const result)[132] =
+      reinterpret_cast<float(*)[132]>(lds + kTile * (PITCH * 2 + 4) + wave * 16 * 132 * 4);
   const int64_t K = p.K;
   const int k0 = col * kCols + wave * 128;
-  if (k0 >= p.K) return;
-  // lane i16 = 4 a + b loads columns 8 (4 b + a) on: its results are then pieces of eight
-  // columns that lie side by side for the four lanes of a token
-  const int mine = k0 + (i16 % 4 * 4 + i16 / 4) * 8;
-  us8_t fa[RB][8];
+  const int mine = min(k0 + i16 * 8, p.K - 8);  // beyond the last column: for no one's results
+  const bool inside = k0 + i16 * 8 < p.K;
+  int64_t at[TB][4];  // of token 16 j + 4 q + h, this lane's eight columns
 #pragma unroll
-  for (int c = 0; c < RB; c++) {
-    us8_t rows[8];
-    const int r = c * 16 + (h & 1) * 8;
+  for (int j = 0; j < TB; j++)
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      rows[i] = us8_t{};
-      if (!none && r < p.R && mine < p.K)
-        rows[i] = *reinterpret_cast<const us8_t*>(p.a + ((int64_t)tile.l * p.R + r + i) * K + mine);
-    }
-    transpose8(rows, fa[c]);
+    for (int q = 0; q < 4; q++)
+      at[j][q] = token_at(p.order, p.T, tile.begin + min(j * 16 + q * 4 + h, tile.count - 1)) * K + mine;
+  // without a base: read what dx holds, to no one's use
+  const uint16_t* const base = g.base ? g.base : g.dx;
+  us8_t had[2][4];
+  auto load_base = [&](us8_t(&to)[4], int j) {
+#pragma unroll
+    for (int q = 0; q < 4; q++)
+      to[q] = *reinterpret_cast<const us8_t*>(base + at[j][q]);
+  };
+  load_base(had[0], 0);
+  us8_t fa[8][C];  // rows of a first, then turned around
+#pragma unroll
+  for (int c = 0; c < C; c++) {
+    // beyond the last rank: read within the pool, cleared before the product
+    const uint16_t* from =
+        p.a + ((int64_t)(none ? 0 : tile.l) * p.R + min(Ranks<RB>::of(c, h), p.R - 8)) * K + mine;
+#pragma unroll
+    for (int i = 0; i < 8; i++) fa[i][c] = *reinterpret_cast<const us8_t*>(from + i * K);
   }
+  spread_parts<BF, RB, kTile, kGradWaves * 64>(
+      [&](int t, int r) {
+        return none ? f4_t{0, 0, 0, 0}
+                    : add_shares(g.shares + ((int64_t)tile.begin + t) * p.R + r, p.T * p.R, g.splits);
+      },
+      none ? 0.0f : p.scales[tile.l], tile.count, p.R, parts, exponent);
+  __syncthreads();
+  if (k0 >= p.K) return;
+#pragma unroll
+  for (int c = 0; c < C; c++) {
+    us8_t rows[8], turned[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) rows[i] = fa[i][c];
+    transpose8(rows, turned);
+    const bool none_such = Ranks<RB>::of(c, h) >= p.R;
+#pragma unroll
+    for (int i = 0; i < 8; i++) fa[i][c] = none_such ? us8_t{} : turned[i];
+  }
+#pragma unroll
   for (int j = 0; j < TB; j++) {
-    const int t = j * 16 + i16;
     if (j * 16 >= tile.count) break;
-    us8_t fu[RB];
-#pragma unroll
-    for (int c = 0; c < RB; c++)
-      fu[c] = *reinterpret_cast<const us8_t*>(&parts[t][c * 32 + h * 8]);
-    f4_t acc[8];
-#pragma unroll
-    for (int m = 0; m < 8; m++) {
-      acc[m] = f4_t{0, 0, 0, 0};
-#pragma unroll
-      for (int c = 0; c < RB; c++) acc[m] = Half16<BF>::mma(fa[c][m], fu[c], acc[m]);
-    }
-    if (t >= tile.count) continue;
-    const int64_t row = token_at(p.order, p.T, tile.begin + t) * K;
-    const int e = exponent[t];
+    if (j + 1 < TB) load_base(had[(j + 1) % 2], j + 1);
+    f4_t acc[8] = {};
+    multiply_parts<BF, RB>(fa, parts[j * 16 + i16], h, acc);
+    // row 4 h + i of product m is column 8 (4 h + i) + m
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      // result row 4 h + i is lane 4 h + i's columns
-      const int k = k0 + (i * 4 + h) * 8;
-      if (k >= p.K) continue;
-      us8_t had = {};
-      if (g.base) had = *reinterpret_cast<const us8_t*>(g.base + row + k);
-      us8_t o;
-#pragma unroll
-      for (int m = 0; m < 8; m++) {
-        float f = acc[m][i];
-        if (!BF) f = times_power(f, -e);
-        if (g.base) f += Half16<BF>::to(had[m]);
-        o[m] = Half16<BF>::from(f);
-      }
-      *reinterpret_cast<us8_t*>(g.dx + row + k) = none ? had : o;
+      float* const to = &result[i16][(h * 4 + i) * 8];
+      *reinterpret_cast<f4_t*>(to) = f4_t{acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
+      *reinterpret_cast<f4_t*>(to + 4) = f4_t{acc[4][i], acc[5][i], acc[6][i], acc[7][i]};
     }
+    wave_lds_order();
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+      const int t = q * 4 + h;
+      const f4_t lo = *reinterpret_cast<const f4_t*>(&result[t][i16 * 8]);
+      const f4_t hi = *reinterpret_cast<const f4_t*>(&result[t][i16 * 8 + 4]);
+      const int e = BF ? 0 : exponent[j * 16 + t];
+      us8_t o = g.base ? had[j % 2][q] : us8_t{};
+      if (!none)
+#pragma unroll
+        for (int m = 0; m < 8; m++) {
+          float f = m < 4 ? lo[m % 4] : hi[m % 4];
+          if (!BF) f = times_power(f, -e);
+          if (g.base) f += Half16<BF>::to(o[m]);
+          o[m] = Half16<BF>::from(f);
+        }
+      if (inside && j * 16 + t < tile.count) *reinterpret_cast<us8_t*>(g.dx + at[j][q]) = o;
+    }
+    wave_lds_order();
   }
 }
 
@@ -268,71 +294,117 @@ __device__ __forceinline__ int64_t share_of(int first, int chunk) { return 2 * (
 
 // da (ROWS_X: sums of u_t x_t) or db (v_t dy_t) of one chunk of tokens, 64 ranks from
 // r0 on and 512 columns, 128 to a wave.  64 tokens at a time pass through LDS as parts
-// of u or v, turned around so that an operand's eight tokens lie side by side; their
-// rows of x or dy go straight to the registers.  fp16: the parts stand for values times
-// 2^e, e by the largest value so far; the sums follow when it changes.
+// of u or v, turned around so that an operand's eight tokens lie side by side, in two
+// buffers; their rows of x or dy go straight to the registers, where the next 64 tokens'
+// are under way while these are multiplied.  fp16: the parts stand for values times 2^e, e
+// by the largest value so far; the sums follow when it changes.
 template <bool BF, int RB, bool ROWS_X>
 __device__ __forceinline__ void sum_part(const SpreadArgs& g, int index, int col, int r0,
                                          char* lds) {
-  constexpr int PARTS = BF ? 3 : 2, TURN = kTile + 8;
+  constexpr int PARTS = BF ? 3 : 2, TURN = kTile + 8, HALVES = kTile / 32;
   constexpr int kPerToken = kGradWaves * 64 / kTile;
-  typedef uint16_t Turned[RB * 16][TURN];
-  Turned* const turned = reinterpret_cast<Turned*>(lds);
-  int* const places = reinterpret_cast<int*>(lds + PARTS * sizeof(Turned));  // tokens
-  int* const tops = places + kTile;
+  typedef uint16_t Turned[PARTS][RB * 16][TURN];
+  Turned* const turned = reinterpret_cast<Turned*>(lds);                       // [2]
+  int(*const places)[kTile] = reinterpret_cast<int(*)[kTile]>(lds + 2 * sizeof(Turned));  // [2]
+  int(*const tops)[kGradWaves] = reinterpret_cast<int(*)[kGradWaves]>(places + 2);     // [2]
   const LoraArgs& p = g.p;
   LoraTile tile;
   if (!find_tile(p.starts, p.L, (int)p.T, g.chunk, index, tile) || tile.l == p.L) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = wave_of_group();
   const int i16 = lane & 15, h = lane >> 4;
   const int64_t C = ROWS_X ? p.K : p.N;
   const uint16_t* const rows_of = ROWS_X ? g.x : g.dy;
   const int ranks = min(p.R - r0, RB * 16);
-  const int c0 = col * kCols + wave * 128 + i16 * 8;  // this lane's eight columns
+  const int w0 = col * kCols + wave * 128;  // the wave's columns
+  // this lane's eight; beyond the last column the last eight again, which somebody else
+  // stores, and where C is no multiple of eight an overlap with the lane before
+  const int wanted = w0 + i16 * 8, c0 = (int)min((int64_t)wanted, C - 8);
+  const bool active = w0 < C;
+  const int t = threadIdx.x / kPerToken, s = threadIdx.x % kPerToken;
   f4_t acc[RB][8];
 #pragma unroll
   for (int i = 0; i < RB; i++)
 #pragma unroll
     for (int m = 0; m < 8; m++) acc[i][m] = f4_t{0, 0, 0, 0};
-  int e = 0;
-  bool any = false;  // whether e was chosen
-  for (int t0 = 0; t0 < tile.count; t0 += kTile) {
-    const int t = threadIdx.x / kPerToken, s = threadIdx.x % kPerToken;
-    const bool has = t0 + t < tile.count;
-    const int64_t token = has ? token_at(p.order, p.T, tile.begin + t0 + t) : 0;
-    f4_t val[RB];
-    int top = 0;
+  // this thread's token and its values of u or v among the 64 from t0 on
+  auto token_of = [&](int t0) {
+    return (int)token_at(p.order, p.T, tile.begin + min(t0 + t, tile.count - 1));
+  };
+  f4_t val[RB][ROWS_X ? kMostSplits : 1];
+  auto load_values = [&](int t0, int token) {
+    // beyond the last token or rank: read within the buffer, cleared when they are used
+    const int64_t at = ROWS_X ? tile.begin + min(t0 + t, tile.count - 1) : token;
 #pragma unroll
     for (int i = 0; i < RB; i++) {
-      const int r = (s + i * kPerToken) * 4;
-      val[i] = f4_t{0, 0, 0, 0};
-      if (!has || r >= ranks) continue;
+      const int r = r0 + min((s + i * kPerToken) * 4, ranks - 4);
       if (ROWS_X) {
-        for (int w = 0; w < g.splits; w++)
-          val[i] += *reinterpret_cast<const f4_t*>(
-              g.shares + ((int64_t)w * p.T + tile.begin + t0 + t) * p.R + r0 + r);
-      } else {
-        val[i] = *reinterpret_cast<const f4_t*>(g.v + token * p.R + r0 + r);
-      }
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const int bits = __builtin_bit_cast(int, (float)val[i][j]) & 0x7fffffff;
-        if (bits < 0x7f800000) top = max(top, bits);
+        for (int w = 0; w < kMostSplits; w++)
+          if (w < g.splits)
+            val[i][w] = *reinterpret_cast<const f4_t*>(g.shares + (w * p.T + at) * p.R + r);
+      } else {
+        val[i][0] = *reinterpret_cast<const f4_t*>(g.v + at * p.R + r);
       }
     }
+  };
+  f4_t sum[RB];
+  auto add_values = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < RB; i++) {
+      sum[i] = val[i][0];
+      if (ROWS_X)
+#pragma unroll
+        for (int w = 1; w < kMostSplits; w++)
+          if (w < g.splits) sum[i] += val[i][w];
+      if (t0 + t >= tile.count || (s + i * kPerToken) * 4 >= ranks) sum[i] = f4_t{0, 0, 0, 0};
+    }
+  };
+  us8_t rows[HALVES][8];
+  // One path for all loads: where two meet, the compiler waits for either's.  A place beyond
+  // the last token holds the last one's row, cleared before the product.
+  auto load_rows = [&](int half, const int (&place)[kTile]) {
+    int tok[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) tok[i] = place[half * 32 + h * 8 + i];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const uint16_t* from = rows_of + tok[i] * C + c0;
+      rows[half][i] = ROWS_X ? *reinterpret_cast<const us8_t*>(from) : load8(from);
+    }
+  };
+  int e = 0;
+  bool any = false;  // whether e was chosen
+  int token = token_of(0), next = token_of(kTile);
+  load_values(0, token);
+  if (s == 0) places[0][t] = token;
+  __syncthreads();
+#pragma unroll
+  for (int half = 0; half < HALVES; half++) {
+    load_rows(half, places[0]);
+    loads_stay();
+  }
+  for (int t0 = 0, b = 0; t0 < tile.count; t0 += kTile, b ^= 1) {
+    add_values(t0);
     if (!BF) {
+      int top = 0;
+#pragma unroll
+      for (int i = 0; i < RB; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const int bits = __builtin_bit_cast(int, (float)sum[i][j]) & 0x7fffffff;
+          if (bits < 0x7f800000) top = max(top, bits);
+        }
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) top = max(top, __shfl_xor(top, off, kWave));
-      if (lane == 0) tops[wave] = top;
-    }
-    __syncthreads();  // the tile before has been read; the tops are there
-    if (!BF) {
+      if (lane == 0) tops[b][wave] = top;
+      __syncthreads();
+      top = 0;
 #pragma unroll
-      for (int w = 0; w < kGradWaves; w++) top = max(top, tops[w]);
-      const int next = fp16_exponent(top);
-      if (top != 0 && (!any || next < e)) {
-        const int by = any ? next - e : 0;
-        e = next;
+      for (int w = 0; w < kGradWaves; w++) top = max(top, tops[b][w]);
+      const int wanted = fp16_exponent(top);
+      if (top != 0 && (!any || wanted < e)) {
+        const int by = any ? wanted - e : 0;
+        e = wanted;
         any = true;
         if (by != 0)
 #pragma unroll
@@ -343,50 +415,45 @@ __device__ __forceinline__ void sum_part(const SpreadArgs& g, int index, int col
               for (int j = 0; j < 4; j++) acc[i][m][j] = times_power(acc[i][m][j], by);
       }
     }
-    if (s == 0) places[t] = (int)token;
 #pragma unroll
     for (int i = 0; i < RB; i++) {
       const int r = (s + i * kPerToken) * 4;
 #pragma unroll
       for (int j = 0; j < 4; j++) {
         uint16_t part[PARTS];
-        split_parts<BF>(BF ? val[i][j] : times_power(val[i][j], e), part);
+        split_parts<BF>(BF ? sum[i][j] : times_power(sum[i][j], e), part);
 #pragma unroll
-        for (int q = 0; q < PARTS; q++) turned[q][r + j][t] = part[q];
+        for (int q = 0; q < PARTS; q++) turned[b][q][r + j][t] = part[q];
       }
     }
-    __syncthreads();
-    if (c0 - i16 * 8 < C) {
+    if (s == 0) places[b ^ 1][t] = next;
+    __syncthreads();  // the parts and the next places are there; the buffers before have been read
+    load_values(t0 + kTile, next);
+    loads_stay();
+    next = token_of(t0 + 2 * kTile);
 #pragma unroll
-      for (int half = 0; half < kTile / 32; half++) {
-        const int at = half * 32 + h * 8;
-        if (t0 + half * 32 >= tile.count) break;
-        us8_t rows[8], cols[8];
+    for (int half = 0; half < HALVES; half++) {
+      const int at = half * 32 + h * 8;
+      us8_t cols[8];
+      if (t0 + half * 32 + 32 > tile.count)
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-          rows[i] = us8_t{};
-          if (t0 + at + i < tile.count) {
-            const uint16_t* from = rows_of + places[at + i] * C + c0;
-            if (ROWS_X) {
-              if (c0 < C) rows[i] = *reinterpret_cast<const us8_t*>(from);
-            } else {
-              rows[i] = load8(from, C - c0);
-            }
-          }
+        for (int i = 0; i < 8; i++)
+          if (t0 + at + i >= tile.count) rows[half][i] = us8_t{};
+      transpose8(rows[half], cols);
+      if (t0 + kTile < tile.count) load_rows(half, places[b ^ 1]);
+      loads_stay();
+      if (!active || t0 + half * 32 >= tile.count) continue;
+#pragma unroll
+      for (int i = 0; i < RB; i++)
+#pragma unroll
+        for (int q = 0; q < PARTS; q++) {
+          const us8_t fu = *reinterpret_cast<const us8_t*>(&turned[b][q][i * 16 + i16][at]);
+#pragma unroll
+          for (int m = 0; m < 8; m++) acc[i][m] = Half16<BF>::mma(fu, cols[m], acc[i][m]);
         }
-        transpose8(rows, cols);
-#pragma unroll
-        for (int i = 0; i < RB; i++)
-#pragma unroll
-          for (int q = 0; q < PARTS; q++) {
-            const us8_t fu = *reinterpret_cast<const us8_t*>(&turned[q][i * 16 + i16][at]);
-#pragma unroll
-            for (int m = 0; m < 8; m++) acc[i][m] = Half16<BF>::mma(fu, cols[m], acc[i][m]);
-          }
-      }
     }
-    __syncthreads();
   }
+  if (!active) return;
   const float scale = p.scales[tile.l];
   const int64_t size = (int64_t)p.R * C;
   // an adapter's only chunk is its whole sum
@@ -407,7 +474,7 @@ __device__ __forceinline__ void sum_part(const SpreadArgs& g, int index, int col
         f[m][j] *= scale;
       }
     if (ROWS_X) {
-      if (c0 < C)
+      if (wanted < C)
 #pragma unroll
         for (int j = 0; j < 4; j++) {
           float* at = out + (r0 + r + j) * C + c0;
@@ -417,39 +484,28 @@ __device__ __forceinline__ void sum_part(const SpreadArgs& g, int index, int col
     } else {
 #pragma unroll
       for (int m = 0; m < 8; m++)
-        if (c0 + m < C)
-          *reinterpret_cast<f4_t*>(out + (c0 + m) * p.R + r0 + r) =
+        if (wanted < C && c0 + m >= wanted)
+          *reinterpret_cast<f4_t*>(out + (int64_t)(c0 + m) * p.R + r0 + r) =
               f4_t{f[m][0], f[m][1], f[m][2], f[m][3]};
     }
   }
 }
 
 template <bool BF, int RB>
-__global__ __launch_bounds__(kGradWaves * 64) void lora_spread_kernel(const SpreadArgs g) {
-  constexpr int RS = RB < 4 ? RB : 4;  // ranks of the sums, in blocks
-  constexpr int kDx = kTile * (RB * 32 + 8) * 2 + kTile * 4;
-  constexpr int kSum = (BF ? 3 : 2) * RS * 16 * (kTile + 8) * 2 + kTile * 4 + kGradWaves * 4;
-  __shared__ __align__(16) char lds[kDx > kSum ? kDx : kSum];
-  int64_t at = blockIdx.x;
-  const int groups = (g.p.R + 63) / 64;
-  const int64_t sums_a = g.chunks * g.k_cols * groups, sums_b = g.chunks * g.n_cols * groups;
-  if (at < sums_a) {
-    const int cg = g.k_cols * groups;
-    sum_part<BF, RS, true>(g, (int)(at / cg), (int)(at % cg / groups), (int)(at % groups) * 64, lds);
-    return;
-  }
-  at -= sums_a;
-  if (at < sums_b) {
-    const int cg = g.n_cols * groups;
-    sum_part<BF, RS, false>(g, (int)(at / cg), (int)(at % cg / groups), (int)(at % groups) * 64, lds);
-    return;
-  }
-  at -= sums_b;
-  dx_part<BF, RB>(g, (int)(at / g.k_cols), (int)(at % g.k_cols), lds);
+__global__ __launch_bounds__(kGradWaves * 64) void lora_sums_kernel(const SpreadArgs g) {
+  constexpr int kSum = 2 * ((BF ? 3 : 2) * RB * 16 * (kTile + 8) * 2 + kTile * 4 + kGradWaves * 4);
+  __shared__ __align__(16) char lds[kSum];
+  const int groups = (g.p.R + 63) / 64, cols = (g.k_cols + g.n_cols) * groups;
+  const int index = blockIdx.x / cols, at = blockIdx.x % cols;
+  const int col = at / groups, r0 = at % groups * 64;
+  if (col < g.k_cols)
+    sum_part<BF, RB, true>(g, index, col, r0, lds);
+  else
+    sum_part<BF, RB, false>(g, index, col - g.k_cols, r0, lds);
 }
 
 // ---------------------------------------------------------------------------
-// the join: da and db of adapters with several chunks, or none
+// the join: da and db of adapters with several chunks, or none; dx beside it
 // ---------------------------------------------------------------------------
 struct JoinArgs {
   const int32_t* starts;
@@ -457,9 +513,10 @@ struct JoinArgs {
   int64_t size_a, size_b;
   const float *part_a, *part_b;
   float *da, *db;
+  int64_t blocks;  // of an adapter
 };
-__global__ __launch_bounds__(256) void lora_join_kernel(const JoinArgs g) {
-  const int l = blockIdx.y;
+__device__ __forceinline__ void join_part(const JoinArgs& g, int64_t index) {
+  const int l = (int)(index / g.blocks);
   int s0 = 0, s1 = 0;
   if (g.T > 0) {
     s0 = min(max(g.starts[l], 0), g.T);
@@ -468,21 +525,31 @@ __global__ __launch_bounds__(256) void lora_join_kernel(const JoinArgs g) {
   const int mine = (s1 - s0 + g.chunk - 1) / g.chunk;
   if (mine == 1) return;
   const int64_t before = share_of(s0, g.chunk);
-  int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  const float* part = g.part_a;
-  float* out = g.da;
-  int64_t size = g.size_a;
-  if (at >= size) {
-    at -= size;
-    part = g.part_b;
-    out = g.db;
-    size = g.size_b;
-    if (at >= size) return;
+  for (int64_t i = index % g.blocks; i * 1024 < g.size_a + g.size_b; i += g.blocks) {
+    int64_t at = (i * 256 + threadIdx.x) * 4;
+    const bool b = at >= g.size_a;
+    if (b) at -= g.size_a;
+    const int64_t size = b ? g.size_b : g.size_a;
+    if (at >= size) break;
+    const float* part = (b ? g.part_b : g.part_a) + before * size + at;
+    f4_t sum = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int c = 0; c < mine; c++) sum += *reinterpret_cast<const f4_t*>(part + c * size);
+    *reinterpret_cast<f4_t*>((b ? g.db : g.da) + l * size + at) = sum;
   }
-  f4_t sum = {0, 0, 0, 0};
-  for (int c = 0; c < mine; c++)
-    sum += *reinterpret_cast<const f4_t*>(part + (before + c) * size + at);
-  *reinterpret_cast<f4_t*>(out + l * size + at) = sum;
+}
+__global__ __launch_bounds__(256) void lora_join_kernel(const JoinArgs g) {
+  join_part(g, blockIdx.x);
+}
+template <bool BF, int RB>
+__global__ __launch_bounds__(kGradWaves * 64) void lora_finish_kernel(const SpreadArgs g,
+                                                                      const JoinArgs join) {
+  extern __shared__ __align__(16) char lds[];
+  const int64_t dx = g.tiles * g.k_cols, at = blockIdx.x;
+  if (at < dx)
+    dx_part<BF, RB>(g, (int)(at / g.k_cols), (int)(at % g.k_cols), lds);
+  else
+    join_part(join, at - dx);
 }
 
 // How a call is divided: shares of N for u, tokens of a chunk of the sums.
@@ -496,16 +563,18 @@ struct Division {
 Division divide(const LoraSizes& s) {
   Division d;
   d.tiles = lora_tiles(s.T, s.L, kTile);
-  const int64_t most = (s.N + 255) / 256;
+  const int64_t most = (s.N + kBackWaves * 64 - 1) / (kBackWaves * 64);
   int64_t n = (512 + d.tiles - 1) / d.tiles;
+  if (n > kMostSplits) n = kMostSplits;
   if (n > most) n = most;
-  d.n_share = (int)(((s.N + n - 1) / n + 255) / 256 * 256);
+  d.n_share = (int)(((s.N + n - 1) / n + 63) / 64 * 64);
   d.splits = (int)((s.N + d.n_share - 1) / d.n_share);
   d.k_cols = (int)((s.K + kCols - 1) / kCols);
   d.n_cols = (int)((s.N + kCols - 1) / kCols);
-  // chunks enough for 512 workgroups, of 256 tokens at least
+  // chunks as many as the card holds workgroups at once, of 256 tokens at least
   const int64_t cols = (d.k_cols + d.n_cols) * ((s.R + 63) / 64);
-  const int64_t wanted = (512 + cols - 1) / cols;
+  const int64_t held = s.R > 32 ? 256 : 512;
+  const int64_t wanted = held > cols ? held / cols : 1;
   int64_t chunk = ((s.T + wanted - 1) / wanted + kTile - 1) / kTile * kTile;
   if (chunk < 256) chunk = 256;
   d.chunk = (int)chunk;
@@ -517,26 +586,29 @@ Division divide(const LoraSizes& s) {
 int64_t u_floats(const LoraSizes& s, const Division& d) { return d.splits * s.T * s.R; }
 
 template <bool BF, int RB>
-hipError_t run(const BackArgs& back, const SpreadArgs& spread, const Division& d,
-               hipStream_t stream) {
+hipError_t run(const BackArgs& back, const SpreadArgs& spread, const JoinArgs& join,
+               const Division& d, hipStream_t stream) {
   constexpr int RU = RB < 4 ? RB : 4;
   const int groups = (back.p.R + 63) / 64;
-  lora_back_kernel<BF, RU><<<dim3((unsigned)d.tiles, d.splits, groups), kGradWaves * 64, 0, stream>>>(back);
-  hipError_t e = hipGetLastError();
+  hipError_t e = launch_lds(lora_back_kernel<BF, RU>, dim3((unsigned)d.tiles, d.splits, groups),
+                            kBackWaves * 64, back_bytes<RU>(), stream, back);
   if (e != hipSuccess) return e;
-  const int64_t grid =
-      d.chunks * (d.k_cols + d.n_cols) * groups + d.tiles * d.k_cols;
-  lora_spread_kernel<BF, RB><<<(unsigned)grid, kGradWaves * 64, 0, stream>>>(spread);
-  return hipGetLastError();
+  lora_sums_kernel<BF, RU><<<(unsigned)(d.chunks * (d.k_cols + d.n_cols) * groups),
+                             kGradWaves * 64, 0, stream>>>(spread);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch_lds(lora_finish_kernel<BF, RB>,
+                    dim3((unsigned)(d.tiles * d.k_cols + join.blocks * join.L)), kGradWaves * 64,
+                    dx_bytes<RB>(), stream, spread, join);
 }
 template <bool BF>
-hipError_t run(const BackArgs& back, const SpreadArgs& spread, const Division& d,
-               hipStream_t stream) {
+hipError_t run(const BackArgs& back, const SpreadArgs& spread, const JoinArgs& join,
+               const Division& d, hipStream_t stream) {
   const int blocks = (back.p.R + 15) / 16;
-  if (blocks <= 1) return run<BF, 1>(back, spread, d, stream);
-  if (blocks <= 2) return run<BF, 2>(back, spread, d, stream);
-  if (blocks <= 4) return run<BF, 4>(back, spread, d, stream);
-  return run<BF, 8>(back, spread, d, stream);
+  if (blocks <= 1) return run<BF, 1>(back, spread, join, d, stream);
+  if (blocks <= 2) return run<BF, 2>(back, spread, join, d, stream);
+  if (blocks <= 4) return run<BF, 4>(back, spread, join, d, stream);
+  return run<BF, 8>(back, spread, join, d, stream);
 }
 
 }  // namespace
@@ -565,15 +637,15 @@ hipError_t launch_lora_grad(const void* dy, const void* x, const float* v, int d
                              da,       db,      part_a,
                              part_b,   d.chunk, d.tiles,
                              d.chunks, d.k_cols, d.n_cols};
-  if (s.T > 0) {
-    const hipError_t e = dtype == kBF16 ? run<true>(back, spread, d, stream)
-                                        : run<false>(back, spread, d, stream);
-    if (e != hipSuccess) return e;
-  }
+  // 1024 values a round; of many adapters, workgroups take several rounds each
+  int64_t blocks = (s.R * (s.K + s.N) + 1023) / 1024;
+  if (blocks > (1 << 20) / s.L) blocks = (1 << 20) / s.L;
   const JoinArgs join = {p.starts, (int)p.T, p.L, s.T > 0 ? d.chunk : 1, s.R * s.K, s.R * s.N,
-                         part_a,   part_b,   da,  db};
-  const int64_t quads = (s.R * (s.K + s.N)) / 4;
-  lora_join_kernel<<<dim3((unsigned)((quads + 255) / 256), (unsigned)s.L), 256, 0, stream>>>(join);
+                         part_a,   part_b,   da,  db, blocks};
+  if (s.T > 0)
+    return dtype == kBF16 ? run<true>(back, spread, join, d, stream)
+                          : run<false>(back, spread, join, d, stream);
+  lora_join_kernel<<<(unsigned)(join.blocks * s.L), 256, 0, stream>>>(join);
   return hipGetLastError();
 }
 
