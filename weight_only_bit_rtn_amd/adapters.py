@@ -16,8 +16,8 @@ from __future__ import annotations
 
 import ctypes
 
-from . import load_library as _load_library
-from .w8a8 import _apart, _check_tensor, _float_type, _out, _run, _torch
+from . import _check, load_library as _load_library
+from .w8a8 import _apart, _check_tensor, _float_type, _out, _run, _stream_handle, _torch
 
 LORA_MAX_R = 128
 LORA_MAX_L = 1024
@@ -27,6 +27,7 @@ EXPORTED_LORA = ("lowbit_lora_plan", "lowbit_lora_workspace_bytes", "lowbit_lora
                  "lowbit_lora_grad_workspace_bytes", "lowbit_lora_grad")
 
 _declared = None
+_entry = {}  # name: (entry point, its workspace size)
 
 
 def _lib() -> ctypes.CDLL:
@@ -44,6 +45,8 @@ def _lib() -> ctypes.CDLL:
                                      vp, vp, vp, vp, vp, i64, vp]
     for name in EXPORTED_LORA:
         getattr(lib, name).restype = i64 if name.endswith("_bytes") else i32
+    for name in ("lowbit_lora", "lowbit_lora_grad"):
+        _entry[name] = (getattr(lib, name), getattr(lib, name + "_workspace_bytes"))
     _declared = lib
     return lib
 
@@ -113,7 +116,7 @@ def _adapters(x, a, b, scales, plan, name: str):
         raise TypeError("a and b must be torch.Tensors")
     if a.dim() != 3 or b.dim() != 3:
         raise ValueError("a and b must have 3 dimensions")
-    L, R = a.shape[0], a.shape[1]
+    L, R, _ = a.shape
     N = b.shape[1]
     _check_tensor(a, "a", dtype, dev, (L, R, K))
     _check_tensor(b, "b", dtype, dev, (L, N, R))
@@ -126,6 +129,29 @@ def _adapters(x, a, b, scales, plan, name: str):
     return kind, T, N, K, R, L, dev, shared
 
 
+def _call(name: str, sizes, args, device) -> None:
+    """Calls an entry point on ``args``, its workspace and the current stream of the tensors'
+    device, which it makes the current one."""
+    torch = _torch()
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(name, sizes, args, device)
+    if not _entry:
+        _lib()
+    call, need_of = _entry[name]
+    need = need_of(*sizes)
+    if need > 0:
+        # torch's caching allocator hands out blocks aligned to 512 bytes
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        at = workspace.data_ptr()
+    else:
+        _check(need, name + "_workspace_bytes")
+        at = None
+    status = call(*args, at, need, _stream_handle(device))
+    if status:
+        _check(status, name)
+
+
 def lora(x, a, b, scales, plan, y=None, out=None, save: bool = False):
     """out[T][N] = y + s_l b_l (a_l x), each token through the adapter l that the plan
     (of ``lora_plan``) names; a token without one keeps y.  ``x`` [T][K], ``y`` [T][N] and the
@@ -136,15 +162,16 @@ def lora(x, a, b, scales, plan, y=None, out=None, save: bool = False):
     kind, T, N, K, R, L, dev, shared = _adapters(x, a, b, scales, plan, "x")
     if y is not None:
         _check_tensor(y, "y", x.dtype, dev, (T, N))
-    o = _out(out, "out", (T, N), x.dtype, dev)
-    if out is not None:
+    if out is None:
+        o = torch.empty((T, N), dtype=x.dtype, device=dev) if y is None else torch.empty_like(y)
+    else:
+        o = _out(out, "out", (T, N), x.dtype, dev)
         inputs = (x, a, b, scales, plan["order"], plan["starts"])
         if y is not None and y.data_ptr() != o.data_ptr():
             inputs += (y,)
         _apart(o, "out", *inputs)
     v = torch.empty((T, R), dtype=torch.float32, device=dev) if save else None
-    _lib()
-    _run("lowbit_lora", (T, N, K, R, L),
+    _call("lowbit_lora", (T, N, K, R, L),
          (x.data_ptr(), kind, T, *shared, None if y is None else y.data_ptr(), o.data_ptr(),
           v.data_ptr() if save else None), dev)
     return (o, v) if save else o
@@ -162,16 +189,17 @@ def lora_grad(dy, x, v, a, b, scales, plan, dx=None, out=None):
     _check_tensor(v, "v", torch.float32, dev, (T, R))
     if dx is not None:
         _check_tensor(dx, "dx", x.dtype, dev, (T, K))
-    o = _out(out, "out", (T, K), x.dtype, dev)
-    if out is not None:
+    if out is None:
+        o = torch.empty_like(x)
+    else:
+        o = _out(out, "out", (T, K), x.dtype, dev)
         inputs = (dy, x, v, a, b, scales, plan["order"], plan["starts"])
         if dx is not None and dx.data_ptr() != o.data_ptr():
             inputs += (dx,)
         _apart(o, "out", *inputs)
     da = torch.empty((L, R, K), dtype=torch.float32, device=dev)
     db = torch.empty((L, N, R), dtype=torch.float32, device=dev)
-    _lib()
-    _run("lowbit_lora_grad", (T, N, K, R, L),
+    _call("lowbit_lora_grad", (T, N, K, R, L),
          (dy.data_ptr(), x.data_ptr(), v.data_ptr(), kind, T, *shared,
           None if dx is None else dx.data_ptr(), o.data_ptr(), da.data_ptr(), db.data_ptr()), dev)
     return o, da, db

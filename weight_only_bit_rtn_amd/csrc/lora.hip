@@ -205,8 +205,8 @@ __global__ __launch_bounds__(kLoraWaves * 64, RB < 8 ? 2 : 1) void lora_up_kerne
       }
     wave_lds_order();
   };
-  // the 64 outputs of token block j, `left` of this lane's eight inside
-  auto finish = [&](int j, int n0, auto whole, int left) {
+  // the 64 outputs of token block j, whose y and places are given, `left` of a lane's eight inside
+  auto finish = [&](int j, int n0, const us8_t* y2, const int64_t* at2, auto whole, int left) {
     f4_t acc[4] = {};
     multiply_parts<BF, RB>(fb, parts[j * 16 + i16], h, acc);
 #pragma unroll
@@ -218,7 +218,7 @@ __global__ __launch_bounds__(kLoraWaves * 64, RB < 8 ? 2 : 1) void lora_up_kerne
       const f4_t lo = *reinterpret_cast<const f4_t*>(&result[t][chunk * 8]);
       const f4_t hi = *reinterpret_cast<const f4_t*>(&result[t][chunk * 8 + 4]);
       const int e = BF ? 0 : exponent[j * 16 + t];
-      us8_t o = g.y ? had[j * 2 + q] : us8_t{};
+      us8_t o = g.y ? y2[q] : us8_t{};
       // a token without an adapter keeps the bits it has
       if (!none)
 #pragma unroll
@@ -230,9 +230,9 @@ __global__ __launch_bounds__(kLoraWaves * 64, RB < 8 ? 2 : 1) void lora_up_kerne
         }
       if (j * 16 + t < tile.count) {
         if (whole)
-          store8(g.out + at[j * 2 + q] + n0, o);
+          store8(g.out + at2[q] + n0, o);
         else
-          store8(g.out + at[j * 2 + q] + n0, o, left);
+          store8(g.out + at2[q] + n0, o, left);
       }
     }
     wave_lds_order();
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(kLoraWaves * 64, RB < 8 ? 2 : 1) void lora_up_kerne
 #pragma unroll
     for (int j = 0; j < TB; j++) {
       if (j * 16 >= tile.count) break;
-      finish(j, n0, std::true_type(), 8);
+      finish(j, n0, had + j * 2, at + j * 2, std::true_type(), 8);
     }
 #pragma unroll
     for (int q = 0; q < TILE / 8; q++) had[q] = ahead[q];
@@ -275,12 +275,19 @@ __global__ __launch_bounds__(kLoraWaves * 64, RB < 8 ? 2 : 1) void lora_up_kerne
     for (int q = 0; q < CHUNKS; q++)  // beyond the last row: for outputs that nobody stores
       if (q < per_row)
         vb[q] = *reinterpret_cast<const us8_t*>(b + (int64_t)n0 * p.R + min(q * 64 + lane, most) * 8);
-#pragma unroll
-    for (int q = 0; q < TILE / 8; q++) had[q] = load8(y + at[q] + n0, left);
     stage_b();
+#pragma unroll 1
+    for (int j = 0; j * 16 < tile.count; j++) {
+      int64_t at2[2];
+      us8_t y2[2];
 #pragma unroll
-    for (int j = 0; j < TB; j++)
-      if (j * 16 < tile.count) finish(j, n0, std::false_type(), left);
+      for (int q = 0; q < 2; q++) {
+        const int t = min(j * 16 + q * 8 + row, tile.count - 1);
+        at2[q] = token_at(p.order, p.T, tile.begin + t) * N + chunk * 8;
+        y2[q] = load8(y + at2[q] + n0, left);
+      }
+      finish(j, n0, y2, at2, std::false_type(), left);
+    }
   }
 }
 
@@ -306,7 +313,10 @@ Division divide(const LoraSizes& s) {
     shares(s.K, 512, 256, d.splits, d.k_share);
   else
     shares(s.K, 256, 512, d.splits, d.k_share);
-  shares(s.N, 256, 1024, d.ranges, d.n_share);
+  // Small tiles: many short workgroups (64 tokens of 64 adapters, 11008 outputs, 16 ranks: 8.4 us
+  // with 1024, 9.7 with 512).  Large ones: as many as the card holds at once (1024 / 512 / 256 of
+  // them: 8192x12288, 64 ranks 101 / 92 / 127; 4096x4096, 128 ranks, one to a CU, 84 / 58 / 42).
+  shares(s.N, 256, d.tile == 16 ? 1024 : s.R > 64 ? 256 : 512, d.ranges, d.n_share);
   return d;
 }
 

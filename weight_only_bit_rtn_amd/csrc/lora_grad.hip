@@ -166,6 +166,7 @@ struct SpreadArgs {
   int chunk;               // tokens
   int64_t tiles, chunks;   // bounds
   int k_cols, n_cols;      // workgroups along K and N
+  int dx_cols;             // columns of one of dx, in units of kCols
 };
 
 // Eight rows' eight elements each, rows[i] for row i, turned around: cols[j] holds
@@ -185,7 +186,7 @@ __device__ __forceinline__ void transpose8(const us8_t (&rows)[8], us8_t (&cols)
   for (int j = 0; j < 8; j++) cols[j] = __builtin_bit_cast(us8_t, out[j]);
 }
 
-// dx of one tile and 512 columns, 128 to a wave, with s u in two parts as s v in the
+// dx of one tile and `cols` times 512 columns, 128 to a wave, with s u in two parts as s v in the
 // forward pass.  Results pass through LDS as there: sixteen lanes then hold the 128
 // columns of one token.
 template <int RB>
@@ -193,7 +194,8 @@ constexpr int dx_bytes() {
   return kTile * ((RB * 32 + 8) * 2 + 4) + kGradWaves * 16 * 132 * 4;
 }
 template <bool BF, int RB>
-__device__ __forceinline__ void dx_part(const SpreadArgs& g, int index, int col, char* lds) {
+__device__ __forceinline__ void dx_part(const SpreadArgs& g, int index, int col, int cols,
+                                        char* lds) {
   constexpr int PITCH = RB * 32 + 8, TB = kTile / 16, C = Ranks<RB>::kChunks;
   uint16_t(*const parts)[PITCH] = reinterpret_cast<uint16_t(*)[PITCH]>(lds);
   int* const exponent = reinterpret_cast<int*>(lds + kTile * PITCH * 2);
@@ -207,33 +209,35 @@ __device__ __forceinline__ void dx_part(const SpreadArgs& g, int index, int col,
   float(*const result)[132] =
       reinterpret_cast<float(*)[132]>(lds + kTile * (PITCH * 2 + 4) + wave * 16 * 132 * 4);
   const int64_t K = p.K;
-  const int k0 = col * kCols + wave * 128;
-  const int mine = min(k0 + i16 * 8, p.K - 8);  // beyond the last column: for no one's results
-  const bool inside = k0 + i16 * 8 < p.K;
-  int64_t at[TB][4];  // of token 16 j + 4 q + h, this lane's eight columns
+  int k0 = col * kCols + wave * 128;
+  int64_t row[TB][4];  // of token 16 j + 4 q + h
 #pragma unroll
   for (int j = 0; j < TB; j++)
 #pragma unroll
     for (int q = 0; q < 4; q++)
-      at[j][q] = token_at(p.order, p.T, tile.begin + min(j * 16 + q * 4 + h, tile.count - 1)) * K + mine;
+      row[j][q] = token_at(p.order, p.T, tile.begin + min(j * 16 + q * 4 + h, tile.count - 1)) * K;
   // without a base: read what dx holds, to no one's use
   const uint16_t* const base = g.base ? g.base : g.dx;
   us8_t had[2][4];
+  auto mine = [&] { return min(k0 + i16 * 8, p.K - 8); };  // beyond the last: for no one's results
   auto load_base = [&](us8_t(&to)[4], int j) {
 #pragma unroll
     for (int q = 0; q < 4; q++)
-      to[q] = *reinterpret_cast<const us8_t*>(base + at[j][q]);
+      to[q] = *reinterpret_cast<const us8_t*>(base + row[j][q] + mine());
+  };
+  us8_t fa[8][C];  // rows of a first, then turned around
+  auto load_a = [&] {
+#pragma unroll
+    for (int c = 0; c < C; c++) {
+      // beyond the last rank: read within the pool, cleared before the product
+      const uint16_t* from =
+          p.a + ((int64_t)(none ? 0 : tile.l) * p.R + min(Ranks<RB>::of(c, h), p.R - 8)) * K + mine();
+#pragma unroll
+      for (int i = 0; i < 8; i++) fa[i][c] = *reinterpret_cast<const us8_t*>(from + i * K);
+    }
   };
   load_base(had[0], 0);
-  us8_t fa[8][C];  // rows of a first, then turned around
-#pragma unroll
-  for (int c = 0; c < C; c++) {
-    // beyond the last rank: read within the pool, cleared before the product
-    const uint16_t* from =
-        p.a + ((int64_t)(none ? 0 : tile.l) * p.R + min(Ranks<RB>::of(c, h), p.R - 8)) * K + mine;
-#pragma unroll
-    for (int i = 0; i < 8; i++) fa[i][c] = *reinterpret_cast<const us8_t*>(from + i * K);
-  }
+  load_a();
   spread_parts<BF, RB, kTile, kGradWaves * 64>(
       [&](int t, int r) {
         return none ? f4_t{0, 0, 0, 0}
@@ -241,49 +245,56 @@ __device__ __forceinline__ void dx_part(const SpreadArgs& g, int index, int col,
       },
       none ? 0.0f : p.scales[tile.l], tile.count, p.R, parts, exponent);
   __syncthreads();
-  if (k0 >= p.K) return;
+  for (; cols > 0 && k0 < p.K; cols--) {
 #pragma unroll
-  for (int c = 0; c < C; c++) {
-    us8_t rows[8], turned[8];
+    for (int c = 0; c < C; c++) {
+      us8_t rows[8], turned[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) rows[i] = fa[i][c];
-    transpose8(rows, turned);
-    const bool none_such = Ranks<RB>::of(c, h) >= p.R;
+      for (int i = 0; i < 8; i++) rows[i] = fa[i][c];
+      transpose8(rows, turned);
+      const bool none_such = Ranks<RB>::of(c, h) >= p.R;
 #pragma unroll
-    for (int i = 0; i < 8; i++) fa[i][c] = none_such ? us8_t{} : turned[i];
-  }
-#pragma unroll
-  for (int j = 0; j < TB; j++) {
-    if (j * 16 >= tile.count) break;
-    if (j + 1 < TB) load_base(had[(j + 1) % 2], j + 1);
-    f4_t acc[8] = {};
-    multiply_parts<BF, RB>(fa, parts[j * 16 + i16], h, acc);
-    // row 4 h + i of product m is column 8 (4 h + i) + m
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      float* const to = &result[i16][(h * 4 + i) * 8];
-      *reinterpret_cast<f4_t*>(to) = f4_t{acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
-      *reinterpret_cast<f4_t*>(to + 4) = f4_t{acc[4][i], acc[5][i], acc[6][i], acc[7][i]};
+      for (int i = 0; i < 8; i++) fa[i][c] = none_such ? us8_t{} : turned[i];
     }
-    wave_lds_order();
 #pragma unroll
-    for (int q = 0; q < 4; q++) {
-      const int t = q * 4 + h;
-      const f4_t lo = *reinterpret_cast<const f4_t*>(&result[t][i16 * 8]);
-      const f4_t hi = *reinterpret_cast<const f4_t*>(&result[t][i16 * 8 + 4]);
-      const int e = BF ? 0 : exponent[j * 16 + t];
-      us8_t o = g.base ? had[j % 2][q] : us8_t{};
-      if (!none)
+    for (int j = 0; j < TB; j++) {
+      if (j * 16 >= tile.count) break;
+      if (j + 1 < TB) load_base(had[(j + 1) % 2], j + 1);
+      f4_t acc[8] = {};
+      multiply_parts<BF, RB>(fa, parts[j * 16 + i16], h, acc);
+      // row 4 h + i of product m is column 8 (4 h + i) + m
 #pragma unroll
-        for (int m = 0; m < 8; m++) {
-          float f = m < 4 ? lo[m % 4] : hi[m % 4];
-          if (!BF) f = times_power(f, -e);
-          if (g.base) f += Half16<BF>::to(o[m]);
-          o[m] = Half16<BF>::from(f);
-        }
-      if (inside && j * 16 + t < tile.count) *reinterpret_cast<us8_t*>(g.dx + at[j][q]) = o;
+      for (int i = 0; i < 4; i++) {
+        float* const to = &result[i16][(h * 4 + i) * 8];
+        *reinterpret_cast<f4_t*>(to) = f4_t{acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
+        *reinterpret_cast<f4_t*>(to + 4) = f4_t{acc[4][i], acc[5][i], acc[6][i], acc[7][i]};
+      }
+      wave_lds_order();
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        const int t = q * 4 + h;
+        const f4_t lo = *reinterpret_cast<const f4_t*>(&result[t][i16 * 8]);
+        const f4_t hi = *reinterpret_cast<const f4_t*>(&result[t][i16 * 8 + 4]);
+        const int e = BF ? 0 : exponent[j * 16 + t];
+        us8_t o = g.base ? had[j % 2][q] : us8_t{};
+        if (!none)
+#pragma unroll
+          for (int m = 0; m < 8; m++) {
+            float f = m < 4 ? lo[m % 4] : hi[m % 4];
+            if (!BF) f = times_power(f, -e);
+            if (g.base) f += Half16<BF>::to(o[m]);
+            o[m] = Half16<BF>::from(f);
+          }
+        if (k0 + i16 * 8 < p.K && j * 16 + t < tile.count)
+          *reinterpret_cast<us8_t*>(g.dx + row[j][q] + mine()) = o;
+      }
+      wave_lds_order();
     }
-    wave_lds_order();
+    k0 += kCols;
+    if (cols > 1 && k0 < p.K) {
+      load_base(had[0], 0);
+      load_a();
+    }
   }
 }
 
@@ -298,15 +309,22 @@ __device__ __forceinline__ int64_t share_of(int first, int chunk) { return 2 * (
 // buffers; their rows of x or dy go straight to the registers, where the next 64 tokens'
 // are under way while these are multiplied.  fp16: the parts stand for values times 2^e, e
 // by the largest value so far; the sums follow when it changes.
+// At most two blocks of ranks to a wave: four double the waves, two for each 128 columns, whose
+// second reading of a row the vector cache serves.
+template <int RB>
+struct SumWaves {
+  static constexpr int kBlocks = RB < 2 ? 1 : 2, kCount = kGradWaves * RB / kBlocks;
+};
 template <bool BF, int RB, bool ROWS_X>
 __device__ __forceinline__ void sum_part(const SpreadArgs& g, int index, int col, int r0,
                                          char* lds) {
   constexpr int PARTS = BF ? 3 : 2, TURN = kTile + 8, HALVES = kTile / 32;
-  constexpr int kPerToken = kGradWaves * 64 / kTile;
+  constexpr int RW = SumWaves<RB>::kBlocks, WAVES = SumWaves<RB>::kCount;
+  constexpr int kPerToken = WAVES * 64 / kTile;
   typedef uint16_t Turned[PARTS][RB * 16][TURN];
   Turned* const turned = reinterpret_cast<Turned*>(lds);                       // [2]
   int(*const places)[kTile] = reinterpret_cast<int(*)[kTile]>(lds + 2 * sizeof(Turned));  // [2]
-  int(*const tops)[kGradWaves] = reinterpret_cast<int(*)[kGradWaves]>(places + 2);     // [2]
+  int(*const tops)[WAVES] = reinterpret_cast<int(*)[WAVES]>(places + 2);     // [2]
   const LoraArgs& p = g.p;
   LoraTile tile;
   if (!find_tile(p.starts, p.L, (int)p.T, g.chunk, index, tile) || tile.l == p.L) return;
@@ -315,27 +333,28 @@ __device__ __forceinline__ void sum_part(const SpreadArgs& g, int index, int col
   const int64_t C = ROWS_X ? p.K : p.N;
   const uint16_t* const rows_of = ROWS_X ? g.x : g.dy;
   const int ranks = min(p.R - r0, RB * 16);
-  const int w0 = col * kCols + wave * 128;  // the wave's columns
+  const int w0 = col * kCols + wave % kGradWaves * 128;  // the wave's columns
+  const int b0 = wave / kGradWaves * RW;                 // and its blocks of ranks
   // this lane's eight; beyond the last column the last eight again, which somebody else
   // stores, and where C is no multiple of eight an overlap with the lane before
   const int wanted = w0 + i16 * 8, c0 = (int)min((int64_t)wanted, C - 8);
   const bool active = w0 < C;
   const int t = threadIdx.x / kPerToken, s = threadIdx.x % kPerToken;
-  f4_t acc[RB][8];
+  f4_t acc[RW][8];
 #pragma unroll
-  for (int i = 0; i < RB; i++)
+  for (int i = 0; i < RW; i++)
 #pragma unroll
     for (int m = 0; m < 8; m++) acc[i][m] = f4_t{0, 0, 0, 0};
   // this thread's token and its values of u or v among the 64 from t0 on
   auto token_of = [&](int t0) {
     return (int)token_at(p.order, p.T, tile.begin + min(t0 + t, tile.count - 1));
   };
-  f4_t val[RB][ROWS_X ? kMostSplits : 1];
+  f4_t val[RW][ROWS_X ? kMostSplits : 1];
   auto load_values = [&](int t0, int token) {
     // beyond the last token or rank: read within the buffer, cleared when they are used
     const int64_t at = ROWS_X ? tile.begin + min(t0 + t, tile.count - 1) : token;
 #pragma unroll
-    for (int i = 0; i < RB; i++) {
+    for (int i = 0; i < RW; i++) {
       const int r = r0 + min((s + i * kPerToken) * 4, ranks - 4);
       if (ROWS_X) {
 #pragma unroll
@@ -347,10 +366,10 @@ __device__ __forceinline__ void sum_part(const SpreadArgs& g, int index, int col
       }
     }
   };
-  f4_t sum[RB];
+  f4_t sum[RW];
   auto add_values = [&](int t0) {
 #pragma unroll
-    for (int i = 0; i < RB; i++) {
+    for (int i = 0; i < RW; i++) {
       sum[i] = val[i][0];
       if (ROWS_X)
 #pragma unroll
@@ -388,7 +407,7 @@ __device__ __forceinline__ void sum_part(const SpreadArgs& g, int index, int col
     if (!BF) {
       int top = 0;
 #pragma unroll
-      for (int i = 0; i < RB; i++)
+      for (int i = 0; i < RW; i++)
 #pragma unroll
         for (int j = 0; j < 4; j++) {
           const int bits = __builtin_bit_cast(int, (float)sum[i][j]) & 0x7fffffff;
@@ -400,7 +419,7 @@ __device__ __forceinline__ void sum_part(const SpreadArgs& g, int index, int col
       __syncthreads();
       top = 0;
 #pragma unroll
-      for (int w = 0; w < kGradWaves; w++) top = max(top, tops[b][w]);
+      for (int w = 0; w < WAVES; w++) top = max(top, tops[b][w]);
       const int wanted = fp16_exponent(top);
       if (top != 0 && (!any || wanted < e)) {
         const int by = any ? wanted - e : 0;
@@ -408,7 +427,7 @@ __device__ __forceinline__ void sum_part(const SpreadArgs& g, int index, int col
         any = true;
         if (by != 0)
 #pragma unroll
-          for (int i = 0; i < RB; i++)
+          for (int i = 0; i < RW; i++)
 #pragma unroll
             for (int m = 0; m < 8; m++)
 #pragma unroll
@@ -416,7 +435,7 @@ __device__ __forceinline__ void sum_part(const SpreadArgs& g, int index, int col
       }
     }
 #pragma unroll
-    for (int i = 0; i < RB; i++) {
+    for (int i = 0; i < RW; i++) {
       const int r = (s + i * kPerToken) * 4;
 #pragma unroll
       for (int j = 0; j < 4; j++) {
@@ -444,10 +463,10 @@ __device__ __forceinline__ void sum_part(const SpreadArgs& g, int index, int col
       loads_stay();
       if (!active || t0 + half * 32 >= tile.count) continue;
 #pragma unroll
-      for (int i = 0; i < RB; i++)
+      for (int i = 0; i < RW; i++)
 #pragma unroll
         for (int q = 0; q < PARTS; q++) {
-          const us8_t fu = *reinterpret_cast<const us8_t*>(&turned[b][q][i * 16 + i16][at]);
+          const us8_t fu = *reinterpret_cast<const us8_t*>(&turned[b][q][(b0 + i) * 16 + i16][at]);
 #pragma unroll
           for (int m = 0; m < 8; m++) acc[i][m] = Half16<BF>::mma(fu, cols[m], acc[i][m]);
         }
@@ -461,8 +480,8 @@ __device__ __forceinline__ void sum_part(const SpreadArgs& g, int index, int col
   float* out = tile.tiles == 1 ? (ROWS_X ? g.da : g.db) + tile.l * size
                                : (ROWS_X ? g.part_a : g.part_b) + share * size;
 #pragma unroll
-  for (int i = 0; i < RB; i++) {
-    const int r = i * 16 + h * 4;
+  for (int i = 0; i < RW; i++) {
+    const int r = (b0 + i) * 16 + h * 4;
     if (r >= ranks) continue;
     float f[8][4];
 #pragma unroll
@@ -492,8 +511,9 @@ __device__ __forceinline__ void sum_part(const SpreadArgs& g, int index, int col
 }
 
 template <bool BF, int RB>
-__global__ __launch_bounds__(kGradWaves * 64) void lora_sums_kernel(const SpreadArgs g) {
-  constexpr int kSum = 2 * ((BF ? 3 : 2) * RB * 16 * (kTile + 8) * 2 + kTile * 4 + kGradWaves * 4);
+__global__ __launch_bounds__(SumWaves<RB>::kCount * 64) void lora_sums_kernel(const SpreadArgs g) {
+  constexpr int kSum =
+      2 * ((BF ? 3 : 2) * RB * 16 * (kTile + 8) * 2 + kTile * 4 + SumWaves<RB>::kCount * 4);
   __shared__ __align__(16) char lds[kSum];
   const int groups = (g.p.R + 63) / 64, cols = (g.k_cols + g.n_cols) * groups;
   const int index = blockIdx.x / cols, at = blockIdx.x % cols;
@@ -545,9 +565,10 @@ template <bool BF, int RB>
 __global__ __launch_bounds__(kGradWaves * 64) void lora_finish_kernel(const SpreadArgs g,
                                                                       const JoinArgs join) {
   extern __shared__ __align__(16) char lds[];
-  const int64_t dx = g.tiles * g.k_cols, at = blockIdx.x;
+  const int ranges = (g.k_cols + g.dx_cols - 1) / g.dx_cols;
+  const int64_t dx = g.tiles * ranges, at = blockIdx.x;
   if (at < dx)
-    dx_part<BF, RB>(g, (int)(at / g.k_cols), (int)(at % g.k_cols), lds);
+    dx_part<BF, RB>(g, (int)(at / ranges), (int)(at % ranges) * g.dx_cols, g.dx_cols, lds);
   else
     join_part(join, at - dx);
 }
@@ -558,7 +579,7 @@ struct Division {
   int splits, n_share;
   int chunk;
   int64_t chunks, shares;
-  int k_cols, n_cols;
+  int k_cols, n_cols, dx_cols;
 };
 Division divide(const LoraSizes& s) {
   Division d;
@@ -571,6 +592,9 @@ Division divide(const LoraSizes& s) {
   d.splits = (int)((s.N + d.n_share - 1) / d.n_share);
   d.k_cols = (int)((s.K + kCols - 1) / kCols);
   d.n_cols = (int)((s.N + kCols - 1) / kCols);
+  // dx: two workgroups to a CU at once
+  const int64_t ranges = 512 / ((s.T + kTile - 1) / kTile);
+  d.dx_cols = ranges < 1 ? d.k_cols : (int)((d.k_cols + ranges - 1) / ranges);
   // chunks as many as the card holds workgroups at once, of 256 tokens at least
   const int64_t cols = (d.k_cols + d.n_cols) * ((s.R + 63) / 64);
   const int64_t held = s.R > 32 ? 256 : 512;
@@ -594,11 +618,12 @@ hipError_t run(const BackArgs& back, const SpreadArgs& spread, const JoinArgs& j
                             kBackWaves * 64, back_bytes<RU>(), stream, back);
   if (e != hipSuccess) return e;
   lora_sums_kernel<BF, RU><<<(unsigned)(d.chunks * (d.k_cols + d.n_cols) * groups),
-                             kGradWaves * 64, 0, stream>>>(spread);
+                             SumWaves<RU>::kCount * 64, 0, stream>>>(spread);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   return launch_lds(lora_finish_kernel<BF, RB>,
-                    dim3((unsigned)(d.tiles * d.k_cols + join.blocks * join.L)), kGradWaves * 64,
+                    dim3((unsigned)(d.tiles * ((d.k_cols + d.dx_cols - 1) / d.dx_cols) +
+                                    join.blocks * join.L)), kGradWaves * 64,
                     dx_bytes<RB>(), stream, spread, join);
 }
 template <bool BF>
@@ -636,7 +661,7 @@ hipError_t launch_lora_grad(const void* dy, const void* x, const float* v, int d
                              static_cast<uint16_t*>(dx),
                              da,       db,      part_a,
                              part_b,   d.chunk, d.tiles,
-                             d.chunks, d.k_cols, d.n_cols};
+                             d.chunks, d.k_cols, d.n_cols, d.dx_cols};
   // 1024 values a round; of many adapters, workgroups take several rounds each
   int64_t blocks = (s.R * (s.K + s.N) + 1023) / 1024;
   if (blocks > (1 << 20) / s.L) blocks = (1 << 20) / s.L;

@@ -112,17 +112,24 @@ def adamw_state(params, bits: int = 8, master: bool = False) -> dict:
 
 
 def _list_type(tensors, name: str, device) -> int:
-    """The type of a list of dense tensors on ``device``, checked."""
+    """The type of a list of dense tensors on ``device``, checked.  A model's adapters are
+    hundreds of tensors: each is asked by a call that needs no Python frame."""
+    Tensor = _torch().Tensor
+    try:
+        fine = (tensors[0].is_cuda and set(map(Tensor.get_device, tensors)) == {device.index}
+                and all(map(Tensor.is_contiguous, tensors))
+                and len(set(map(Tensor.dtype.__get__, tensors))) == 1)
+    except TypeError:
+        raise TypeError(f"{name} must be torch.Tensors") from None
+    if fine:
+        return _type_of(tensors[0].dtype, name)
     dtype = tensors[0].dtype
-    kind = _type_of(dtype, name)
-    index = device.index
     if not tensors[0].is_cuda:
         raise ValueError(f"{name} must live on the GPU")
     for i, t in enumerate(tensors):
-        if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != index:
+        if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != device.index:
             raise ValueError(f"{name}[{i}] must be contiguous, {dtype} and on {device}, as {name}[0] is; "
                              f"got {t.dtype} on {t.device}")
-    return kind
 
 
 def adamw(params, grads, state: dict, lr, betas=(0.9, 0.999), eps: float = 1e-8,
@@ -134,19 +141,20 @@ def adamw(params, grads, state: dict, lr, betas=(0.9, 0.999), eps: float = 1e-8,
     a captured step follows them.  A grad_scale of infinity or NaN leaves everything as it was."""
     torch = _torch()
     params, grads = list(params), list(grads)
-    if len(params) != len(grads):
-        raise ValueError(f"params and grads must be as many, got {len(params)} and {len(grads)}")
+    count = len(params)
+    if count != len(grads):
+        raise ValueError(f"params and grads must be as many, got {count} and {len(grads)}")
     if not params:
         return
-    dev = params[0].device
+    Tensor = torch.Tensor
+    dev = getattr(params[0], "device", None)
     p_kind = _list_type(params, "params", dev)
     g_kind = _list_type(grads, "grads", dev)
-    table = np.empty((len(params), 3), np.int64)
-    table[:, 0] = [p.data_ptr() for p in params]
-    table[:, 1] = [g.data_ptr() for g in grads]
-    table[:, 2] = sizes = [p.numel() for p in params]
-    if sizes != [g.numel() for g in grads]:
+    sizes = list(map(Tensor.numel, params))
+    if sizes != list(map(Tensor.numel, grads)):
         raise ValueError("each gradient must have its parameter's size")
+    table = np.array((list(map(Tensor.data_ptr, params)), list(map(Tensor.data_ptr, grads)), sizes),
+                     np.int64).T.copy()
     blocks = sum(-(-n // ADAMW_BLOCK) for n in sizes)
     n = blocks * ADAMW_BLOCK
     m = state["m"]
@@ -179,7 +187,7 @@ def adamw(params, grads, state: dict, lr, betas=(0.9, 0.999), eps: float = 1e-8,
     place = AdamwState(m.data_ptr(), state["v"].data_ptr(), *tops,
                        None if master is None else master.data_ptr())
     _lib()
-    _run("lowbit_adamw", None, (table.ctypes.data, len(params), p_kind, g_kind, bits,
+    _run("lowbit_adamw", None, (table.ctypes.data, count, p_kind, g_kind, bits,
                                 ctypes.addressof(place), ctypes.addressof(options)), dev)
     torch.autograd.graph.increment_version(params)
 
