@@ -23,16 +23,18 @@
 namespace lowbit {
 namespace {
 
-constexpr int kMostTensors = 90;      // of a launch: with the rest below 4 KB of kernel arguments
+constexpr int kMostTensors = 128;     // of a launch: with the rest below 4 KB of kernel arguments
 constexpr int kWaves = 4;
-constexpr int kWaveBlocks = 4;        // blocks of a wave
+// Blocks of a wave (us of 1 / 2 / 4, kernels alone: 448 fp32 tensors of 112 thousand values 172 /
+// 182 / 212; 100 million bf16 values with an fp32 copy 306 / 300 / 310; two of 65536 3.6 / 4.0 / 5.3)
+constexpr int kWaveBlocks = 1;
 constexpr int kChunk = kWaves * kWaveBlocks * kAdamBlock;  // values of a workgroup
 
 struct Entry {
   void* param;
   const void* grad;
-  int64_t n;
-  int64_t first_block;  // of its moments
+  uint32_t n;            // a larger tensor is several entries, or launches
+  uint32_t first_block;  // of its moments, after the launch's first one
 };
 struct Scalars {
   float b1, c1, b2, c2, eps;
@@ -44,6 +46,7 @@ struct Args {
   Entry t[kMostTensors];
   int32_t first_chunk[kMostTensors + 1];  // workgroups before a tensor's
   int32_t count;
+  int64_t first_block;
   AdamState s;
   Scalars k;
   const float* grad_scale_at;
@@ -115,10 +118,10 @@ __device__ __forceinline__ void store4(void* to, int64_t at, int64_t left, const
   }
 }
 
-// The largest of the wave's values, none negative.
-__device__ __forceinline__ int wave_top(int v) {
+// The largest of the wave's values.
+__device__ __forceinline__ uint32_t wave_top(uint32_t v) {
 #define LOWBIT_DPP_TOP(ctrl, rmask) \
-  v = max(v, __builtin_amdgcn_update_dpp(0, v, ctrl, rmask, 0xf, false))
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rmask, 0xf, false))
   LOWBIT_DPP_TOP(0xb1, 0xf);   // quad_perm [1,0,3,2]
   LOWBIT_DPP_TOP(0x4e, 0xf);   // quad_perm [2,3,0,1]
   LOWBIT_DPP_TOP(0x141, 0xf);  // row_half_mirror
@@ -126,52 +129,44 @@ __device__ __forceinline__ int wave_top(int v) {
   LOWBIT_DPP_TOP(0x142, 0xa);  // row_bcast:15
   LOWBIT_DPP_TOP(0x143, 0xc);  // row_bcast:31
 #undef LOWBIT_DPP_TOP
-  return __builtin_amdgcn_readlane(v, 63);
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
 // Numbers of codes: the upper bits of fp32, counted down from 1's.
-constexpr int kDownM = 0x3F8 - 127, kDownV = 0x3F8 - 255;
-template <int DOWN>
-__device__ __forceinline__ float number(int code) {
-  return code ? __builtin_bit_cast(float, (code + DOWN) << 20) : 0.0f;
+constexpr uint32_t kDownM = 0x3F8 - 127, kDownV = 0x3F8 - 255;
+template <uint32_t DOWN>
+__device__ __forceinline__ float number(uint32_t code) {
+  const float f = __builtin_bit_cast(float, (code << 20) + (DOWN << 20));
+  return code ? f : 0.0f;
 }
-template <int DOWN, int TOP>
-__device__ __forceinline__ int nearest(float q) {
-  const int c = (int)((__builtin_bit_cast(uint32_t, q) + 0x80000u) >> 20) - DOWN;
-  return min(max(c, 0), TOP);
+// The nearest code to q in [0, 1 + 2^-23]: the last one stands for 1, and no clamp is needed.
+template <uint32_t DOWN>
+__device__ __forceinline__ uint32_t nearest(float q) {
+  return __builtin_elementwise_sub_sat((__builtin_bit_cast(uint32_t, q) + 0x80000u) >> 20, DOWN);
 }
 
 __device__ __forceinline__ void unpack4(uint32_t cm, uint32_t cv, float m_max, float v_max,
                                         float (&m)[4], float (&v)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    const int a = (cm >> (8 * i)) & 255;
-    const float f = number<kDownM>(a & 127) * m_max;
-    m[i] = a & 128 ? -f : f;
+    const float f = number<kDownM>((cm >> (8 * i)) & 127);
+    const uint32_t sign = (cm << (24 - 8 * i)) & 0x80000000u;
+    m[i] = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, f) | sign) * m_max;
     v[i] = number<kDownV>((cv >> (8 * i)) & 255) * v_max;
   }
 }
 
-// A block's maximum as it is stored, its reciprocal, and whether the block is finite.
-__device__ __forceinline__ bool block_top(int bits, float& top, float& inverse) {
-  if (bits >= 0x7f800000) {
-    top = __builtin_nanf("");
-    inverse = 0.0f;
-    return false;
-  }
-  top = bits < 0x00800000 ? 0.0f : __builtin_bit_cast(float, bits);
-  inverse = bits < 0x00800000 ? 0.0f : 1.0f / top;
-  return true;
-}
-
 template <int PT, int GT, int BITS, bool MASTER>
 __global__ __launch_bounds__(kWaves * 64) void adamw_kernel(const Args a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   // the tensor of this workgroup: the last that begins at or before it
+  static_assert(kMostTensors <= 128, "two lookups of 64 lanes");
   const int at0 = a.first_chunk[min(lane, a.count)], at1 = a.first_chunk[min(lane + 64, a.count)];
   const int chunk = (int)blockIdx.x;
-  const int t = __popcll(__ballot(lane < a.count && at0 <= chunk)) +
-                __popcll(__ballot(lane + 64 < a.count && at1 <= chunk)) - 1;
+  const int t = __builtin_amdgcn_readfirstlane(
+      __popcll(__ballot(lane < a.count && at0 <= chunk)) +
+      __popcll(__ballot(lane + 64 < a.count && at1 <= chunk)) - 1);
   float scale = 1.0f;
   if (a.grad_scale_at) {
     scale = *a.grad_scale_at;
@@ -183,7 +178,7 @@ __global__ __launch_bounds__(kWaves * 64) void adamw_kernel(const Args a) {
                a.step_at ? (int64_t)max(*a.step_at, 1) : a.step, k);
   void* const param = a.t[t].param;
   const void* const grad = a.t[t].grad;
-  const int64_t n = a.t[t].n, first = a.t[t].first_block;
+  const int64_t n = a.t[t].n, first = a.first_block + a.t[t].first_block;
   const int64_t e0 = ((int64_t)(chunk - a.first_chunk[t]) * kWaves + wave) *
                      (kWaveBlocks * kAdamBlock);
   float p[kWaveBlocks][4], g[kWaveBlocks][4], m[kWaveBlocks][4], v[kWaveBlocks][4];
@@ -207,63 +202,85 @@ __global__ __launch_bounds__(kWaves * 64) void adamw_kernel(const Args a) {
               a.s.m_max[block], a.s.v_max[block], m[j], v[j]);
     }
   }
+  // lane j and lane 4 + j: the maxima of block j's m and v, as bits
+  uint32_t tops = 0;
 #pragma unroll
   for (int j = 0; j < kWaveBlocks; j++) {
     const int64_t b = e0 + j * kAdamBlock;
     if (b >= n) continue;
     const int64_t e = b + lane * 4, left = n - e;
     const int64_t s = first * kAdamBlock + e;
-    int top_m = 0, top_v = 0;
+    uint32_t top_m = 0, top_v = 0;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      const bool inside = i < left;
       float x = g[j][i];
       if (a.grad_scale_at) x = x * scale;
       m[j][i] = k.b1 * m[j][i] + k.c1 * x;
       v[j][i] = k.b2 * v[j][i] + k.c2 * (x * x);
-      if (!inside) m[j][i] = v[j][i] = 0.0f;
-      top_m = max(top_m, __builtin_bit_cast(int, m[j][i]) & 0x7fffffff);
-      top_v = max(top_v, __builtin_bit_cast(int, v[j][i]) & 0x7fffffff);
-      const float step = m[j][i] / (sqrtf(v[j][i]) * k.rsq + k.eps);
-      p[j][i] = p[j][i] * k.decay - k.alpha * step;
     }
-    if (MASTER) {
-      if (left < 4) {
+    if (left < 4) {
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-          if (i >= left) p[j][i] = 0.0f;
-      }
-      store4<kAdamF32>(a.s.master, s, 4, p[j]);
+      for (int i = 0; i < 4; i++)
+        if (i >= left) p[j][i] = m[j][i] = v[j][i] = 0.0f;
     }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      top_m = max(top_m, __builtin_bit_cast(uint32_t, m[j][i]) & 0x7fffffffu);
+      top_v = max(top_v, __builtin_bit_cast(uint32_t, v[j][i]) & 0x7fffffffu);
+      // The hardware's square root and reciprocal are off by 2^-23 of the step taken (their IEEE
+      // forms took 1.3 times as long in all).  The root is of no subnormal number, which
+      // the instruction takes for 0; a NaN stays one.
+      const float root = __builtin_amdgcn_sqrtf(v[j][i] < 0x1p-126f ? 0x1p-126f : v[j][i]);
+      const float step = m[j][i] * __builtin_amdgcn_rcpf(__builtin_fmaf(root, k.rsq, k.eps));
+      p[j][i] = __builtin_fmaf(-k.alpha, step, p[j][i] * k.decay);
+    }
+    if (MASTER) store4<kAdamF32>(a.s.master, s, 4, p[j]);
     store4<PT>(param, e, left, p[j]);
     if (BITS == 32) {
       store4<kAdamF32>(a.s.m, s, 4, m[j]);
       store4<kAdamF32>(a.s.v, s, 4, v[j]);
     } else {
-      float max_m, inv_m, max_v, inv_v;
-      const bool fine_m = block_top(wave_top(top_m), max_m, inv_m);
-      const bool fine_v = block_top(wave_top(top_v), max_v, inv_v);
-      uint32_t cm = 0, cv = 0;
+      const uint32_t all_m = wave_top(top_m), all_v = wave_top(top_v);
+      tops = lane == j ? all_m : lane == kWaveBlocks + j ? all_v : tops;
+    }
+  }
+  if (BITS == 32) return;
+  // Every lane its maximum: as it is stored, and its reciprocal.  A block that is not finite has
+  // a NaN and codes 0, as a block of zeros has codes 0.
+  const bool small = tops < 0x00800000u, finite = tops < 0x7f800000u;
+  const float top = finite ? (small ? 0.0f : __builtin_bit_cast(float, tops)) : __builtin_nanf("");
+  const float inverse = finite && !small ? 1.0f / top : 0.0f;
+  const int64_t block = first + e0 / kAdamBlock;
+  if (lane < 2 * kWaveBlocks && e0 + lane % kWaveBlocks * kAdamBlock < n)
+    (lane < kWaveBlocks ? a.s.m_max : a.s.v_max)[block + lane % kWaveBlocks] = top;
+  const uint64_t numbers = __ballot(finite);
+#pragma unroll
+  for (int j = 0; j < kWaveBlocks; j++) {
+    const int64_t b = e0 + j * kAdamBlock;
+    if (b >= n) continue;
+    const int64_t s = first * kAdamBlock + b + lane * 4;
+    const int lane_v = kWaveBlocks + j;
+    const float inv_m = __builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, inverse), j));
+    const float inv_v = __builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, inverse), lane_v));
+    uint32_t cm = 0, cv = 0;
+    if (numbers >> j & 1)
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        if (fine_m) {
-          const int c = nearest<kDownM, 127>(fabsf(m[j][i]) * inv_m);
-          cm |= (uint32_t)(c ? c | (m[j][i] < 0.0f ? 128 : 0) : 0) << (8 * i);
-        }
-        if (fine_v) {
-          const float q = v[j][i] * inv_v;
-          const int c = nearest<kDownV, 255>(q);
-          cv |= (uint32_t)max(c, q > 0.0f ? 1 : 0) << (8 * i);
-        }
+        const uint32_t c = nearest<kDownM>(fabsf(m[j][i]) * inv_m);
+        const uint32_t sign = __builtin_bit_cast(uint32_t, m[j][i]) >> 31 << 7;
+        cm |= (c ? c | sign : 0u) << (8 * i);
       }
-      static_cast<uint32_t*>(a.s.m)[s / 4] = cm;
-      static_cast<uint32_t*>(a.s.v)[s / 4] = cv;
-      if (lane == 0) {
-        const int64_t block = first + b / kAdamBlock;
-        a.s.m_max[block] = max_m;
-        a.s.v_max[block] = max_v;
+    if (numbers >> lane_v & 1)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const float q = v[j][i] * inv_v;
+        // one at least where q is not 0
+        cv |= max(nearest<kDownV>(q), min(__builtin_bit_cast(uint32_t, q), 1u)) << (8 * i);
       }
-    }
+    static_cast<uint32_t*>(a.s.m)[s / 4] = cm;
+    static_cast<uint32_t*>(a.s.v)[s / 4] = cv;
   }
 }
 
@@ -338,11 +355,12 @@ hipError_t launch_adamw(const AdamTensor* tensors, int64_t count, int param_type
     while (i < count && a.count < kMostTensors && chunks < kMostChunks) {
       const int64_t n = tensors[i].n - done;
       const int64_t take = n < (kMostChunks - chunks) * kChunk ? n : (kMostChunks - chunks) * kChunk;
+      if (a.count == 0) a.first_block = block + done / kAdamBlock;
       if (take > 0) {
         const int64_t pw = param_type == kAdamF32 ? 4 : 2, gw = grad_type == kAdamF32 ? 4 : 2;
         a.t[a.count] = {static_cast<char*>(tensors[i].param) + done * pw,
-                        static_cast<const char*>(tensors[i].grad) + done * gw, take,
-                        block + done / kAdamBlock};
+                        static_cast<const char*>(tensors[i].grad) + done * gw, (uint32_t)take,
+                        (uint32_t)(block + done / kAdamBlock - a.first_block)};
         a.first_chunk[a.count++] = (int32_t)chunks;
         chunks += (take + kChunk - 1) / kChunk;
       }

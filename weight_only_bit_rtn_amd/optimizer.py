@@ -12,6 +12,8 @@ begins with a block.
 from __future__ import annotations
 
 import ctypes
+from array import array
+from itertools import chain
 
 import numpy as np
 
@@ -153,9 +155,9 @@ def adamw(params, grads, state: dict, lr, betas=(0.9, 0.999), eps: float = 1e-8,
     sizes = list(map(Tensor.numel, params))
     if sizes != list(map(Tensor.numel, grads)):
         raise ValueError("each gradient must have its parameter's size")
-    table = np.array((list(map(Tensor.data_ptr, params)), list(map(Tensor.data_ptr, grads)), sizes),
-                     np.int64).T.copy()
-    blocks = sum(-(-n // ADAMW_BLOCK) for n in sizes)
+    table = array("q", chain.from_iterable(zip(map(Tensor.data_ptr, params), map(Tensor.data_ptr, grads),
+                                               sizes)))
+    blocks = int((np.frombuffer(table, np.int64)[2::3] + (ADAMW_BLOCK - 1) >> 8).sum())
     n = blocks * ADAMW_BLOCK
     m = state["m"]
     if m.dtype is torch.uint8:
@@ -187,7 +189,7 @@ def adamw(params, grads, state: dict, lr, betas=(0.9, 0.999), eps: float = 1e-8,
     place = AdamwState(m.data_ptr(), state["v"].data_ptr(), *tops,
                        None if master is None else master.data_ptr())
     _lib()
-    _run("lowbit_adamw", None, (table.ctypes.data, count, p_kind, g_kind, bits,
+    _run("lowbit_adamw", None, (table.buffer_info()[0], count, p_kind, g_kind, bits,
                                 ctypes.addressof(place), ctypes.addressof(options)), dev)
     torch.autograd.graph.increment_version(params)
 
