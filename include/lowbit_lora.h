@@ -29,8 +29,10 @@
  *  - a token without an adapter: out_t = y_t, v_t = 0, dx_t = base_t, and it
  *    adds nothing to da and db.  An adapter without tokens has zero gradients.
  *    Nothing of such a token's x and dy, nor of an adapter without tokens, reaches
- *    any result, infinities and NaN included.
- *    The order of the sums is fixed by the sizes and the plan alone, so results
+ *    any result, infinities and NaN included.  An infinity elsewhere makes the results
+ *    that it enters infinities or NaN (its products with the parts of one value may have
+ *    different signs);
+ *  - the order of the sums is fixed by the sizes and the plan alone, so results
  *    repeat bit for bit.
  *
  * Layouts, ownership, alignment (16 bytes), streams and errors as in lowbit.h:
