@@ -8,6 +8,7 @@
 // and out (2 T (K + 2 N) bytes).
 #include "lora.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace lowbit {
@@ -302,21 +303,24 @@ Division divide(const LoraSizes& s) {
   Division d;
   d.tile = s.T <= 256 ? 16 : 64;
   d.tiles = lora_tiles(s.T, s.L, d.tile);
-  auto shares = [&](int64_t length, int64_t step, int64_t wanted, int& count, int& share) {
-    const int64_t most = (length + step - 1) / step;
-    int64_t n = (wanted + d.tiles - 1) / d.tiles;
-    if (n > most) n = most;
+  auto shares = [&](int64_t length, int64_t n, int& count, int& share) {
     share = (int)(((length + n - 1) / n + 63) / 64 * 64);
     count = (int)((length + share - 1) / share);
   };
-  if (d.tile == 16)
-    shares(s.K, 512, 256, d.splits, d.k_share);
-  else
-    shares(s.K, 256, 512, d.splits, d.k_share);
+  auto over_tiles = [&](int64_t workgroups) { return (workgroups + d.tiles - 1) / d.tiles; };
+  // Shares of K: a step for every wave at the least, and few, as every workgroup of the expansion
+  // adds them up again (us of both kernels with 8 / 4 at most: 1500 tokens of 8192x8192, 128 ranks
+  // 85 / 71, 700 of 11008x4096, 64 ranks 31 / 29; in small tiles 200 of 4096x8192, 64 ranks 13.8 / 15.3).
+  const int64_t step = d.tile == 16 ? 512 : 256;
+  int64_t n = over_tiles(512);
+  if (n > s.K / (4 * step)) n = std::max(s.K / (4 * step), over_tiles(256));
+  n = std::max<int64_t>(1, std::min({n, (s.K + step - 1) / step, d.tile == 16 ? (int64_t)8 : 4}));
+  shares(s.K, n, d.splits, d.k_share);
   // Small tiles: many short workgroups (64 tokens of 64 adapters, 11008 outputs, 16 ranks: 8.4 us
   // with 1024, 9.7 with 512).  Large ones: as many as the card holds at once (1024 / 512 / 256 of
   // them: 8192x12288, 64 ranks 101 / 92 / 127; 4096x4096, 128 ranks, one to a CU, 84 / 58 / 42).
-  shares(s.N, 256, d.tile == 16 ? 1024 : s.R > 64 ? 256 : 512, d.ranges, d.n_share);
+  n = std::min(over_tiles(d.tile == 16 ? 1024 : s.R > 64 ? 256 : 512), (s.N + 255) / 256);
+  shares(s.N, n, d.ranges, d.n_share);
   return d;
 }
 

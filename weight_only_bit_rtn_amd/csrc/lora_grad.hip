@@ -595,12 +595,14 @@ Division divide(const LoraSizes& s) {
   // dx: two workgroups to a CU at once
   const int64_t ranges = 512 / ((s.T + kTile - 1) / kTile);
   d.dx_cols = ranges < 1 ? d.k_cols : (int)((d.k_cols + ranges - 1) / ranges);
-  // chunks as many as the card holds workgroups at once, of 256 tokens at least
+  // chunks as many as the card holds workgroups at once, of 128 tokens at least (us of the
+  // sums with 256 / 128: 400 tokens 4096x4096, 16 ranks 12.5 / 8.6; 700 of 11008x4096, 64 ranks
+  // 20.1 / 16.3, where the join takes 1.9 more)
   const int64_t cols = (d.k_cols + d.n_cols) * ((s.R + 63) / 64);
   const int64_t held = s.R > 32 ? 256 : 512;
   const int64_t wanted = held > cols ? held / cols : 1;
   int64_t chunk = ((s.T + wanted - 1) / wanted + kTile - 1) / kTile * kTile;
-  if (chunk < 256) chunk = 256;
+  if (chunk < 128) chunk = 128;
   d.chunk = (int)chunk;
   d.chunks = lora_tiles(s.T, s.L, d.chunk);
   d.shares = s.T > d.chunk ? 2 * s.T / d.chunk + 1 : 0;

@@ -19,8 +19,8 @@ __global__ __launch_bounds__(kPlanWaves * 64) void lora_plan_kernel(
     const int32_t* __restrict__ ids, int64_t T, int L, int bits, int32_t* __restrict__ order,
     int32_t* __restrict__ starts) {
   extern __shared__ int place[];  // [kPlanWaves][L + 1]: counts, then next places
-  __shared__ int wave_total[kPlanWaves];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, keys = L + 1;
+  __shared__ int wave_total[kPlanWaves], nobody[kPlanWaves][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_of_group(), keys = L + 1;
   for (int i = tid; i < kPlanWaves * keys; i += kPlanWaves * 64) place[i] = 0;
   __syncthreads();
   const int64_t run = (T + kPlanWaves * 64 - 1) / (kPlanWaves * 64) * 64;
@@ -29,23 +29,34 @@ __global__ __launch_bounds__(kPlanWaves * 64) void lora_plan_kernel(
   // lanes with this lane's id, of the lanes that have a token
   auto same_ids = [&](int key, bool has) {
     uint64_t same = __ballot(has);
+    // most steps are one request's prompt
+    if (__ballot(has && key != __builtin_amdgcn_readfirstlane(key)) == 0) return has ? same : 0;
     for (int b = 0; b < bits; b++) {
       const uint64_t ones = __ballot((key >> b) & 1);
       same &= (key >> b) & 1 ? ones : ~ones;
     }
     return same;
   };
-  auto key_of = [&](int64_t t) {
-    if (t >= t1) return L;
-    const int id = ids[t];
-    return id >= 0 && id < L ? id : L;
+  auto key_of = [&](int64_t t) {  // the last token's again beyond the run: no condition on a load
+    const int id = ids[min(t, T - 1)];
+    return (uint32_t)id < (uint32_t)L ? id : L;
   };
   const uint64_t below = ((uint64_t)1 << lane) - 1;
-  for (int64_t t = t0; t < t1; t += 64) {
-    const bool has = t + lane < t1;
-    const int key = key_of(t + lane);
-    const uint64_t same = same_ids(key, has);
-    if (has && !(same & below)) mine[key] += __popcll(same);
+  // eight steps' ids are under way at a time
+  constexpr int kAhead = 8;
+  for (int64_t t = t0; t < t1; t += 64 * kAhead) {
+    int key[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; i++) key[i] = key_of(t + i * 64 + lane);
+#pragma unroll
+    for (int i = 0; i < kAhead; i++) {
+      if (t + i * 64 >= t1) break;
+      const bool has = t + i * 64 + lane < t1;
+      // additions to one place come one after the other: one for all of a prompt's
+      const bool one = __ballot(has && key[i] != __builtin_amdgcn_readfirstlane(key[i])) == 0;
+      const int n = one ? (int)__popcll(__ballot(has)) : 1;
+      if (one ? lane == 0 : has) atomicAdd(&mine[key[i]], n);
+    }
   }
   __syncthreads();
   // places: all of an adapter's tokens before the next one's, wave by wave
@@ -78,15 +89,28 @@ __global__ __launch_bounds__(kPlanWaves * 64) void lora_plan_kernel(
   if (tid < L) hand_out(tid, first);
   if (tid == 0) hand_out(L, all);
   __syncthreads();
-  for (int64_t t = t0; t < t1; t += 64) {
-    const bool has = t + lane < t1;
-    const int key = key_of(t + lane);
-    const uint64_t same = same_ids(key, has);
-    const int leader = same ? __ffsll((unsigned long long)same) - 1 : 0;
-    int at = 0;
-    if (has && lane == leader) at = atomicAdd(&mine[key], (int)__popcll(same));
-    at = __shfl(at, leader, kWave) + (int)__popcll(same & below);
-    if (has) order[at] = (int32_t)(t + lane);
+  // An adapter's first lane of 64 takes the places of all; the other lanes' additions go to
+  // nobody, so that eight steps' may be under way.
+  for (int64_t t = t0; t < t1; t += 64 * kAhead) {
+    int key[kAhead], at[kAhead];
+    uint64_t same[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; i++) key[i] = key_of(t + i * 64 + lane);
+#pragma unroll
+    for (int i = 0; i < kAhead; i++) {
+      if (t + i * 64 >= t1) break;
+      same[i] = same_ids(key[i], t + i * 64 + lane < t1);
+      const bool first_of = (same[i] >> lane & 1) && !(same[i] & below);
+      at[i] = atomicAdd(first_of ? &mine[key[i]] : &nobody[wave][lane], (int)__popcll(same[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; i++) {
+      if (t + i * 64 >= t1) break;
+      const int first_of = same[i] ? __ffsll((unsigned long long)same[i]) - 1 : 0;
+      const int from = __shfl(at[i], first_of, kWave);
+      if (t + i * 64 + lane < t1)
+        order[from + (int)__popcll(same[i] & below)] = (int32_t)(t + i * 64 + lane);
+    }
   }
 }
 
