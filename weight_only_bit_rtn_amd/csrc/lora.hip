@@ -127,12 +127,15 @@ struct UpArgs {
   float* v;
 };
 
-// A wave's step is 64 outputs.  The next step's rows of b and y are under way while one is
-// multiplied.  Results pass through LDS too, in fp32, 16 tokens at a time: eight lanes then
-// hold the 64 outputs of one token as y's rows lie.
+// A wave's step is 64 outputs, or 32 where there are more than 64 ranks, so that two
+// workgroups fit a CU (1500 tokens of 8192x8192, 128 ranks: 53 -> 31 us).  The next step's rows
+// of b and y are under way while one is multiplied.  Results pass through LDS too, in fp32,
+// 16 tokens at a time: eight (four) lanes then hold the outputs of one token as y's rows lie.
+template <int RB>
+constexpr int kOut = RB < 8 ? 64 : 32;
 template <int RB>
 constexpr int up_wave_bytes() {
-  constexpr int b = 64 * RB * 32, result = 16 * 68 * 4;
+  constexpr int b = kOut<RB> * RB * 32, result = 16 * (kOut<RB> + 4) * 4;
   return b > result ? b : result;
 }
 template <int RB, int TB>
@@ -140,9 +143,12 @@ constexpr int up_bytes() {
   return TB * 16 * ((RB * 32 + 8) * 2 + 4) + kLoraWaves * up_wave_bytes<RB>();
 }
 template <bool BF, int RB, int TB>
-__global__ __launch_bounds__(kLoraWaves * 64, RB < 8 ? 2 : 1) void lora_up_kernel(const UpArgs g) {
-  constexpr int TILE = 16 * TB, PITCH = RB * 32 + 8, STEP = kLoraWaves * 64;
+__global__ __launch_bounds__(kLoraWaves * 64, 2) void lora_up_kernel(const UpArgs g) {
+  constexpr int TILE = 16 * TB, PITCH = RB * 32 + 8, OUT = kOut<RB>, STEP = kLoraWaves * OUT;
   constexpr int C = Ranks<RB>::kChunks, CHUNKS = RB * 2;
+  constexpr int LOADS = OUT * CHUNKS / 64;             // of b's rows, a lane
+  constexpr int LANES = OUT / 8, ROWS = 64 / LANES;    // lanes of a row of y, rows of a load
+  constexpr int ROUNDS = 16 / ROWS;                    // loads of 16 tokens
   extern __shared__ __align__(16) char lds[];
   uint16_t(*const parts)[PITCH] = reinterpret_cast<uint16_t(*)[PITCH]>(lds);
   int* const exponent = reinterpret_cast<int*>(lds + TILE * PITCH * 2);
@@ -153,51 +159,55 @@ __global__ __launch_bounds__(kLoraWaves * 64, RB < 8 ? 2 : 1) void lora_up_kerne
   const bool in_place = g.y == g.out;
   if (none && in_place && !g.v) return;
   const int lane = threadIdx.x & 63, wave = wave_of_group();
-  const int i16 = lane & 15, h = lane >> 4, row = lane >> 3, chunk = lane & 7;
+  const int i16 = lane & 15, h = lane >> 4, row = lane / LANES, chunk = lane % LANES;
   char* const mine = lds + TILE * (PITCH * 2 + 4) + wave * up_wave_bytes<RB>();
-  uint16_t* const sb = reinterpret_cast<uint16_t*>(mine);             // [64][CHUNKS] chunks
-  float(*const result)[68] = reinterpret_cast<float(*)[68]>(mine);    // [16], after b is read
+  uint16_t* const sb = reinterpret_cast<uint16_t*>(mine);  // [OUT][CHUNKS] chunks
+  float(*const result)[OUT + 4] = reinterpret_cast<float(*)[OUT + 4]>(mine);  // [16], after b is read
   const int64_t N = p.N;
-  int64_t at[TILE / 8];  // of row 8 q + lane / 8, this lane's eight outputs
+  int64_t at[TILE / ROWS];  // of token ROWS q + row, this lane's eight outputs
 #pragma unroll
-  for (int q = 0; q < TILE / 8; q++)
-    at[q] = token_at(p.order, p.T, tile.begin + min(q * 8 + row, tile.count - 1)) * N + chunk * 8;
+  for (int q = 0; q < TILE / ROWS; q++)
+    at[q] = token_at(p.order, p.T, tile.begin + min(q * ROWS + row, tile.count - 1)) * N + chunk * 8;
   const int n1 = min((int)(blockIdx.y + 1) * g.n_share, p.N);
-  // b's 64 rows lie in one piece: 16-byte chunk 64 q + lane of it, and where it goes.
+  // b's rows lie in one piece: 16-byte chunk 64 q + lane of it (the last one again beyond), and
+  // where it goes.
   // Chunk c of row n is in slot c ^ (n / (8 / CHUNKS)) % CHUNKS, as in row_slot().
-  const int per_row = p.R / 8, count = per_row * 64;
+  const int per_row = p.R / 8;
   auto slot = [&](int n, int c) {
     constexpr int SHIFT = RB == 1 ? 3 : RB == 2 ? 2 : 1;
     return n * RB * 16 + ((c ^ ((n >> SHIFT) & (CHUNKS - 1))) << 3);
   };
-  int place[CHUNKS];
+  auto item = [&](int q) {
+    return OUT == 64 ? q * 64 + lane : min(q * 64 + lane, per_row * OUT - 1);
+  };
+  int place[LOADS];
 #pragma unroll
-  for (int q = 0; q < CHUNKS; q++) {
-    const int i = q * 64 + lane;
-    place[q] = slot(i / per_row % 64, i % per_row);
+  for (int q = 0; q < LOADS; q++) {
+    const int i = item(q);
+    place[q] = slot(i / per_row % OUT, i % per_row);
   }
-  us8_t vb[CHUNKS], had[TILE / 8], ahead[TILE / 8];
+  us8_t vb[LOADS], had[TILE / ROWS], ahead[TILE / ROWS];
   const uint16_t* const b = p.b + (int64_t)(none ? 0 : tile.l) * N * p.R;
   auto load_b = [&](int n0) {
 #pragma unroll
-    for (int q = 0; q < CHUNKS; q++)
-      if (q < per_row)
-        vb[q] = *reinterpret_cast<const us8_t*>(b + (int64_t)n0 * p.R + (q * 64 + lane) * 8);
+    for (int q = 0; q < LOADS; q++)
+      if (q * 64 < per_row * OUT)
+        vb[q] = *reinterpret_cast<const us8_t*>(b + (int64_t)n0 * p.R + item(q) * 8);
   };
   // without a y: read what out holds, to no one's use
   const uint16_t* const y = g.y ? g.y : g.out;
-  auto load_y = [&](us8_t(&to)[TILE / 8], int n0) {
+  auto load_y = [&](us8_t(&to)[TILE / ROWS], int n0) {
 #pragma unroll
-    for (int q = 0; q < TILE / 8; q++) to[q] = load8(y + at[q] + n0);
+    for (int q = 0; q < TILE / ROWS; q++) to[q] = load8(y + at[q] + n0);
   };
-  us8_t fb[4][C];
+  us8_t fb[OUT / 16][C];
   auto stage_b = [&] {
 #pragma unroll
-    for (int q = 0; q < CHUNKS; q++)
-      if (q < per_row) *reinterpret_cast<us8_t*>(sb + place[q]) = vb[q];
+    for (int q = 0; q < LOADS; q++)
+      if (q * 64 < per_row * OUT) *reinterpret_cast<us8_t*>(sb + place[q]) = vb[q];
     wave_lds_order();
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < OUT / 16; i++)
 #pragma unroll
       for (int c = 0; c < C; c++) {
         const int r = Ranks<RB>::of(c, h);
@@ -206,16 +216,17 @@ __global__ __launch_bounds__(kLoraWaves * 64, RB < 8 ? 2 : 1) void lora_up_kerne
       }
     wave_lds_order();
   };
-  // the 64 outputs of token block j, whose y and places are given, `left` of a lane's eight inside
+  // the step's outputs of token block j, whose y and places are given, `left` of a lane's eight inside
   auto finish = [&](int j, int n0, const us8_t* y2, const int64_t* at2, auto whole, int left) {
-    f4_t acc[4] = {};
+    f4_t acc[OUT / 16] = {};
     multiply_parts<BF, RB>(fb, parts[j * 16 + i16], h, acc);
 #pragma unroll
-    for (int i = 0; i < 4; i++) *reinterpret_cast<f4_t*>(&result[i16][i * 16 + h * 4]) = acc[i];
+    for (int i = 0; i < OUT / 16; i++)
+      *reinterpret_cast<f4_t*>(&result[i16][i * 16 + h * 4]) = acc[i];
     wave_lds_order();
 #pragma unroll
-    for (int q = 0; q < 2; q++) {
-      const int t = q * 8 + row;
+    for (int q = 0; q < ROUNDS; q++) {
+      const int t = q * ROWS + row;
       const f4_t lo = *reinterpret_cast<const f4_t*>(&result[t][chunk * 8]);
       const f4_t hi = *reinterpret_cast<const f4_t*>(&result[t][chunk * 8 + 4]);
       const int e = BF ? 0 : exponent[j * 16 + t];
@@ -238,9 +249,9 @@ __global__ __launch_bounds__(kLoraWaves * 64, RB < 8 ? 2 : 1) void lora_up_kerne
     }
     wave_lds_order();
   };
-  int n0 = blockIdx.y * g.n_share + wave * 64;
+  int n0 = blockIdx.y * g.n_share + wave * OUT;
   // the first step's loads are under way while v's shares are added up
-  if (n0 + 64 <= n1) {
+  if (n0 + OUT <= n1) {
     load_y(had, n0);
     load_b(n0);
   }
@@ -256,34 +267,34 @@ __global__ __launch_bounds__(kLoraWaves * 64, RB < 8 ? 2 : 1) void lora_up_kerne
       none ? 0.0f : p.scales[tile.l], tile.count, p.R, parts, exponent);
   __syncthreads();
   if (none && in_place) return;
-  for (; n0 + 64 <= n1; n0 += STEP) {
+  for (; n0 + OUT <= n1; n0 += STEP) {
     stage_b();
-    if (n0 + STEP + 64 <= n1) {
+    if (n0 + STEP + OUT <= n1) {
       load_y(ahead, n0 + STEP);
       load_b(n0 + STEP);
     }
 #pragma unroll
     for (int j = 0; j < TB; j++) {
       if (j * 16 >= tile.count) break;
-      finish(j, n0, had + j * 2, at + j * 2, std::true_type(), 8);
+      finish(j, n0, had + j * ROUNDS, at + j * ROUNDS, std::true_type(), 8);
     }
 #pragma unroll
-    for (int q = 0; q < TILE / 8; q++) had[q] = ahead[q];
+    for (int q = 0; q < TILE / ROWS; q++) had[q] = ahead[q];
   }
-  if (n0 < n1) {  // the last outputs, fewer than 64
+  if (n0 < n1) {  // the last outputs, fewer than a step's
     const int left = n1 - n0 - chunk * 8, most = (n1 - n0) * per_row - 1;
 #pragma unroll
-    for (int q = 0; q < CHUNKS; q++)  // beyond the last row: for outputs that nobody stores
-      if (q < per_row)
-        vb[q] = *reinterpret_cast<const us8_t*>(b + (int64_t)n0 * p.R + min(q * 64 + lane, most) * 8);
+    for (int q = 0; q < LOADS; q++)  // beyond the last row: for outputs that nobody stores
+      if (q * 64 < per_row * OUT)
+        vb[q] = *reinterpret_cast<const us8_t*>(b + (int64_t)n0 * p.R + min(item(q), most) * 8);
     stage_b();
 #pragma unroll 1
     for (int j = 0; j * 16 < tile.count; j++) {
-      int64_t at2[2];
-      us8_t y2[2];
+      int64_t at2[ROUNDS];
+      us8_t y2[ROUNDS];
 #pragma unroll
-      for (int q = 0; q < 2; q++) {
-        const int t = min(j * 16 + q * 8 + row, tile.count - 1);
+      for (int q = 0; q < ROUNDS; q++) {
+        const int t = min(j * 16 + q * ROWS + row, tile.count - 1);
         at2[q] = token_at(p.order, p.T, tile.begin + t) * N + chunk * 8;
         y2[q] = load8(y + at2[q] + n0, left);
       }
@@ -319,7 +330,7 @@ Division divide(const LoraSizes& s) {
   // Small tiles: many short workgroups (64 tokens of 64 adapters, 11008 outputs, 16 ranks: 8.4 us
   // with 1024, 9.7 with 512).  Large ones: as many as the card holds at once (1024 / 512 / 256 of
   // them: 8192x12288, 64 ranks 101 / 92 / 127; 4096x4096, 128 ranks, one to a CU, 84 / 58 / 42).
-  n = std::min(over_tiles(d.tile == 16 ? 1024 : s.R > 64 ? 256 : 512), (s.N + 255) / 256);
+  n = std::min(over_tiles(d.tile == 16 ? 1024 : 512), (s.N + 255) / 256);
   shares(s.N, n, d.ranges, d.n_share);
   return d;
 }

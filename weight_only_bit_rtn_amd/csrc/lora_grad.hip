@@ -562,7 +562,7 @@ __global__ __launch_bounds__(256) void lora_join_kernel(const JoinArgs g) {
   join_part(g, blockIdx.x);
 }
 template <bool BF, int RB>
-__global__ __launch_bounds__(kGradWaves * 64) void lora_finish_kernel(const SpreadArgs g,
+__global__ __launch_bounds__(kGradWaves * 64, 2) void lora_finish_kernel(const SpreadArgs g,
                                                                       const JoinArgs join) {
   extern __shared__ __align__(16) char lds[];
   const int ranges = (g.k_cols + g.dx_cols - 1) / g.dx_cols;
