@@ -137,7 +137,7 @@ def test_workspace_sizes(lw):
         need, grad = lw.lora_workspace_bytes(T, N, K, R, L), lw.lora_grad_workspace_bytes(T, N, K, R, L)
         # one share of every token's coefficients at the least, and no more than 64, or of N's 4
         assert 4 * T * R <= need <= 64 * 4 * T * R
-        assert 4 * T * R <= grad <= 4 * 4 * T * R + 4 * R * (K + N) * (2 * T / 256 + 1)
+        assert 4 * T * R <= grad <= 4 * 4 * T * R + 4 * R * (K + N) * (2 * T / 128 + 1)
         if need < 1 << 40:
             assert lora(lw, T=T, N=N, K=K, R=R, L=L, size=need - 1) == ARG
             assert lora_grad(lw, T=T, N=N, K=K, R=R, L=L, size=grad - 1) == ARG

@@ -104,29 +104,32 @@ def lora_plan(ids, L: int, out: dict | None = None) -> dict:
     return {"order": order, "starts": starts}
 
 
-def _adapters(x, a, b, scales, plan, name: str):
-    """(element type, T, N, K, R, L, device) and the shared pointers, checked."""
-    torch = _torch()
-    kind = _float_type(x, name)
-    dtype = x.dtype
-    _check_tensor(x, name, dtype)
-    T, K = x.shape
-    dev = x.device
-    if not (isinstance(a, torch.Tensor) and isinstance(b, torch.Tensor)):
-        raise TypeError("a and b must be torch.Tensors")
-    if a.dim() != 3 or b.dim() != 3:
-        raise ValueError("a and b must have 3 dimensions")
-    L, R, _ = a.shape
-    N = b.shape[1]
-    _check_tensor(a, "a", dtype, dev, (L, R, K))
-    _check_tensor(b, "b", dtype, dev, (L, N, R))
-    _check_tensor(scales, "scales", torch.float32, dev, (L,))
-    order, starts = plan["order"], plan["starts"]
-    _check_tensor(order, "order", torch.int32, dev, (T,))
-    _check_tensor(starts, "starts", torch.int32, dev, (L + 1,))
-    shared = (order.data_ptr(), starts.data_ptr(), a.data_ptr(), b.data_ptr(), scales.data_ptr(),
-              L, R, N, K)
-    return kind, T, N, K, R, L, dev, shared
+def _fine(device, *tensors) -> None:
+    """Checks (tensor, name, type, shape) one after the other: dense GPU tensors on ``device`` whose
+    gradients nobody waits for.  Decoding takes some microseconds, so a call's tensors are looked at in
+    one loop, and spelled out by ``_check_tensor`` only when one is wrong."""
+    index = device.index
+    recorded = _torch().is_grad_enabled()
+    for t, name, dtype, shape in tensors:
+        try:
+            if (t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
+                    and not (recorded and t.requires_grad)):
+                continue
+        except AttributeError:
+            pass
+        _check_tensor(t, name, dtype, device, shape)
+
+
+def _sizes(x, a, b):
+    """T, N, K, R, L from the tensors' shapes."""
+    try:
+        (T, K), (L, R, _), (_, N, _) = x.shape, a.shape, b.shape
+        return T, N, K, R, L
+    except (AttributeError, ValueError):
+        torch = _torch()
+        if not all(isinstance(t, torch.Tensor) for t in (x, a, b)):
+            raise TypeError("x, a and b must be torch.Tensors") from None
+        raise ValueError("x must have 2 dimensions, a and b 3") from None
 
 
 def _call(name: str, sizes, args, device) -> None:
@@ -159,21 +162,30 @@ def lora(x, a, b, scales, plan, y=None, out=None, save: bool = False):
     Without ``y`` the adapters' part alone.  ``out``: a tensor to write into, y itself
     allowed.  ``save``: (out, v), v = a_l x in fp32 [T][R], which ``lora_grad`` takes."""
     torch = _torch()
-    kind, T, N, K, R, L, dev, shared = _adapters(x, a, b, scales, plan, "x")
+    kind = _float_type(x, "x")
+    T, N, K, R, L = _sizes(x, a, b)
+    dtype, dev = x.dtype, x.device
+    order, starts = plan["order"], plan["starts"]
+    if not x.is_cuda:
+        raise ValueError("x must live on the GPU")
+    _fine(dev, (x, "x", dtype, (T, K)), (a, "a", dtype, (L, R, K)), (b, "b", dtype, (L, N, R)),
+          (scales, "scales", torch.float32, (L,)), (order, "order", torch.int32, (T,)),
+          (starts, "starts", torch.int32, (L + 1,)))
     if y is not None:
-        _check_tensor(y, "y", x.dtype, dev, (T, N))
+        _fine(dev, (y, "y", dtype, (T, N)))
     if out is None:
-        o = torch.empty((T, N), dtype=x.dtype, device=dev) if y is None else torch.empty_like(y)
+        o = torch.empty((T, N), dtype=dtype, device=dev) if y is None else torch.empty_like(y)
     else:
-        o = _out(out, "out", (T, N), x.dtype, dev)
-        inputs = (x, a, b, scales, plan["order"], plan["starts"])
+        o = _out(out, "out", (T, N), dtype, dev)
+        inputs = (x, a, b, scales, order, starts)
         if y is not None and y.data_ptr() != o.data_ptr():
             inputs += (y,)
         _apart(o, "out", *inputs)
     v = torch.empty((T, R), dtype=torch.float32, device=dev) if save else None
     _call("lowbit_lora", (T, N, K, R, L),
-         (x.data_ptr(), kind, T, *shared, None if y is None else y.data_ptr(), o.data_ptr(),
-          v.data_ptr() if save else None), dev)
+          (x.data_ptr(), kind, T, order.data_ptr(), starts.data_ptr(), a.data_ptr(), b.data_ptr(),
+           scales.data_ptr(), L, R, N, K, None if y is None else y.data_ptr(), o.data_ptr(),
+           v.data_ptr() if save else None), dev)
     return (o, v) if save else o
 
 
@@ -184,22 +196,30 @@ def lora_grad(dy, x, v, a, b, scales, plan, dx=None, out=None):
     written, ``dx`` itself allowed.  da [L][R][K] and db [L][N][R] are fp32, the sums as they
     are; an adapter without tokens has zeros."""
     torch = _torch()
-    kind, T, N, K, R, L, dev, shared = _adapters(x, a, b, scales, plan, "x")
-    _check_tensor(dy, "dy", x.dtype, dev, (T, N))
-    _check_tensor(v, "v", torch.float32, dev, (T, R))
+    kind = _float_type(x, "x")
+    T, N, K, R, L = _sizes(x, a, b)
+    dtype, dev = x.dtype, x.device
+    order, starts = plan["order"], plan["starts"]
+    if not x.is_cuda:
+        raise ValueError("x must live on the GPU")
+    _fine(dev, (x, "x", dtype, (T, K)), (a, "a", dtype, (L, R, K)), (b, "b", dtype, (L, N, R)),
+          (scales, "scales", torch.float32, (L,)), (order, "order", torch.int32, (T,)),
+          (starts, "starts", torch.int32, (L + 1,)), (dy, "dy", dtype, (T, N)),
+          (v, "v", torch.float32, (T, R)))
     if dx is not None:
-        _check_tensor(dx, "dx", x.dtype, dev, (T, K))
+        _fine(dev, (dx, "dx", dtype, (T, K)))
     if out is None:
         o = torch.empty_like(x)
     else:
-        o = _out(out, "out", (T, K), x.dtype, dev)
-        inputs = (dy, x, v, a, b, scales, plan["order"], plan["starts"])
+        o = _out(out, "out", (T, K), dtype, dev)
+        inputs = (dy, x, v, a, b, scales, order, starts)
         if dx is not None and dx.data_ptr() != o.data_ptr():
             inputs += (dx,)
         _apart(o, "out", *inputs)
     da = torch.empty((L, R, K), dtype=torch.float32, device=dev)
     db = torch.empty((L, N, R), dtype=torch.float32, device=dev)
     _call("lowbit_lora_grad", (T, N, K, R, L),
-         (dy.data_ptr(), x.data_ptr(), v.data_ptr(), kind, T, *shared,
-          None if dx is None else dx.data_ptr(), o.data_ptr(), da.data_ptr(), db.data_ptr()), dev)
+          (dy.data_ptr(), x.data_ptr(), v.data_ptr(), kind, T, order.data_ptr(), starts.data_ptr(),
+           a.data_ptr(), b.data_ptr(), scales.data_ptr(), L, R, N, K,
+           None if dx is None else dx.data_ptr(), o.data_ptr(), da.data_ptr(), db.data_ptr()), dev)
     return o, da, db
