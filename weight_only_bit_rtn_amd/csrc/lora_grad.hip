@@ -23,7 +23,7 @@ constexpr int kCols = kGradWaves * 128;  // columns of a workgroup of dx, da or 
 // ---------------------------------------------------------------------------
 // u = b^T dy
 // ---------------------------------------------------------------------------
-constexpr int kBackWaves = 4;
+constexpr int kBackWaves = 8;
 constexpr int kMostSplits = 4;  // shares of u: the sums hold them in registers
 
 struct BackArgs {
@@ -45,7 +45,7 @@ constexpr int back_bytes() {
   return stage > reduce ? stage : reduce;
 }
 template <bool BF, int RB>
-__global__ __launch_bounds__(kBackWaves * 64, 2) void lora_back_kernel(const BackArgs g) {
+__global__ __launch_bounds__(kBackWaves * 64) void lora_back_kernel(const BackArgs g) {
   constexpr int TB = kTile / 16, TURN = 64 + 8, RANKS = RB * 16;
   extern __shared__ __align__(16) char lds[];
   const LoraArgs& p = g.p;
@@ -585,7 +585,10 @@ Division divide(const LoraSizes& s) {
   Division d;
   d.tiles = lora_tiles(s.T, s.L, kTile);
   const int64_t most = (s.N + kBackWaves * 64 - 1) / (kBackWaves * 64);
-  int64_t n = (512 + d.tiles - 1) / d.tiles;
+  // shares of N: the sums read them all again (us of u / sums, 64 ranks: 8192 tokens of 12288x12288
+  // with 4 of four waves, 2 of eight, 1: 66 / 120, 74 / 107, 91 / 106; 4096 of 4096x4096 with 4 and 2:
+  // 20 / 37, 21 / 33)
+  int64_t n = (192 + d.tiles - 1) / d.tiles;
   if (n > kMostSplits) n = kMostSplits;
   if (n > most) n = most;
   d.n_share = (int)(((s.N + n - 1) / n + 63) / 64 * 64);
