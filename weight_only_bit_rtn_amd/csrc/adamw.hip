@@ -4,9 +4,10 @@
 //   p' = p (1 - lr wd) - lr / (1 - beta1^t) m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
 //
 // Elementwise, so bound by HBM: fp32 parameters and gradients with 8-bit moments
-// move 16 bytes a value, with 32-bit ones 28.  The tensors' addresses travel as
+// move 16 bytes a value, with 32-bit ones 28: 448 tensors of 112 thousand values 172 us in four
+// launches (4.7 TB/s), 100 million bf16 values with an fp32 copy 305 us (5.3).  The tensors' addresses travel as
 // kernel arguments, kMostTensors to a launch, so a step needs no table in device
-// memory and can be captured.  A wave holds one block of 256 values at a time, four
+// memory and can be captured.  A wave holds one block of 256 values, four
 // to a lane: 16-byte loads of fp32, and the block's maximum stays within the wave.
 //
 // Every operation on the moments is rounded by itself (no contraction): their
@@ -227,8 +228,8 @@ __global__ __launch_bounds__(kWaves * 64) void adamw_kernel(const Args a) {
     for (int i = 0; i < 4; i++) {
       top_m = max(top_m, __builtin_bit_cast(uint32_t, m[j][i]) & 0x7fffffffu);
       top_v = max(top_v, __builtin_bit_cast(uint32_t, v[j][i]) & 0x7fffffffu);
-      // The hardware's square root and reciprocal are off by 2^-23 of the step taken (their IEEE
-      // forms took 1.3 times as long in all).  The root is of no subnormal number, which
+      // The hardware's square root and reciprocal are off by 2^-23 of the step taken (with
+      // their IEEE forms the 100 million values took 330 us).  The root is of no subnormal number, which
       // the instruction takes for 0; a NaN stays one.
       const float root = __builtin_amdgcn_sqrtf(v[j][i] < 0x1p-126f ? 0x1p-126f : v[j][i]);
       const float step = m[j][i] * __builtin_amdgcn_rcpf(__builtin_fmaf(root, k.rsq, k.eps));

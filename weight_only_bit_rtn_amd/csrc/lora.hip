@@ -5,7 +5,11 @@
 // one adapter and a share of K, and leaves v's share in the workspace.  The second
 // adds the shares up, and expands over N: it takes a tile and a range of outputs.
 // Bound by HBM: for few tokens the adapters (2 R (K + N) bytes each), for many x, y
-// and out (2 T (K + 2 N) bytes).
+// and out (2 T (K + 2 N) bytes).  8192 tokens of 12288x12288, 64 ranks: contraction 63 us
+// (39 where the last call's outputs are not on their way to HBM, 5.1 TB/s), expansion 92
+// (4.4 TB/s; 16 ranks 75, 5.4).  64 tokens of 64 adapters of 11008x4096, 16 ranks: 5.0 + 8.4 us.
+// Both at once, each workgroup of the expansion contracting for itself, took 9.1 us against
+// 3.7 + 4.7 for one token of 4096x4096 and 13.6 against 13.4 for these 64.
 #include "lora.h"
 
 #include <algorithm>
