@@ -487,3 +487,46 @@ def test_two_calls_at_once(lw):
                 got[i] = (*lw.lora(c.x, *c.pools(), y=c.y, save=True), *lw.lora_grad(c.dy, c.x, c.v, *c.pools(), dx=c.base))
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for w, g in zip(want, got) for p, q in zip(w, g))
+
+
+def test_first_calls_captured():
+    """In a new process, the very first calls go into a graph."""
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    print("[adapters] first calls captured", flush=True)
+    code = """
+import torch, sys
+sys.path.insert(0, %r)
+import weight_only_bit_rtn_amd as lw
+g = torch.Generator(device="cuda").manual_seed(0)
+sets = []
+for T, R in ((1, 8), (300, 64), (300, 128)):
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda").half()
+    sets.append((n(T, 256), n(T, 200), n(2, R, 256), n(2, 200, R), torch.ones(2, device="cuda"),
+                 (torch.arange(T, device="cuda") %% 3 - 1).int()))
+def run(x, y, a, b, s, ids):
+    plan = lw.lora_plan(ids, 2)
+    out, v = lw.lora(x, a, b, s, plan, y=y, save=True)
+    return (out, v, *lw.lora_grad(y, x, v, a, b, s, plan))
+p, q = (torch.ones(5000, device="cuda") for _ in range(2))
+mine = {k: torch.zeros(5120 if len(k) == 1 else 20, dtype=torch.uint8 if len(k) == 1 else torch.float32, device="cuda")
+        for k in ("m", "v", "m_max", "v_max")}
+other = {k: t.clone() for k, t in mine.items()}
+grad = torch.randn(5000, generator=g, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    outs = [run(*s) for s in sets]
+    lw.adamw([p], [grad], mine, lr=1e-2, step=5)
+for _ in range(3):
+    graph.replay()
+    lw.adamw([q], [grad], other, lr=1e-2, step=5)
+    torch.cuda.synchronize()
+    for s, o in zip(sets, outs):
+        assert all(torch.equal(x, y) for x, y in zip(o, run(*s)))
+    assert torch.equal(p, q) and all(torch.equal(mine[k], other[k]) for k in mine)
+print("captured")
+""" % root
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]

@@ -136,22 +136,27 @@ __device__ __forceinline__ void store8(uint16_t* p, us8_t v, int64_t left) {
 struct LoraTile {
   int l, begin, count, first, tiles;
 };
-// Tile `index` of the plan, found by every wave for itself: 64 adapters' tile counts
-// at a time are summed along the lanes.  False beyond the last one.  starts is kept
-// within [0, T], so that no plan leads outside the buffers.
+// Tile `index` of the plan, found by every wave for itself: 256 adapters' tile counts
+// at a time, four to a lane, are summed along the lanes.  False beyond the last one.
+// starts is kept within [0, T], so that no plan leads outside the buffers.
 __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ starts, int L, int T,
                                           int size, int index, LoraTile& tile) {
   const int lane = threadIdx.x & 63;
   int before = 0;
-  for (int base = 0; base <= L; base += 64) {
-    const int l = base + lane;
-    int s0 = T, s1 = T;
-    if (l <= L) {
-      s0 = min(max(starts[l], 0), T);
-      s1 = l < L ? min(max(starts[l + 1], s0), T) : T;
+  for (int base = 0; base <= L; base += 256) {
+    int s[5], tiles[4], all = 0;
+#pragma unroll
+    for (int j = 0; j < 5; j++) s[j] = starts[min(base + lane * 4 + j, L)];
+#pragma unroll
+    for (int j = 0; j < 5; j++) {
+      s[j] = base + lane * 4 + j <= L ? min(max(s[j], 0), T) : T;
+      if (j > 0) {
+        s[j] = max(s[j], s[j - 1]);
+        tiles[j - 1] = (s[j] - s[j - 1] + size - 1) / size;
+        all += tiles[j - 1];
+      }
     }
-    const int tiles = (s1 - s0 + size - 1) / size;
-    int sum = tiles;
+    int sum = all;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const int other = __shfl_up(sum, off, kWave);
@@ -159,16 +164,27 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ starts, in
     }
     const uint64_t past = __ballot(index < before + sum);
     if (past) {
+      // the adapter among this lane's four, for the lane that has it
+      int rest = index - (before + sum - all), l = 0;
+      int first = s[0], end = s[1], n = tiles[0];
+#pragma unroll
+      for (int j = 1; j < 4; j++)
+        if (l == j - 1 && rest >= n) {
+          rest -= n;
+          l = j;
+          first = s[j];
+          end = s[j + 1];
+          n = tiles[j];
+        }
       const int at = __ffsll((unsigned long long)past) - 1;
-      const int skip = (index - __shfl(before + sum - tiles, at, kWave)) * size;
-      tile.l = __builtin_amdgcn_readfirstlane(base + at);
-      tile.first = __builtin_amdgcn_readfirstlane(__shfl(s0, at, kWave));
-      tile.tiles = __builtin_amdgcn_readfirstlane(__shfl(tiles, at, kWave));
-      tile.begin = __builtin_amdgcn_readfirstlane(tile.first + skip);
-      tile.count = __builtin_amdgcn_readfirstlane(min(size, __shfl(s1, at, kWave) - tile.begin));
+      tile.l = base + at * 4 + __builtin_amdgcn_readlane(l, at);
+      tile.first = __builtin_amdgcn_readlane(first, at);
+      tile.tiles = __builtin_amdgcn_readlane(n, at);
+      tile.begin = tile.first + __builtin_amdgcn_readlane(rest, at) * size;
+      tile.count = min(size, __builtin_amdgcn_readlane(end, at) - tile.begin);
       return true;
     }
-    before += __shfl(sum, 63, kWave);
+    before += __builtin_amdgcn_readlane(sum, 63);
   }
   return false;
 }
