@@ -17,7 +17,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _check, load_library as _load_library
-from .w8a8 import _apart, _check_tensor, _float_type, _out, _run, _stream_handle, _torch
+from .w8a8 import _apart, _check_tensor, _float_type, _out, _stream_handle, _torch
 
 LORA_MAX_R = 128
 LORA_MAX_L = 1024
@@ -45,8 +45,8 @@ def _lib() -> ctypes.CDLL:
                                      vp, vp, vp, vp, vp, i64, vp]
     for name in EXPORTED_LORA:
         getattr(lib, name).restype = i64 if name.endswith("_bytes") else i32
-    for name in ("lowbit_lora", "lowbit_lora_grad"):
-        _entry[name] = (getattr(lib, name), getattr(lib, name + "_workspace_bytes"))
+    for name in ("lowbit_lora_plan", "lowbit_lora", "lowbit_lora_grad"):
+        _entry[name] = (getattr(lib, name), getattr(lib, name + "_workspace_bytes", None))
     _declared = lib
     return lib
 
@@ -93,14 +93,15 @@ def lora_plan(ids, L: int, out: dict | None = None) -> dict:
         raise ValueError("ids must have 1 dimension")
     T, dev = ids.shape[0], ids.device
     _check_tensor(ids, "ids", torch.int32, None, (T,))
-    out = out or {}
-    order = _out(out.get("order"), "order", (T,), torch.int32, dev)
-    starts = _out(out.get("starts"), "starts", (L + 1,), torch.int32, dev)
-    if out:
+    if out is None:
+        order = torch.empty_like(ids)
+        starts = torch.empty(L + 1, dtype=torch.int32, device=dev)
+    else:
+        order = _out(out.get("order"), "order", (T,), torch.int32, dev)
+        starts = _out(out.get("starts"), "starts", (L + 1,), torch.int32, dev)
         _apart(order, "order", ids, starts)
         _apart(starts, "starts", ids)
-    _lib()
-    _run("lowbit_lora_plan", None, (ids.data_ptr(), T, L, order.data_ptr(), starts.data_ptr()), dev)
+    _call("lowbit_lora_plan", None, (ids.data_ptr(), T, L, order.data_ptr(), starts.data_ptr()), dev)
     return {"order": order, "starts": starts}
 
 
@@ -133,8 +134,8 @@ def _sizes(x, a, b):
 
 
 def _call(name: str, sizes, args, device) -> None:
-    """Calls an entry point on ``args``, its workspace and the current stream of the tensors'
-    device, which it makes the current one."""
+    """Calls an entry point on ``args``, its workspace (for ``sizes``; None: it takes none) and the
+    current stream of the tensors' device, which it makes the current one."""
     torch = _torch()
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
@@ -142,6 +143,8 @@ def _call(name: str, sizes, args, device) -> None:
     if not _entry:
         _lib()
     call, need_of = _entry[name]
+    if sizes is None:  # no workspace
+        return _check(call(*args, _stream_handle(device)), name)
     need = need_of(*sizes)
     if need > 0:
         # torch's caching allocator hands out blocks aligned to 512 bytes
