@@ -4,11 +4,12 @@
 //   p' = p (1 - lr wd) - lr / (1 - beta1^t) m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
 //
 // Elementwise, so bound by HBM: fp32 parameters and gradients with 8-bit moments
-// move 16 bytes a value, with 32-bit ones 28: 448 tensors of 112 thousand values 172 us in four
-// launches (4.7 TB/s), 100 million bf16 values with an fp32 copy 305 us (5.3).  The tensors' addresses travel as
-// kernel arguments, kMostTensors to a launch, so a step needs no table in device
-// memory and can be captured.  A wave holds one block of 256 values, four
-// to a lane: 16-byte loads of fp32, and the block's maximum stays within the wave.
+// move 16 bytes a value, with 32-bit ones 28.  448 tensors of 112 thousand values take
+// 172 us in four launches (4.7 TB/s), 100 million bf16 values with an fp32 copy 305 us
+// (5.3 TB/s).  The tensors' addresses travel as kernel arguments, kMostTensors to a launch, so
+// a step needs no table in device memory and can be captured.  A wave holds one block of
+// 256 values, four to a lane: 16-byte loads of fp32, and the block's maximum stays within
+// the wave.
 //
 // Every operation on the moments is rounded by itself (no contraction): their
 // 8-bit codes are then the same wherever they are computed, also next to a border

@@ -14,7 +14,7 @@
 // The sums over tokens need, for a lane's operand, eight tokens' elements of one
 // column, where rows lie along the columns.  A lane loads eight rows' 16 bytes at
 // eight columns and pairs them up with byte permutes: an 8 x 8 transpose in its own
-// registers, 32 permutes for 8 products, and x and dy never pass through LDS.
+// registers, 32 permutes for 8 products, and the rows never pass through LDS.
 #include "lora.h"
 
 namespace lowbit {
@@ -615,7 +615,7 @@ Division divide(const LoraSizes& s) {
   d.shares = s.T > d.chunk ? 2 * s.T / d.chunk + 1 : 0;
   return d;
 }
-// floats of u's shares, rounded up to 16 bytes, and of da's and db's
+// floats of u's shares
 int64_t u_floats(const LoraSizes& s, const Division& d) { return d.splits * s.T * s.R; }
 
 template <bool BF, int RB>
