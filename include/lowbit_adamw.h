@@ -26,9 +26,10 @@
  *    g  = grad * grad_scale        (grad alone without one)
  *    m' = b1 m + c1 g,   v' = b2 v + c2 (g g)
  *    p' = p * fl32(1 - lr * weight_decay)
- *         - fl32(lr / (1 - beta1^step)) * m' / (sqrt(v') * fl32((1 - beta2^step)^-1/2) + eps)
+ *         - fl32(lr / (1 - beta1^step)) * m' / (sqrt(v') * fl32((1 - beta2^step)^-1/2) + fl32(eps))
  *    in fp32, p' within some 2^-24 of itself and 2^-21 of the step taken, rounded to the
- *    parameters' type; master receives p' unrounded.
+ *    parameters' type; master receives p' unrounded.  Where there is nothing to divide by (an
+ *    eps of 0, and a v' that is 0 in fp32) no step is taken.
  * 8-bit moments are stored from m' and v':  max is the block's largest |value|,
  * or 0 where that is below 2^-126; q = |value| * fl32(1 / max), and the code is the
  * one whose number is nearest to q, the upper of two at the same distance (for m,

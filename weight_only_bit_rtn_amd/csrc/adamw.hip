@@ -158,6 +158,18 @@ __device__ __forceinline__ void unpack4(uint32_t cm, uint32_t cv, float m_max, f
   }
 }
 
+// m / (sqrt(v) rsq + eps) where v or eps may be subnormal or 0: the operands of the hardware's
+// square root and reciprocal are 2^64 times as large.  0 where there is nothing to divide by.
+__device__ __forceinline__ float small_step(float m, float v, const Scalars& k) {
+  const bool low = v < 0x1p-126f;
+  float root = __builtin_amdgcn_sqrtf(low ? v * 0x1p64f : v);
+  root = low ? root * 0x1p-32f : root;
+  const float under = __builtin_fmaf(root, k.rsq, k.eps);
+  if (under == 0.0f) return m * 0.0f;  // a NaN for an m that is no number
+  const float up = under < 0x1p-126f ? 0x1p64f : 1.0f;
+  return m * __builtin_amdgcn_rcpf(under * up) * up;
+}
+
 template <int PT, int GT, int BITS, bool MASTER>
 __global__ __launch_bounds__(kWaves * 64) void adamw_kernel(const Args a) {
   const int lane = threadIdx.x & 63;
@@ -212,7 +224,8 @@ __global__ __launch_bounds__(kWaves * 64) void adamw_kernel(const Args a) {
     if (b >= n) continue;
     const int64_t e = b + lane * 4, left = n - e;
     const int64_t s = first * kAdamBlock + e;
-    uint32_t top_m = 0, top_v = 0;
+    uint32_t top_m = 0, top_v = 0, least_v = ~0u;  // least_v: bits of the least v but 0, less 1
+    float taken[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       float x = g[j][i];
@@ -229,13 +242,18 @@ __global__ __launch_bounds__(kWaves * 64) void adamw_kernel(const Args a) {
     for (int i = 0; i < 4; i++) {
       top_m = max(top_m, __builtin_bit_cast(uint32_t, m[j][i]) & 0x7fffffffu);
       top_v = max(top_v, __builtin_bit_cast(uint32_t, v[j][i]) & 0x7fffffffu);
+      least_v = min(least_v, __builtin_bit_cast(uint32_t, v[j][i]) - 1);
       // The hardware's square root and reciprocal are off by 2^-23 of the step taken (with
-      // their IEEE forms the 100 million values took 330 us).  The root is of no subnormal number, which
-      // the instruction takes for 0; a NaN stays one.
-      const float root = __builtin_amdgcn_sqrtf(v[j][i] < 0x1p-126f ? 0x1p-126f : v[j][i]);
-      const float step = m[j][i] * __builtin_amdgcn_rcpf(__builtin_fmaf(root, k.rsq, k.eps));
-      p[j][i] = __builtin_fmaf(-k.alpha, step, p[j][i] * k.decay);
+      // their IEEE forms the 100 million values took 330 us).
+      taken[i] = m[j][i] * __builtin_amdgcn_rcpf(
+                               __builtin_fmaf(__builtin_amdgcn_sqrtf(v[j][i]), k.rsq, k.eps));
     }
+    // both take a subnormal number for 0: a second moment below 2^-126, or an eps with no second moment
+    if (least_v < 0x7fffffu || k.eps < 0x1p-126f)
+#pragma unroll
+      for (int i = 0; i < 4; i++) taken[i] = small_step(m[j][i], v[j][i], k);
+#pragma unroll
+    for (int i = 0; i < 4; i++) p[j][i] = __builtin_fmaf(-k.alpha, taken[i], p[j][i] * k.decay);
     if (MASTER) store4<kAdamF32>(a.s.master, s, 4, p[j]);
     store4<PT>(param, e, left, p[j]);
     if (BITS == 32) {
