@@ -88,11 +88,12 @@ typedef struct {
  * (LOWBIT_F32, LOWBIT_F16, LOWBIT_BF16).  tensors, state and options are host
  * memory, read during the call.  bits is 8 or 32.
  *   LOWBIT_ERR_ARG: a null or misaligned pointer, n < 0, count < 0, step < 1, a beta
- *     outside [0, 1), or lr, eps or weight_decay negative or not finite;
+ *     outside [0, 1), or lr, eps or weight_decay negative or not finite; or memory that the
+ *     step writes (a param, m, v, m_max, v_max, master) that shares a byte with another such
+ *     piece, a gradient or a device scalar (gradients may share memory with one another);
  *   LOWBIT_ERR_SHAPE: more than 2^36 values in all;
  *   LOWBIT_ERR_UNSUPPORTED: another type, or bits not in {8, 32}.
- * Tensors of no values take no block; count == 0 is an empty problem.  A tensor must
- * not appear twice, nor share memory with another's.
+ * Tensors of no values take no block; count == 0 is an empty problem.
  */
 LOWBIT_API int lowbit_adamw(const lowbit_adamw_tensor* tensors, int64_t count, int param_dtype,
                             int grad_dtype, int bits, const lowbit_adamw_state* state,

@@ -2,6 +2,10 @@
 // then launches.  Every check runs on the host before anything is enqueued.
 #include <stdint.h>
 
+#include <algorithm>
+#include <memory>
+#include <new>
+
 #include "../../include/lowbit_adamw.h"
 #include "adamw.h"
 
@@ -21,6 +25,44 @@ bool finite_positive(double v) { return within(v, 0.0, 1e300); }
 int hip_status(hipError_t e) { return e == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP; }
 
 constexpr int64_t kMostValues = (int64_t)1 << 36;
+
+// What a step writes (tensors, moments, their maxima, the copy), in order of addresses: no
+// piece may meet another, nor anything that the step reads (gradients, its scalars).  448
+// tensors in any order take some 20 us, a pair 0.1.
+struct Piece {
+  uintptr_t at, end;
+};
+class Written {
+ public:
+  explicit Written(int64_t most)
+      : heap_(most > kFew ? new (std::nothrow) Piece[most] : nullptr), p_(most > kFew ? heap_.get() : few_) {}
+  bool has_room() const { return p_ != nullptr; }
+  void add(const void* at, int64_t bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(at);
+    if (at && bytes > 0) p_[n_++] = {a, a + bytes};
+  }
+  // Whether no piece meets the next; before the first question about others.
+  bool apart() {
+    const auto lower = [](const Piece& x, const Piece& y) { return x.at < y.at; };
+    if (!std::is_sorted(p_, p_ + n_, lower)) std::sort(p_, p_ + n_, lower);
+    for (int64_t i = 1; i < n_; i++)
+      if (p_[i - 1].end > p_[i].at) return false;
+    return true;
+  }
+  bool meets(const void* at, int64_t bytes) const {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(at);
+    if (!at || bytes <= 0) return false;
+    const Piece* next = std::upper_bound(p_, p_ + n_, a, [](uintptr_t x, const Piece& y) { return x < y.at; });
+    return (next != p_ + n_ && next->at < a + bytes) || (next != p_ && next[-1].end > a);
+  }
+
+ private:
+  static constexpr int64_t kFew = 64;
+  Piece few_[kFew];
+  std::unique_ptr<Piece[]> heap_;
+  Piece* p_;
+  int64_t n_ = 0;
+};
 
 }  // namespace
 
@@ -51,6 +93,24 @@ int lowbit_adamw(const lowbit_adamw_tensor* tensors, int64_t count, int param_dt
   if (bad(state->m) || bad(state->v) || bad_or_null(state->master, 16)) return LOWBIT_ERR_ARG;
   if (bits == 8 ? bad(state->m_max) || bad(state->v_max) : state->m_max || state->v_max)
     return LOWBIT_ERR_ARG;
+  Written written(count + 5);
+  if (!written.has_room()) return LOWBIT_ERR_HIP;  // no host memory
+  const int64_t pw = param_dtype == LOWBIT_F32 ? 4 : 2, gw = grad_dtype == LOWBIT_F32 ? 4 : 2;
+  int64_t blocks = 0;
+  for (int64_t i = 0; i < count; i++) {
+    written.add(tensors[i].param, tensors[i].n * pw);
+    blocks += (tensors[i].n + LOWBIT_ADAMW_BLOCK - 1) / LOWBIT_ADAMW_BLOCK;
+  }
+  written.add(state->m, blocks * LOWBIT_ADAMW_BLOCK * (bits / 8));
+  written.add(state->v, blocks * LOWBIT_ADAMW_BLOCK * (bits / 8));
+  written.add(state->m_max, blocks * 4);
+  written.add(state->v_max, blocks * 4);
+  written.add(state->master, blocks * LOWBIT_ADAMW_BLOCK * 4);
+  if (!written.apart() || written.meets(o.lr_or_null, 4) || written.meets(o.step_or_null, 4) ||
+      written.meets(o.grad_scale_or_null, 4))
+    return LOWBIT_ERR_ARG;
+  for (int64_t i = 0; i < count; i++)
+    if (written.meets(tensors[i].grad, tensors[i].n * gw)) return LOWBIT_ERR_ARG;
   static_assert(sizeof(lowbit_adamw_tensor) == sizeof(lowbit::AdamTensor), "one layout");
   return hip_status(lowbit::launch_adamw(
       reinterpret_cast<const lowbit::AdamTensor*>(tensors), count, param_dtype, grad_dtype, bits,

@@ -17,7 +17,7 @@ from itertools import chain
 
 import numpy as np
 
-from . import load_library as _load_library
+from . import LowbitError, load_library as _load_library
 from .w8a8 import _check_tensor, _run, _torch
 
 ADAMW_BLOCK = 256
@@ -134,13 +134,32 @@ def _list_type(tensors, name: str, device) -> int:
                              f"got {t.dtype} on {t.device}")
 
 
+def _refuse_shared(params, grads, state: dict, scalars) -> None:
+    """Names what shares memory with something that a step writes."""
+    torch = _torch()
+    written = [(f"params[{i}]", p) for i, p in enumerate(params)]
+    names = ("m", "v", "m_max", "v_max", "master") if state["m"].dtype is torch.uint8 else ("m", "v", "master")
+    written += [(name, state[name]) for name in names if state.get(name) is not None]
+    read = [(f"grads[{i}]", g) for i, g in enumerate(grads)]
+    read += [(name, t) for name, t in zip(("lr", "step", "grad_scale"), scalars) if isinstance(t, torch.Tensor)]
+    pieces = sorted((t.data_ptr(), t.data_ptr() + t.nbytes, name, i < len(written))
+                    for i, (name, t) in enumerate(written + read) if t.nbytes)
+    ends = {True: (0, ""), False: (0, "")}  # of the pieces so far that are written, and are read: the last end
+    for lo, hi, name, write in pieces:
+        for other in (True, False) if write else (True,):
+            if ends[other][0] > lo:
+                raise ValueError(f"{ends[other][1]} and {name} must not share memory: a step writes to one of them")
+        ends[write] = max(ends[write], (hi, name))
+
+
 def adamw(params, grads, state: dict, lr, betas=(0.9, 0.999), eps: float = 1e-8,
           weight_decay: float = 0.01, step=1, grad_scale=None) -> None:
     """One AdamW step, in place: ``params`` (tensors of one type: fp32, fp16 or bf16) and
     ``state`` (of ``adamw_state``) from ``grads`` (tensors of one type, one for each parameter).
     ``step`` counts from 1.  ``lr`` (fp32) and ``step`` (int32) may be GPU tensors of one
     element, read when the step runs, and ``grad_scale`` is one (fp32) that multiplies the gradients:
-    a captured step follows them.  A grad_scale of infinity or NaN leaves everything as it was."""
+    a captured step follows them.  A grad_scale of infinity or NaN leaves everything as it was.
+    What a step writes shares memory with nothing else of the call; gradients may with each other."""
     torch = _torch()
     params, grads = list(params), list(grads)
     count = len(params)
@@ -152,12 +171,7 @@ def adamw(params, grads, state: dict, lr, betas=(0.9, 0.999), eps: float = 1e-8,
     dev = getattr(params[0], "device", None)
     p_kind = _list_type(params, "params", dev)
     g_kind = _list_type(grads, "grads", dev)
-    places = list(map(Tensor.data_ptr, params))
-    if len(set(places)) < count:
-        at = [i for i in places if i]  # empty tensors have none
-        if len(set(at)) < len(at):
-            raise ValueError("params must not hold a tensor twice")
-    columns = (places, map(Tensor.data_ptr, grads), map(Tensor.numel, params))
+    columns = (map(Tensor.data_ptr, params), map(Tensor.data_ptr, grads), map(Tensor.numel, params))
     if count < 64:  # a few tensors: 4 us less without numpy, hundreds: 24 us more
         sizes = [p.numel() for p in params]
         same = sizes == [g.numel() for g in grads]
@@ -205,8 +219,12 @@ def adamw(params, grads, state: dict, lr, betas=(0.9, 0.999), eps: float = 1e-8,
     place = AdamwState(m.data_ptr(), state["v"].data_ptr(), *tops,
                        None if master is None else master.data_ptr())
     _lib()
-    _run("lowbit_adamw", None, (at, count, p_kind, g_kind, bits,
-                                ctypes.addressof(place), ctypes.addressof(options)), dev)
+    try:
+        _run("lowbit_adamw", None, (at, count, p_kind, g_kind, bits,
+                                    ctypes.addressof(place), ctypes.addressof(options)), dev)
+    except LowbitError:
+        _refuse_shared(params, grads, state, (lr, step, grad_scale))
+        raise
     torch.autograd.graph.increment_version(params)
 
 
