@@ -156,6 +156,9 @@ def adamw(params, grads, state: dict, lr, betas=(0.9, 0.999), eps: float = 1e-8,
           weight_decay: float = 0.01, step=1, grad_scale=None) -> None:
     """One AdamW step, in place: ``params`` (tensors of one type: fp32, fp16 or bf16) and
     ``state`` (of ``adamw_state``) from ``grads`` (tensors of one type, one for each parameter).
+    A gradient has as many values as its parameter, and they pair up in the order of memory: a flat or
+    reshaped gradient is fine, and a transposed one, which has the values in another order, is not told
+    from it (comparing the shapes of 448 pairs takes 34 us of a call's 267).
     ``step`` counts from 1.  ``lr`` (fp32) and ``step`` (int32) may be GPU tensors of one
     element, read when the step runs, and ``grad_scale`` is one (fp32) that multiplies the gradients:
     a captured step follows them.  A grad_scale of infinity or NaN leaves everything as it was.
@@ -230,7 +233,8 @@ def adamw(params, grads, state: dict, lr, betas=(0.9, 0.999), eps: float = 1e-8,
 
 def adamw_moments(state: dict):
     """(m, v), the moments of a state as fp32 values, 256 for each block: of 8-bit ones what
-    the codes stand for, 32-bit ones as they are."""
+    the codes stand for, in new tensors; 32-bit ones are the state's own buffers, and what is
+    written into them is written into the state."""
     torch = _torch()
     m, v = state["m"], state["v"]
     if m.dtype is torch.float32:
