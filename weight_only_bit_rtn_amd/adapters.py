@@ -102,6 +102,8 @@ def lora_plan(ids, L: int, out: dict | None = None) -> dict:
         _apart(order, "order", ids, starts)
         _apart(starts, "starts", ids)
     _call("lowbit_lora_plan", None, (ids.data_ptr(), T, L, order.data_ptr(), starts.data_ptr()), dev)
+    if out is not None:
+        torch.autograd.graph.increment_version((order, starts))
     return {"order": order, "starts": starts}
 
 
@@ -189,6 +191,8 @@ def lora(x, a, b, scales, plan, y=None, out=None, save: bool = False):
           (x.data_ptr(), kind, T, order.data_ptr(), starts.data_ptr(), a.data_ptr(), b.data_ptr(),
            scales.data_ptr(), L, R, N, K, None if y is None else y.data_ptr(), o.data_ptr(),
            v.data_ptr() if save else None), dev)
+    if out is not None:  # a recorded operation that saved it notices
+        torch.autograd.graph.increment_version(o)
     return (o, v) if save else o
 
 
@@ -225,4 +229,6 @@ def lora_grad(dy, x, v, a, b, scales, plan, dx=None, out=None):
           (dy.data_ptr(), x.data_ptr(), v.data_ptr(), kind, T, order.data_ptr(), starts.data_ptr(),
            a.data_ptr(), b.data_ptr(), scales.data_ptr(), L, R, N, K,
            None if dx is None else dx.data_ptr(), o.data_ptr(), da.data_ptr(), db.data_ptr()), dev)
+    if out is not None:
+        torch.autograd.graph.increment_version(o)
     return o, da, db
