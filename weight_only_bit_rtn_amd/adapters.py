@@ -45,8 +45,9 @@ def _lib() -> ctypes.CDLL:
                                      vp, vp, vp, vp, vp, i64, vp]
     for name in EXPORTED_LORA:
         getattr(lib, name).restype = i64 if name.endswith("_bytes") else i32
-    for name in ("lowbit_lora_plan", "lowbit_lora", "lowbit_lora_grad"):
-        _entry[name] = (getattr(lib, name), getattr(lib, name + "_workspace_bytes", None))
+    # at once: another thread's first call sees all of them or none
+    _entry.update({name: (getattr(lib, name), getattr(lib, name + "_workspace_bytes", None))
+                   for name in ("lowbit_lora_plan", "lowbit_lora", "lowbit_lora_grad")})
     _declared = lib
     return lib
 
