@@ -2,22 +2,13 @@
 // products, the tiles of a plan, and the launchers behind the C ABI (not exported).
 #pragma once
 
+#include "lora_division.h"
 #include "w8a8.h"
 
 namespace lowbit {
 
 typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
 
-// Host arithmetic of the launches.  Every bound on a number of tiles counts one for
-// each adapter that has tokens, whose last tile may be a part, and one for the tokens
-// without an adapter.
-struct LoraSizes {
-  int64_t T, N, K, R, L;
-};
-inline int64_t lora_tiles(int64_t T, int64_t L, int tile) {
-  const int64_t most = (T + tile - 1) / tile + L;
-  return most < T ? most : T;
-}
 size_t lora_workspace_bytes(const LoraSizes& s);
 size_t lora_grad_workspace_bytes(const LoraSizes& s);
 

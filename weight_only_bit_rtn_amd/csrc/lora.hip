@@ -12,7 +12,6 @@
 // 3.7 + 4.7 for one token of 4096x4096 and 13.6 against 13.4 for these 64.
 #include "lora.h"
 
-#include <algorithm>
 #include <type_traits>
 
 namespace lowbit {
@@ -307,40 +306,8 @@ __global__ __launch_bounds__(kLoraWaves * 64, 2) void lora_up_kernel(const UpArg
   }
 }
 
-// How a call is divided: tokens in a tile, shares of K, outputs of a workgroup.
-struct Division {
-  int tile;
-  int64_t tiles;
-  int splits, k_share;
-  int ranges, n_share;
-};
-Division divide(const LoraSizes& s) {
-  Division d;
-  d.tile = s.T <= 256 ? 16 : 64;
-  d.tiles = lora_tiles(s.T, s.L, d.tile);
-  auto shares = [&](int64_t length, int64_t n, int& count, int& share) {
-    share = (int)(((length + n - 1) / n + 63) / 64 * 64);
-    count = (int)((length + share - 1) / share);
-  };
-  auto over_tiles = [&](int64_t workgroups) { return (workgroups + d.tiles - 1) / d.tiles; };
-  // Shares of K: a step for every wave at the least, and few, as every workgroup of the expansion
-  // adds them up again (us of both kernels with 8 / 4 at most: 1500 tokens of 8192x8192, 128 ranks
-  // 85 / 71, 700 of 11008x4096, 64 ranks 31 / 29; in small tiles 200 of 4096x8192, 64 ranks 13.8 / 15.3).
-  const int64_t step = d.tile == 16 ? 512 : 256;
-  int64_t n = over_tiles(512);
-  if (n > s.K / (4 * step)) n = std::max(s.K / (4 * step), over_tiles(256));
-  n = std::max<int64_t>(1, std::min({n, (s.K + step - 1) / step, d.tile == 16 ? (int64_t)8 : 4}));
-  shares(s.K, n, d.splits, d.k_share);
-  // Small tiles: many short workgroups (64 tokens of 64 adapters, 11008 outputs, 16 ranks: 8.4 us
-  // with 1024, 9.7 with 512).  Large ones: as many as the card holds at once (1024 / 512 / 256 of
-  // them: 8192x12288, 64 ranks 101 / 92 / 127; 4096x4096, 128 ranks, one to a CU, 84 / 58 / 42).
-  n = std::min(over_tiles(d.tile == 16 ? 1024 : 512), (s.N + 255) / 256);
-  shares(s.N, n, d.ranges, d.n_share);
-  return d;
-}
-
 template <bool BF, int RB, int TB>
-hipError_t run(const DownArgs& down, const UpArgs& up, const Division& d, hipStream_t stream) {
+hipError_t run(const DownArgs& down, const UpArgs& up, const LoraDivision& d, hipStream_t stream) {
   constexpr int DOWN = RB < 4 ? RB : 4, W = TB == 1 && RB <= 2 ? 8 : 4;
   const hipError_t e = launch_lds(lora_down_kernel<BF, DOWN, TB, W>,
                                   dim3((unsigned)d.tiles, d.splits, (down.p.R + 63) / 64), W * 64,
@@ -350,11 +317,11 @@ hipError_t run(const DownArgs& down, const UpArgs& up, const Division& d, hipStr
                     up_bytes<RB, TB>(), stream, up);
 }
 template <bool BF, int RB>
-hipError_t run(const DownArgs& down, const UpArgs& up, const Division& d, hipStream_t stream) {
+hipError_t run(const DownArgs& down, const UpArgs& up, const LoraDivision& d, hipStream_t stream) {
   return d.tile == 16 ? run<BF, RB, 1>(down, up, d, stream) : run<BF, RB, 4>(down, up, d, stream);
 }
 template <bool BF>
-hipError_t run(const DownArgs& down, const UpArgs& up, const Division& d, hipStream_t stream) {
+hipError_t run(const DownArgs& down, const UpArgs& up, const LoraDivision& d, hipStream_t stream) {
   const int blocks = (down.p.R + 15) / 16;
   if (blocks <= 1) return run<BF, 1>(down, up, d, stream);
   if (blocks <= 2) return run<BF, 2>(down, up, d, stream);
@@ -366,12 +333,12 @@ hipError_t run(const DownArgs& down, const UpArgs& up, const Division& d, hipStr
 
 size_t lora_workspace_bytes(const LoraSizes& s) {
   if (s.T == 0) return 0;
-  return (size_t)divide(s).splits * s.T * s.R * sizeof(float);
+  return (size_t)divide_lora(s).splits * s.T * s.R * sizeof(float);
 }
 
 hipError_t launch_lora(const void* x, int dtype, const LoraArgs& p, const void* y, void* out,
                        float* v, void* workspace, hipStream_t stream) {
-  const Division d = divide({p.T, p.N, p.K, p.R, p.L});
+  const LoraDivision d = divide_lora({p.T, p.N, p.K, p.R, p.L});
   float* const shares = static_cast<float*>(workspace);
   const DownArgs down = {p, static_cast<const uint16_t*>(x), shares, d.k_share};
   const UpArgs up = {p,           shares, d.splits, d.n_share, static_cast<const uint16_t*>(y),

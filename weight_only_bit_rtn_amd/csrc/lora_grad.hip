@@ -20,16 +20,9 @@
 namespace lowbit {
 namespace {
 
-constexpr int kGradWaves = 4;
-constexpr int kTile = 64;   // tokens of u's and dx's tiles
-constexpr int kCols = kGradWaves * 128;  // columns of a workgroup of dx, da or db
-
 // ---------------------------------------------------------------------------
 // u = b^T dy
 // ---------------------------------------------------------------------------
-constexpr int kBackWaves = 8;
-constexpr int kMostSplits = 4;  // shares of u: the sums hold them in registers
-
 struct BackArgs {
   LoraArgs p;
   const uint16_t* dy;
@@ -577,50 +570,12 @@ __global__ __launch_bounds__(kGradWaves * 64, 2) void lora_finish_kernel(const S
     join_part(join, at - dx);
 }
 
-// How a call is divided: shares of N for u, tokens of a chunk of the sums.
-struct Division {
-  int64_t tiles;
-  int splits, n_share;
-  int chunk;
-  int64_t chunks, shares;
-  int k_cols, n_cols, dx_cols;
-};
-Division divide(const LoraSizes& s) {
-  Division d;
-  d.tiles = lora_tiles(s.T, s.L, kTile);
-  const int64_t most = (s.N + kBackWaves * 64 - 1) / (kBackWaves * 64);
-  // shares of N: the sums read them all again (us of u / sums, 64 ranks: 8192 tokens of 12288x12288
-  // with 4 of four waves, 2 of eight, 1: 66 / 120, 74 / 107, 91 / 106; 4096 of 4096x4096 with 4 and 2:
-  // 20 / 37, 21 / 33)
-  int64_t n = (192 + d.tiles - 1) / d.tiles;
-  if (n > kMostSplits) n = kMostSplits;
-  if (n > most) n = most;
-  d.n_share = (int)(((s.N + n - 1) / n + 63) / 64 * 64);
-  d.splits = (int)((s.N + d.n_share - 1) / d.n_share);
-  d.k_cols = (int)((s.K + kCols - 1) / kCols);
-  d.n_cols = (int)((s.N + kCols - 1) / kCols);
-  // dx: two workgroups to a CU at once
-  const int64_t ranges = 512 / ((s.T + kTile - 1) / kTile);
-  d.dx_cols = ranges < 1 ? d.k_cols : (int)((d.k_cols + ranges - 1) / ranges);
-  // chunks as many as the card holds workgroups at once, of 128 tokens at least (us of the
-  // sums with 256 / 128: 400 tokens 4096x4096, 16 ranks 12.5 / 8.6; 700 of 11008x4096, 64 ranks
-  // 20.1 / 16.3, where the join takes 1.9 more)
-  const int64_t cols = (d.k_cols + d.n_cols) * ((s.R + 63) / 64);
-  const int64_t held = s.R > 32 ? 256 : 512;
-  const int64_t wanted = held > cols ? held / cols : 1;
-  int64_t chunk = ((s.T + wanted - 1) / wanted + kTile - 1) / kTile * kTile;
-  if (chunk < 128) chunk = 128;
-  d.chunk = (int)chunk;
-  d.chunks = lora_tiles(s.T, s.L, d.chunk);
-  d.shares = s.T > d.chunk ? 2 * s.T / d.chunk + 1 : 0;
-  return d;
-}
 // floats of u's shares
-int64_t u_floats(const LoraSizes& s, const Division& d) { return d.splits * s.T * s.R; }
+int64_t u_floats(const LoraSizes& s, const LoraGradDivision& d) { return d.splits * s.T * s.R; }
 
 template <bool BF, int RB>
 hipError_t run(const BackArgs& back, const SpreadArgs& spread, const JoinArgs& join,
-               const Division& d, hipStream_t stream) {
+               const LoraGradDivision& d, hipStream_t stream) {
   constexpr int RU = RB < 4 ? RB : 4;
   const int groups = (back.p.R + 63) / 64;
   hipError_t e = launch_lds(lora_back_kernel<BF, RU>, dim3((unsigned)d.tiles, d.splits, groups),
@@ -637,7 +592,7 @@ hipError_t run(const BackArgs& back, const SpreadArgs& spread, const JoinArgs& j
 }
 template <bool BF>
 hipError_t run(const BackArgs& back, const SpreadArgs& spread, const JoinArgs& join,
-               const Division& d, hipStream_t stream) {
+               const LoraGradDivision& d, hipStream_t stream) {
   const int blocks = (back.p.R + 15) / 16;
   if (blocks <= 1) return run<BF, 1>(back, spread, join, d, stream);
   if (blocks <= 2) return run<BF, 2>(back, spread, join, d, stream);
@@ -649,7 +604,7 @@ hipError_t run(const BackArgs& back, const SpreadArgs& spread, const JoinArgs& j
 
 size_t lora_grad_workspace_bytes(const LoraSizes& s) {
   if (s.T == 0) return 0;
-  const Division d = divide(s);
+  const LoraGradDivision d = divide_lora_grad(s);
   const int64_t parts = d.shares * s.R * (s.K + s.N);
   return (size_t)(u_floats(s, d) + parts) * sizeof(float);
 }
@@ -658,7 +613,7 @@ hipError_t launch_lora_grad(const void* dy, const void* x, const float* v, int d
                             const LoraArgs& p, const void* base, void* dx, float* da, float* db,
                             void* workspace, hipStream_t stream) {
   const LoraSizes s = {p.T, p.N, p.K, p.R, p.L};
-  const Division d = s.T > 0 ? divide(s) : Division{};
+  const LoraGradDivision d = s.T > 0 ? divide_lora_grad(s) : LoraGradDivision{};
   float* const shares = static_cast<float*>(workspace);
   float* const part_a = shares + u_floats(s, d);
   float* const part_b = part_a + d.shares * s.R * s.K;
