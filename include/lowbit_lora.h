@@ -23,9 +23,12 @@
  *    2^-17 of the largest loses bits, as fp16 subnormals do);
  *  - u_t = b_l^T dy_t in fp32;  dx_t = base_t + s_l (a_l^T u_t), in the same two parts;
  *  - da_l = s_l sum_t u_t x_t^T and db_l = s_l sum_t dy_t v_t^T over the adapter's
- *    tokens, fp32.  u and v enter in 24 bits, three parts, for LOWBIT_BF16; for
- *    LOWBIT_F16 in 22 bits, after a power of two chosen for some hundreds of
- *    tokens at most, by their largest value;
+ *    tokens, fp32.  u and v enter in 24 bits, three parts, for LOWBIT_BF16.  For
+ *    LOWBIT_F16 they enter in two parts after a power of two that follows the largest
+ *    finite value so far, of up to 64 ranks together and of the tokens of one chunk of the
+ *    adapter's, which can be thousands and all that it has.  A value of u or v is then
+ *    off by 2^-22 of itself or by 2^-39 of that largest one, whichever is more: one 2^-30
+ *    below it keeps about 9 bits, and one 2^-39 below it none;
  *  - a token without an adapter: out_t = y_t, v_t = 0, dx_t = base_t, and it
  *    adds nothing to da and db.  An adapter without tokens has zero gradients.
  *    Nothing of such a token's x and dy, nor of an adapter without tokens, reaches

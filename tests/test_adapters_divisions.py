@@ -171,3 +171,30 @@ def test_many_steps_of_the_forward_pass(lw, shape, kind, order):  # noqa: F811
         assert (np.abs(some(got, at, 1) - want) <= far).all() and (np.abs(f64(v) - want_v) <= far_v).all()
     y = c.y.clone()
     assert lw.lora(c.x, *c.pools(), y=y, out=y) is y and torch.equal(y, out)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+def test_ranks_and_tokens_far_below_the_others(lw, kind):  # noqa: F811
+    """Every other rank's u 2^-12 and every third one's v 2^-20 below the rest, the largest tokens first: da and db of each
+    rank are within 2^-22 of its own values and 2^-39 of the largest (fp16), or 2^-24 of its own (bf16)."""
+    T, N, K, R, L = LONG_SUMS_A[3]
+    c = Case(lw, T, N, K, R, 1, kind, "mixed", seed=14)
+    c.b[:, :, 1::2] *= 2.0 ** -12
+    c.v[:, ::3] *= 2.0 ** -20
+    first = c.plan["order"][:100].long()
+    c.dy[first] *= 16
+    c.v[first] *= 64
+    dx, da, db = lw.lora_grad(c.dy, c.x, c.v, *c.pools(), dx=c.base)
+    k_at = columns(K)
+    check_gradients(c, dx, da, db, c.base, k_at, np.arange(N))
+    # and rank by rank: what the sums' roundings leave of that
+    s, t = f64(c.scales)[0], np.flatnonzero(c.ids == 0)
+    dy, x, v, b = f64(c.dy)[t], some(c.x, k_at, 1)[t], f64(c.v)[t], f64(c.b)[0]
+    u, deep = dy @ b, ref.depth(N) * (np.abs(dy) @ np.abs(b))
+    for got, val, rows, off in ((some(da, k_at, 2)[0], u, x, deep), (f64(db)[0].T, v, dy, 0 * v)):
+        own = np.abs(val)
+        floor = 2.0 ** -39 * own.max() if kind == "fp16" else 0.0
+        part = np.maximum(own * (2.0 ** -22 if kind == "fp16" else 2.0 ** -24), floor)
+        far = s * ((off + part + ref.depth(3 * len(t)) * own).T @ np.abs(rows)) * 1.01 + 2.0 ** -140
+        assert (np.abs(got - s * (val.T @ rows)) <= far).all()

@@ -202,7 +202,8 @@ def lora_grad(dy, x, v, a, b, scales, plan, dx=None, out=None):
     saved.  ``dx``: the gradient through the shared projection (of ``linear_w8a8_grad``),
     which the adapters' part is added to; without it that part alone.  ``out``: where dx is
     written, ``dx`` itself allowed.  da [L][R][K] and db [L][N][R] are fp32, the sums as they
-    are; an adapter without tokens has zeros."""
+    are; an adapter without tokens has zeros.  fp16: u and v enter them with 22 bits each, and not
+    below 2^-39 of the largest among up to 64 ranks and all tokens of an adapter (bf16: 24 bits each)."""
     torch = _torch()
     kind = _float_type(x, "x")
     T, N, K, R, L = _sizes(x, a, b)

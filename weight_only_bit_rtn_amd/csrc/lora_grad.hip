@@ -305,7 +305,8 @@ __device__ __forceinline__ int64_t share_of(int first, int chunk) { return 2 * (
 // of u or v, turned around so that an operand's eight tokens lie side by side, in two
 // buffers; their rows of x or dy go straight to the registers, where the next 64 tokens'
 // are under way while these are multiplied.  fp16: the parts stand for values times 2^e, e
-// by the largest value so far; the sums follow when it changes.
+// by the largest value of the chunk so far (all of this workgroup's ranks, and a chunk's length has
+// no upper limit); the sums follow when it changes.
 // At most two blocks of ranks to a wave: four double the waves, two for each 128 columns, whose
 // second reading of a row the vector cache serves.
 template <int RB>
