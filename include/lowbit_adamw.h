@@ -31,10 +31,26 @@
  *    parameters' type; master receives p' unrounded.  Where there is nothing to divide by (an
  *    eps of 0, and a v' that is 0 in fp32) no step is taken.
  * 8-bit moments are stored from m' and v':  max is the block's largest |value|,
- * or 0 where that is below 2^-126; q = |value| * fl32(1 / max), and the code is the
- * one whose number is nearest to q, the upper of two at the same distance (for m,
+ * or 0 where that is below 2^-126; q = |value| * fl32(1 / max), and with bits == 8 the code
+ * is the one whose number is nearest to q, the upper of two at the same distance (for m,
  * q below 1.1875 * 2^-16 becomes 0; for v, a q that is not zero becomes 1 at least,
  * so that no second moment is lost that a first one may still be divided by).
+ *    What that loses: codes lie 6% to 12% apart, and a step of beta2 = 0.999 changes v
+ * by a thousandth of itself and of g^2, so a value's ratio to its block's largest moves only
+ * when g^2 is some 30 to 60 times v, and it never falls.  Where all gradients of a block grow or
+ * shrink together nothing is lost; where some change against the rest, their v stays
+ * behind: after 7000 steps in which half of a block's gradients were a tenth of
+ * before, their v was 72 times too large, and where half were four times as large, the
+ * other half's was 7.7 times.
+ *    bits == (8 | LOWBIT_ADAMW_RANDOM) has none of that: the code is that of one
+ * of the two numbers next to q, the upper one where the fp32 bits of q plus r pass a
+ * multiple of 2^20.  r = 16 h + 8, h the upper (m) or lower (v) 16 bits of
+ * mix(p ^ mix(mix(step) + P)), p and P the lower and upper 32 bits of the value's place
+ * in the moments, step its lower 32 bits, mix(x): x ^= x >> 16, x *= 0x6A09E667,
+ * x ^= x >> 15, x *= 0xBB67AE85, x ^= x >> 16.  So v follows its definition in the mean
+ * (within 0.7 to 1.5 of it for nine in ten values) and results still repeat bit for bit.  m with
+ * q below 1.125 * 2^-16 becomes 0, v is never 0 for a q that is not.  The format is the
+ * same, and the two can take turns on one state.
  * A block that holds an infinity or a NaN has a NaN maximum and codes 0: everything
  * computed from it is NaN.
  * A grad_scale that is an infinity or a NaN leaves everything as it was: a step of
@@ -53,6 +69,7 @@ extern "C" {
 #endif
 
 #define LOWBIT_ADAMW_BLOCK 256
+#define LOWBIT_ADAMW_RANDOM 256 /* bits == (8 | LOWBIT_ADAMW_RANDOM): codes rounded up or down */
 #define LOWBIT_F32 3 /* beside LOWBIT_F16 and LOWBIT_BF16: type of parameters and gradients */
 
 /* One tensor of a step: device pointers (16-byte aligned), and how many values. */
@@ -86,13 +103,13 @@ typedef struct {
 /*
  * One step over `count` tensors of one parameter type and one gradient type
  * (LOWBIT_F32, LOWBIT_F16, LOWBIT_BF16).  tensors, state and options are host
- * memory, read during the call.  bits is 8 or 32.
+ * memory, read during the call.  bits is 8, 8 | LOWBIT_ADAMW_RANDOM or 32.
  *   LOWBIT_ERR_ARG: a null or misaligned pointer, n < 0, count < 0, step < 1, a beta
  *     outside [0, 1), or lr, eps or weight_decay negative or not finite; or memory that the
  *     step writes (a param, m, v, m_max, v_max, master) that shares a byte with another such
  *     piece, a gradient or a device scalar (gradients may share memory with one another);
  *   LOWBIT_ERR_SHAPE: more than 2^36 values in all;
- *   LOWBIT_ERR_UNSUPPORTED: another type, or bits not in {8, 32}.
+ *   LOWBIT_ERR_UNSUPPORTED: another type, or other bits.
  * Tensors of no values take no block; count == 0 is an empty problem.
  */
 LOWBIT_API int lowbit_adamw(const lowbit_adamw_tensor* tensors, int64_t count, int param_dtype,

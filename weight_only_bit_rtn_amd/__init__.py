@@ -375,5 +375,5 @@ from .adapters import (  # noqa: E402,F401
 
 # the AdamW step (include/lowbit_adamw.h)
 from .optimizer import (  # noqa: E402,F401
-    ADAMW_BLOCK, EXPORTED_ADAMW, AdamwOptions, AdamwState, adamw, adamw_moments, adamw_moments_raw,
+    ADAMW_BLOCK, ADAMW_RANDOM, EXPORTED_ADAMW, AdamwOptions, AdamwState, adamw, adamw_moments, adamw_moments_raw,
     adamw_raw, adamw_state)

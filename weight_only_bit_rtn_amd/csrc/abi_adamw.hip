@@ -9,7 +9,8 @@
 #include "../../include/lowbit_adamw.h"
 #include "adamw.h"
 
-static_assert(LOWBIT_ADAMW_BLOCK == lowbit::kAdamBlock && LOWBIT_F32 == lowbit::kAdamF32,
+static_assert(LOWBIT_ADAMW_BLOCK == lowbit::kAdamBlock && LOWBIT_F32 == lowbit::kAdamF32 &&
+                  LOWBIT_ADAMW_RANDOM == lowbit::kAdamRandom,
               "the header's constants are the library's");
 
 namespace {
@@ -71,7 +72,8 @@ extern "C" {
 int lowbit_adamw(const lowbit_adamw_tensor* tensors, int64_t count, int param_dtype,
                  int grad_dtype, int bits, const lowbit_adamw_state* state,
                  const lowbit_adamw_options* options, void* hip_stream) {
-  if (!is_type(param_dtype) || !is_type(grad_dtype) || (bits != 8 && bits != 32))
+  if (!is_type(param_dtype) || !is_type(grad_dtype) ||
+      (bits != 8 && bits != (8 | LOWBIT_ADAMW_RANDOM) && bits != 32))
     return LOWBIT_ERR_UNSUPPORTED;
   if (count < 0 || !options) return LOWBIT_ERR_ARG;
   const lowbit_adamw_options& o = *options;
@@ -91,18 +93,19 @@ int lowbit_adamw(const lowbit_adamw_tensor* tensors, int64_t count, int param_dt
   }
   if (values == 0) return LOWBIT_OK;
   if (bad(state->m) || bad(state->v) || bad_or_null(state->master, 16)) return LOWBIT_ERR_ARG;
-  if (bits == 8 ? bad(state->m_max) || bad(state->v_max) : state->m_max || state->v_max)
+  if (bits != 32 ? bad(state->m_max) || bad(state->v_max) : state->m_max || state->v_max)
     return LOWBIT_ERR_ARG;
   Written written(count + 5);
   if (!written.has_room()) return LOWBIT_ERR_HIP;  // no host memory
   const int64_t pw = param_dtype == LOWBIT_F32 ? 4 : 2, gw = grad_dtype == LOWBIT_F32 ? 4 : 2;
+  const int64_t mw = bits == 32 ? 4 : 1;
   int64_t blocks = 0;
   for (int64_t i = 0; i < count; i++) {
     written.add(tensors[i].param, tensors[i].n * pw);
     blocks += (tensors[i].n + LOWBIT_ADAMW_BLOCK - 1) / LOWBIT_ADAMW_BLOCK;
   }
-  written.add(state->m, blocks * LOWBIT_ADAMW_BLOCK * (bits / 8));
-  written.add(state->v, blocks * LOWBIT_ADAMW_BLOCK * (bits / 8));
+  written.add(state->m, blocks * LOWBIT_ADAMW_BLOCK * mw);
+  written.add(state->v, blocks * LOWBIT_ADAMW_BLOCK * mw);
   written.add(state->m_max, blocks * 4);
   written.add(state->v_max, blocks * 4);
   written.add(state->master, blocks * LOWBIT_ADAMW_BLOCK * 4);

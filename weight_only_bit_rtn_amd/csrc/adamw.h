@@ -27,6 +27,8 @@ struct AdamOptions {
 
 // Parameter and gradient types: ElemType's fp16 and bf16, and fp32.
 constexpr int kAdamF32 = 3;
+// bits: 32, 8, or 8 | kAdamRandom, whose codes are rounded up or down by a number of step and place.
+constexpr int kAdamRandom = 256;
 
 hipError_t launch_adamw(const AdamTensor* tensors, int64_t count, int param_type, int grad_type,
                         int bits, const AdamState& state, const AdamOptions& options,

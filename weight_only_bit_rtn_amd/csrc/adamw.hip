@@ -147,6 +147,20 @@ __device__ __forceinline__ uint32_t nearest(float q) {
   return __builtin_elementwise_sub_sat((__builtin_bit_cast(uint32_t, q) + 0x80000u) >> 20, DOWN);
 }
 
+// One of the two codes next to q, each by its nearness: r / 2^20 of the way between their numbers
+// and more goes up, 8 <= r < 2^20.  (From 1 + 2^-23 no r reaches past the last code.)
+template <uint32_t DOWN>
+__device__ __forceinline__ uint32_t either(float q, uint32_t r) {
+  return __builtin_elementwise_sub_sat((__builtin_bit_cast(uint32_t, q) + r) >> 20, DOWN);
+}
+// 32 bits that depend on all of x's in no visible way; the factors are the binary digits of the
+// square roots of 2 and 3.
+__host__ __device__ inline uint32_t mixed(uint32_t x) {
+  x = (x ^ x >> 16) * 0x6A09E667u;
+  x = (x ^ x >> 15) * 0xBB67AE85u;
+  return x ^ x >> 16;
+}
+
 __device__ __forceinline__ void unpack4(uint32_t cm, uint32_t cv, float m_max, float v_max,
                                         float (&m)[4], float (&v)[4]) {
 #pragma unroll
@@ -169,6 +183,8 @@ __device__ __forceinline__ float small_step(float m, float v, const Scalars& k) 
   const float up = under < 0x1p-126f ? 0x1p64f : 1.0f;
   return m * __builtin_amdgcn_rcpf(under * up) * up;
 }
+
+constexpr int kRandom8 = 8 | kAdamRandom;
 
 template <int PT, int GT, int BITS, bool MASTER>
 __global__ __launch_bounds__(kWaves * 64) void adamw_kernel(const Args a) {
@@ -285,10 +301,20 @@ __global__ __launch_bounds__(kWaves * 64) void adamw_kernel(const Args a) {
     const float inv_v = __builtin_bit_cast(
         float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, inverse), lane_v));
     uint32_t cm = 0, cv = 0;
+    // for each place a number of its own in every step, 16 bits for m and 16 for v
+    uint32_t random[4];
+    if (BITS == kRandom8) {
+      const int64_t t = a.step_at ? (int64_t)max(*a.step_at, 1) : a.step;
+      const uint32_t key = mixed(mixed((uint32_t)t) + (uint32_t)(s >> 32));
+#pragma unroll
+      for (int i = 0; i < 4; i++) random[i] = mixed(((uint32_t)s + i) ^ key);
+    }
     if (numbers >> j & 1)
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        const uint32_t c = nearest<kDownM>(fabsf(m[j][i]) * inv_m);
+        const float q = fabsf(m[j][i]) * inv_m;
+        const uint32_t c = BITS == kRandom8 ? either<kDownM>(q, random[i] >> 16 << 4 | 8)
+                                            : nearest<kDownM>(q);
         const uint32_t sign = __builtin_bit_cast(uint32_t, m[j][i]) >> 31 << 7;
         cm |= (c ? c | sign : 0u) << (8 * i);
       }
@@ -296,8 +322,10 @@ __global__ __launch_bounds__(kWaves * 64) void adamw_kernel(const Args a) {
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         const float q = v[j][i] * inv_v;
+        const uint32_t c = BITS == kRandom8 ? either<kDownV>(q, (random[i] & 0xffff) << 4 | 8)
+                                            : nearest<kDownV>(q);
         // one at least where q is not 0
-        cv |= max(nearest<kDownV>(q), min(__builtin_bit_cast(uint32_t, q), 1u)) << (8 * i);
+        cv |= max(c, min(__builtin_bit_cast(uint32_t, q), 1u)) << (8 * i);
       }
     static_cast<uint32_t*>(a.s.m)[s / 4] = cm;
     static_cast<uint32_t*>(a.s.v)[s / 4] = cv;
@@ -332,6 +360,8 @@ template <int PT, int GT>
 void launch(int bits, bool master, unsigned grid, const Args& a, hipStream_t stream) {
   if (bits == 8)
     launch<PT, GT, 8>(master, grid, a, stream);
+  else if (bits == kRandom8)
+    launch<PT, GT, kRandom8>(master, grid, a, stream);
   else
     launch<PT, GT, 32>(master, grid, a, stream);
 }
