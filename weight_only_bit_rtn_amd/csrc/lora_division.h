@@ -27,6 +27,11 @@ struct LoraDivision {
 };
 inline LoraDivision divide_lora(const LoraSizes& s) {
   LoraDivision d;
+  // Small tiles up to 256 tokens, large ones beyond (us of both kernels, tiles of 16 / 64, 4096
+  // outputs and K unless given: 64 tokens, 16 ranks 8.9 / 11.4; 256 tokens 10.2 / 12.5; 2000 of
+  // 11008x4096, 64 ranks 50.5 / 43.2; 8192 of 12288x12288, 64 ranks 234 / 156).  The border is a plain
+  // one: small tiles lead further on where adapters have few tokens or ranks are few (512 tokens of
+  // 64 adapters, 64 ranks 26.3 / 36.2; 1333 of 4096x11008, 24 ranks 25.5 / 28.7; 4096, 16 ranks 28.8 / 31.7).
   d.tile = s.T <= 256 ? 16 : 64;
   d.tiles = lora_tiles(s.T, s.L, d.tile);
   auto shares = [&](int64_t length, int64_t n, int& count, int& share) {
@@ -34,7 +39,9 @@ inline LoraDivision divide_lora(const LoraSizes& s) {
     count = (int)((length + share - 1) / share);
   };
   auto over_tiles = [&](int64_t workgroups) { return (workgroups + d.tiles - 1) / d.tiles; };
-  // Shares of K: a step for every wave at the least, and few, as every workgroup of the expansion
+  // Shares of K: 512 workgroups (us of both kernels with 256 / 512 / 1024: 8192 tokens of 12288x12288,
+  // 64 ranks 186 / 156 / 156, 16 ranks 154 / 136 / 135; from 4096 tokens down the limits decide and it is one),
+  // a step for every wave at the least, and few, as every workgroup of the expansion
   // adds them up again (us of both kernels with 8 / 4 at most: 1500 tokens of 8192x8192, 128 ranks
   // 85 / 71, 700 of 11008x4096, 64 ranks 31 / 29; in small tiles 200 of 4096x8192, 64 ranks 13.8 / 15.3).
   const int64_t step = d.tile == 16 ? 512 : 256;
@@ -70,7 +77,9 @@ inline LoraGradDivision divide_lora_grad(const LoraSizes& s) {
   const int64_t most = (s.N + kBackWaves * 64 - 1) / (kBackWaves * 64);
   // shares of N: the sums read them all again (us of u / sums, 64 ranks: 8192 tokens of 12288x12288
   // with 4 of four waves, 2 of eight, 1: 66 / 120, 74 / 107, 91 / 106; 4096 of 4096x4096 with 4 and 2:
-  // 20 / 37, 21 / 33)
+  // 20 / 37, 21 / 33).  192 workgroups (the whole gradient with 96 / 192 / 384: 8192 of 12288x12288, 64
+  // ranks 272 / 264 / 281; 2000 of 11008x4096, 16 ranks 48.6 / 46.3 / 46.2; 4096 of 11008x4096, 16 ranks
+  // 74.5 / 72.8 / 69.6; fewer tokens have the most shares with any of them)
   int64_t n = (192 + d.tiles - 1) / d.tiles;
   if (n > kMostSplits) n = kMostSplits;
   if (n > most) n = most;
@@ -78,12 +87,17 @@ inline LoraGradDivision divide_lora_grad(const LoraSizes& s) {
   d.splits = (int)((s.N + d.n_share - 1) / d.n_share);
   d.k_cols = (int)((s.K + kCols - 1) / kCols);
   d.n_cols = (int)((s.N + kCols - 1) / kCols);
-  // dx: two workgroups to a CU at once
+  // dx: two workgroups to a CU at once (us of the whole gradient with 256 / 512 / 1024 workgroups: 8192
+  // tokens of 12288x12288, 64 ranks 281 / 261 / 264, 16 ranks 232 / 207 / 207; 1500 of 8192x8192, 128 ranks
+  // 93 / 87 / 88; 700 of 11008x4096 one)
   const int64_t ranges = 512 / ((s.T + kTile - 1) / kTile);
   d.dx_cols = ranges < 1 ? d.k_cols : (int)((d.k_cols + ranges - 1) / ranges);
   // chunks as many as the card holds workgroups at once, of 128 tokens at least (us of the
   // sums with 256 / 128: 400 tokens 4096x4096, 16 ranks 12.5 / 8.6; 700 of 11008x4096, 64 ranks
-  // 20.1 / 16.3, where the join takes 1.9 more)
+  // 20.1 / 16.3, where the join takes 1.9 more).  Above 32 ranks they have twice the waves, and one
+  // fills a CU (us of the whole gradient with 256 / 512 held: 64 ranks, 8192 tokens of 12288x12288 261 / 276,
+  // 4096 of 4096x4096 84 / 93; 16 ranks, 8192 of 12288x12288 211 / 206, 4096 of 4096x4096 52.4 / 52.0,
+  // 8192 of 4096x4096 80 / 85)
   const int64_t cols = (d.k_cols + d.n_cols) * ((s.R + 63) / 64);
   const int64_t held = s.R > 32 ? 256 : 512;
   const int64_t wanted = held > cols ? held / cols : 1;

@@ -6,7 +6,8 @@
 // Three launches: u; then da and db; then dx, and beside it the join of da's and db's
 // shares where an adapter has more than one chunk of tokens.  Bound by HBM: dy is read
 // twice, x and base once, dx is written, 2 T (2 N + 3 K) bytes.  8192 tokens of 12288x12288,
-// 64 ranks: 68 + 107 + 83 us (200, 400 and 400 MB); 16 ranks 59 + 71 + 68, 3.4, 5.7 and 5.9 TB/s.
+// 64 ranks: 75 + 114 + 85 us (200, 400 and 400 MB: 2.7, 3.5 and 4.7 TB/s); 16 ranks 59 + 71 + 68, 3.4, 5.7
+// and 5.9 TB/s.
 // With 64 ranks the sums are held up by the products (27% of the matrix cores' time) and the
 // parts' making between barriers: without the latter they take 8 us less, without two of
 // three parts 3 less.
