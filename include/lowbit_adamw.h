@@ -110,6 +110,7 @@ typedef struct {
  *     piece, a gradient or a device scalar (gradients may share memory with one another);
  *   LOWBIT_ERR_SHAPE: more than 2^36 values in all;
  *   LOWBIT_ERR_UNSUPPORTED: another type, or other bits.
+ *   LOWBIT_ERR_HIP: a launch failed, or the host has no memory to compare more than 59 tensors.
  * Tensors of no values take no block; count == 0 is an empty problem.
  */
 LOWBIT_API int lowbit_adamw(const lowbit_adamw_tensor* tensors, int64_t count, int param_dtype,

@@ -29,7 +29,7 @@ constexpr int64_t kMostValues = (int64_t)1 << 36;
 
 // What a step writes (tensors, moments, their maxima, the copy), in order of addresses: no
 // piece may meet another, nor anything that the step reads (gradients, its scalars).  448
-// tensors in any order take some 20 us, a pair 0.1.
+// tensors take 19 us of the host, 25 in a random order of addresses; a pair less than 1.
 struct Piece {
   uintptr_t at, end;
 };
