@@ -48,7 +48,7 @@
  * mix(p ^ mix(mix(step) + P)), p and P the lower and upper 32 bits of the value's place
  * in the moments, step its lower 32 bits, mix(x): x ^= x >> 16, x *= 0x6A09E667,
  * x ^= x >> 15, x *= 0xBB67AE85, x ^= x >> 16.  So v follows its definition in the mean
- * (within 0.7 to 1.5 of it for nine in ten values) and results still repeat bit for bit.  m with
+ * (within 0.67 to 1.45 of it for nine in ten values) and results still repeat bit for bit.  m with
  * q below 1.125 * 2^-16 becomes 0, v is never 0 for a q that is not.  The format is the
  * same, and the two can take turns on one state.
  * A block that holds an infinity or a NaN has a NaN maximum and codes 0: everything

@@ -153,8 +153,8 @@ template <uint32_t DOWN>
 __device__ __forceinline__ uint32_t either(float q, uint32_t r) {
   return __builtin_elementwise_sub_sat((__builtin_bit_cast(uint32_t, q) + r) >> 20, DOWN);
 }
-// 32 bits that depend on all of x's in no visible way; the factors are the binary digits of the
-// square roots of 2 and 3.
+// 32 bits that depend on all of x's in no visible way; the factors are the first 32 binary
+// digits behind the points of the square roots of 2 and 3.
 __host__ __device__ inline uint32_t mixed(uint32_t x) {
   x = (x ^ x >> 16) * 0x6A09E667u;
   x = (x ^ x >> 15) * 0xBB67AE85u;
